@@ -375,6 +375,288 @@ int wq_moe_step_prepare(int64_t e, int64_t dim, int64_t f, const wq_moe_layer* l
  * either. */
 int wq_moe_step_run(const wq_moe_plan* plan, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Between the linears of a verify pass -- [GUIDE] "Key Features" (the      */
+/* larger model checks the draft's tokens), [README] "推测采样".  A request */
+/* has a context in a paged cache and brings a few drafted tokens (a tree,  */
+/* a chain, or the one token of an ordinary decode step).  wqkv's product   */
+/* goes through wq_qkv_rope (norms, rotation, append), the drafted tokens   */
+/* attend through wq_tree_attention, and after the judgement wq_kv_accept   */
+/* moves the accepted tokens' rows next to the context.                     */
+/*                                                                          */
+/* Each call is a prepare, which checks every argument on the host and      */
+/* fills a plan (caller-owned host memory, passed on unchanged), and a run, */
+/* which enqueues on `stream` and may be captured into a HIP graph.  A plan */
+/* holds addresses and sizes only: the buffers' contents (lengths, tables,  */
+/* masks, ...) are read by each run on the device, so they may change       */
+/* between runs, and the buffers must stay where they are.  A plan is run   */
+/* on the device that was current when it was prepared (WQ_ERR_DEVICE       */
+/* otherwise).  Indexes that the device reads are bounds-checked there, as  */
+/* stated at each call; nothing outside the described buffers is touched.   */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A layer's keys and values in pages of `page_size` positions.  Position p of
+ * request r is row p % page_size of page table[r][p / page_size]; head h of
+ * that row starts at k (or v) + page * page_stride + row * token_stride +
+ * h * head_stride (strides in elements, any order of the axes).  A position
+ * whose table entry lies past table_width, or names a page outside
+ * [0, pages), holds nothing: it is not read, attended to or written.
+ *   k, v bf16, 16-byte aligned, strides multiples of 8, head_dim elements of
+ *   one head contiguous; table int32 [requests][table_stride].
+ * 1 <= page_size, table_width * page_size <= 2^30, 1 <= kv_heads <= 1024,
+ * head_dim a multiple of 8 up to 256 (wq_tree_attention: 64, 96, 128, 256).
+ * Two positions in use must not share a cache row.
+ */
+typedef struct {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t pages;
+  int64_t page_size;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  const int32_t* table;
+  int64_t table_width;
+  int64_t table_stride;
+  int32_t kv_heads;
+  int32_t head_dim;
+} wq_kv_cache;
+
+/*
+ * The drafted tokens of `requests` requests in the rows of one batch:
+ * request r brings rows starts[r] .. starts[r + 1] - 1 (starts int32
+ * [requests + 1], non-decreasing, within [0, tokens]; a request may bring
+ * none) on top of lengths[r] cached positions (int32, a negative one counts
+ * as 0); its row j stands at cache position lengths[r] + j.  Rows of no
+ * request are left alone.  (With starts out of order or range it is
+ * unspecified which rows of the batch are written; nothing else is touched.)
+ * 0 <= tokens <= 2^20, 0 <= requests <= 4096.
+ */
+typedef struct {
+  const int32_t* starts;
+  const int32_t* lengths;
+  int64_t tokens;
+  int64_t requests;
+} wq_batch;
+
+/*
+ * Rotary frequencies, radians per position, for rot_dim / 2 rotated pairs, in
+ * HOST memory (computed in fp64, rounded once): f_i = base^(-2i / rot_dim),
+ * then for contexts past the `original` length that a model was trained on
+ *   WQ_ROPE_PLAIN     f_i
+ *   WQ_ROPE_LINEAR    f_i / factor
+ *   WQ_ROPE_BANDS     by wavelength w = 2 pi / f_i: f_i below original / high,
+ *                     f_i / factor above original / low, and between them
+ *                     f_i * ((1 - t) / factor + t), t = (original / w - low) / (high - low)
+ *   WQ_ROPE_RAMP      by pair: f_i below pair a, f_i / factor above pair b and
+ *                     linear in i between, with a = floor(pair(high)), b =
+ *                     ceil(pair(low)), pair(n) = rot_dim ln(original / (2 pi n))
+ *                     / (2 ln base) the pair that turns n times in `original`
+ *                     positions, both limited to [0, rot_dim - 1]; *rot_scale =
+ *                     0.1 ln(factor) + 1 (for the other kinds 1)
+ * factor >= 1; 0 < low < high and original >= 1 where they are used; base > 1;
+ * rot_dim even, 2 .. 256.  rot_scale may be NULL.  Needs no device.
+ */
+enum { WQ_ROPE_PLAIN = 0, WQ_ROPE_LINEAR = 1, WQ_ROPE_BANDS = 2, WQ_ROPE_RAMP = 3 };
+int wq_rope_frequencies(int32_t kind, int32_t rot_dim, double base, double factor, double low, double high,
+                        double original, float* freq_host, float* rot_scale);
+
+/*
+ * What stands between wqkv and attention, in one pass over the product:
+ *   qkv   [tokens][qkv_stride]: a row is heads query heads, kv_heads key
+ *         heads, kv_heads value heads of head_dim; exactly one of qkv_f32
+ *         (stride a multiple of 4) and qkv_bf16 (of 8) is given
+ *   u     = x / sqrt(mean(x^2) + eps) * norm  for each query and key head
+ *         (q_norm, k_norm bf16 [head_dim], each may be NULL: u = x)
+ *   q, k  the first rot_dim elements of u turned in pairs by the angle
+ *         positions[t] * freq[i]: (a, b) -> rot_scale * (a cos - b sin,
+ *         b cos + a sin), pairs (2i, 2i + 1) if interleaved, else
+ *         (i, i + rot_dim / 2); the others as they are
+ *   q     bf16 [tokens][q_stride] out; keys and values (bf16) go to the
+ *         cache rows of the tokens
+ * positions int32 [tokens], or NULL: cache positions (drafts of a tree turn
+ * by their depth, which is not their place in the cache).  freq fp32
+ * [rot_dim / 2] on the device; angles are reduced in fp64, all else is fp32,
+ * each result rounded to nearest-even once.  rot_dim even, 0 .. head_dim (0:
+ * freq may be NULL).  heads a multiple of kv_heads, up to 1024; q and qkv
+ * 16-byte aligned, q_stride a multiple of 8; strides at least a row.
+ */
+typedef struct {
+  wq_kv_cache cache;
+  wq_batch batch;
+  const float* qkv_f32;
+  const uint16_t* qkv_bf16;
+  int64_t qkv_stride;
+  uint16_t* q;
+  int64_t q_stride;
+  const int32_t* positions;
+  const uint16_t* q_norm;
+  const uint16_t* k_norm;
+  const float* freq;
+  float eps;
+  float rot_scale;
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t heads;
+} wq_qkv_rope;
+
+typedef struct {
+  int64_t made;        /* set by prepare */
+  int32_t device;
+  int32_t split;
+  wq_qkv_rope a;
+} wq_qkv_rope_plan;
+
+int wq_qkv_rope_prepare(const wq_qkv_rope* a, wq_qkv_rope_plan* plan);
+int wq_qkv_rope_run(const wq_qkv_rope_plan* plan, void* stream);
+
+/*
+ * Attention of each request's drafted tokens over its context and its tree:
+ *   y[t][h] = sum_p w_p v[p], w = softmax over the visible p of
+ *             scale * q[t][h] . k[p], key head h / (heads / kv_heads)
+ * Every position < lengths[r] is visible; position lengths[r] + j is visible
+ * to the request's row i if bit j of tree[starts[r] + i] is set (tree uint64
+ * [tokens]: normally the token's ancestors and itself), and with tree == NULL
+ * if j <= i (a chain; one token: ordinary decode attention).  The drafts' own
+ * keys and values must be in the cache (wq_qkv_rope).  A row that sees
+ * nothing gets zeros; what a row does not see (NaN and infinities too) does
+ * not change it.
+ *   q, y  bf16 [tokens][q_stride / y_stride], rows of heads * head_dim,
+ *         16-byte aligned, strides multiples of 8; y must not overlap q
+ * A request brings at most max_tokens rows, 1 <= max_tokens <= 64; one that
+ * brings more is left alone.  heads / kv_heads <= 64.  scale finite.
+ * Scores and sums are fp32; the weights enter the second product as bf16.
+ *
+ * The positions of all requests are cut into equal shares for the launch's
+ * workgroups and partial results joined in a fixed order: results are
+ * bitwise reproducible.  `workspace` (device, 16-byte aligned,
+ * wq_tree_attention_workspace_bytes long) holds the partial results and must
+ * stay allocated and unmodified while the plan is used; prepare clears its
+ * flags synchronously (call it outside graph capture).  Runs that share a
+ * workspace must not overlap.
+ */
+typedef struct {
+  wq_kv_cache cache;
+  wq_batch batch;
+  const uint16_t* q;
+  int64_t q_stride;
+  uint16_t* y;
+  int64_t y_stride;
+  const uint64_t* tree;
+  float scale;
+  int32_t heads;
+  int32_t max_tokens;
+} wq_tree_attention;
+
+typedef struct {
+  int64_t made;        /* set by prepare */
+  int32_t device;
+  int32_t variant;
+  void* workspace;
+  wq_tree_attention a;
+} wq_tree_attention_plan;
+
+/* Workspace of a plan with these heads, head_dim and max_tokens (0 if they
+ * are not supported). */
+int64_t wq_tree_attention_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_tokens);
+int wq_tree_attention_prepare(const wq_tree_attention* a, void* workspace, int64_t workspace_bytes,
+                              wq_tree_attention_plan* plan);
+int wq_tree_attention_run(const wq_tree_attention_plan* plan, void* stream);
+
+/*
+ * After the judgement: the cache rows of each request's accepted drafts move
+ * next to its context, in every layer at once.  path int32 [requests][64 or
+ * less: path_width] (stride path_stride) lists the accepted drafts of a
+ * request by depth, accepted[r] of them (limited to [0, path_width]); the
+ * rows of draft path[r][i] (position lengths[r] + path[r][i]) are copied to
+ * position lengths[r] + i for i = 0, 1, ...  path[r] must increase and start
+ * at 0 or later: a request whose path does not is left alone, as is a row
+ * whose source or target holds nothing.  Lengths are the caller's to advance.
+ * cache describes layer 0; layer l lies l * layer_stride elements on (a
+ * multiple of 8), 1 <= layers <= 4096.
+ */
+typedef struct {
+  wq_kv_cache cache;
+  int64_t layers;
+  int64_t layer_stride;
+  int64_t requests;
+  const int32_t* lengths;
+  const int32_t* path;
+  int64_t path_width;
+  int64_t path_stride;
+  const int32_t* accepted;
+} wq_kv_accept;
+
+typedef struct {
+  int64_t made;        /* set by prepare */
+  int32_t device;
+  int32_t reserved;
+  wq_kv_accept a;
+} wq_kv_accept_plan;
+
+int wq_kv_accept_prepare(const wq_kv_accept* a, wq_kv_accept_plan* plan);
+int wq_kv_accept_run(const wq_kv_accept_plan* plan, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Low-rank adapters beside a shared projection (the quantized products     */
+/* above), a different one for each row.                                    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ *   y[t] = base[t] + scale[c] * B[c] (A[c] x[t]),   c = adapter[t]
+ *   x     bf16 [tokens][x_stride]
+ *   base  fp32 [tokens][base_stride] (a shared product's y_f32), or NULL: 0
+ *   a     bf16 [adapters][rank][k];  b  bf16 [adapters][n][rank]
+ *   adapter int32 [tokens]; outside [0, adapters): no adapter, y = base
+ *   ranks int32 [adapters] or NULL: only the first ranks[c] of the `rank`
+ *         rows of A and columns of B count (limited to [0, rank]; the rest is
+ *         not used, whatever it holds)
+ *   scale fp32 [adapters] or NULL: 1
+ *   y_f32 / y_bf16 [tokens][y_stride], either may be NULL but not both; base
+ *         may be y_f32 itself (then with the same stride)
+ * Rows of one adapter share its weights, wherever they stand in the batch.
+ * Sums are fp32, and A x is carried to the second product in three bf16
+ * parts (24 bits).  k % 8 == 0, 8 <= k <= 65536; rank % 8 == 0,
+ * 8 <= rank <= 128; 0 <= n <= 2^20; 0 <= tokens <= 4096;
+ * 1 <= adapters <= 4096; x, a, b 16-byte aligned, x_stride a multiple of 8.
+ * `workspace` as for wq_tree_attention (prepare clears its flags).
+ */
+typedef struct {
+  const uint16_t* x;
+  int64_t x_stride;
+  const float* base;
+  int64_t base_stride;
+  float* y_f32;
+  uint16_t* y_bf16;
+  int64_t y_stride;
+  const uint16_t* a;
+  const uint16_t* b;
+  const int32_t* adapter;
+  const int32_t* ranks;
+  const float* scale;
+  int64_t tokens;
+  int64_t k;
+  int64_t n;
+  int64_t adapters;
+  int32_t rank;
+} wq_lora;
+
+typedef struct {
+  int64_t made;        /* set by prepare */
+  int32_t device;
+  int32_t tiles;
+  int32_t splits;
+  int32_t reserved;
+  void* workspace;
+  wq_lora a;
+} wq_lora_plan;
+
+/* Workspace of a plan with these sizes (0 if they are not supported). */
+int64_t wq_lora_workspace_bytes(int64_t tokens, int64_t k, int64_t adapters, int32_t rank);
+int wq_lora_prepare(const wq_lora* a, void* workspace, int64_t workspace_bytes, wq_lora_plan* plan);
+int wq_lora_run(const wq_lora_plan* plan, void* stream);
+
 /* Static text for a wq_status value ("unknown status" otherwise). */
 const char* wq_status_string(int status);
 

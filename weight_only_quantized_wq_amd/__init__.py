@@ -15,6 +15,12 @@ _EXPORTS = (
     "WQ_FORMAT", "wq_matrix", "wq_step_plan",
     "wq_decode_step_workspace_bytes", "wq_decode_step_prepare", "wq_decode_step_run",
     "wq_moe_layer", "wq_moe_plan", "wq_moe_step_workspace_bytes", "wq_moe_step_prepare", "wq_moe_step_run",
+    "WQ_ROPE", "wq_rope_frequencies",
+    "wq_kv_cache", "wq_batch", "wq_qkv_rope", "wq_qkv_rope_plan", "wq_qkv_rope_prepare", "wq_qkv_rope_run",
+    "wq_tree_attention", "wq_tree_attention_plan", "wq_tree_attention_workspace_bytes", "wq_tree_attention_prepare",
+    "wq_tree_attention_run",
+    "wq_kv_accept", "wq_kv_accept_plan", "wq_kv_accept_prepare", "wq_kv_accept_run",
+    "wq_lora", "wq_lora_plan", "wq_lora_workspace_bytes", "wq_lora_prepare", "wq_lora_run",
 )
 
 __all__ = list(_EXPORTS)

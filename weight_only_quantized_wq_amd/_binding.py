@@ -61,6 +61,60 @@ class wq_moe_plan(ctypes.Structure):
                 ("grid13", ctypes.c_int32), ("grid2", ctypes.c_int32), ("workspace", ctypes.c_void_p)]
 
 
+class wq_kv_cache(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("pages", _I64), ("page_size", _I64), ("page_stride", _I64),
+                ("token_stride", _I64), ("head_stride", _I64), ("table", _P), ("table_width", _I64),
+                ("table_stride", _I64), ("kv_heads", _I32), ("head_dim", _I32)]
+
+
+class wq_batch(ctypes.Structure):
+    _fields_ = [("starts", _P), ("lengths", _P), ("tokens", _I64), ("requests", _I64)]
+
+
+class wq_qkv_rope(ctypes.Structure):
+    _fields_ = [("cache", wq_kv_cache), ("batch", wq_batch), ("qkv_f32", _P), ("qkv_bf16", _P), ("qkv_stride", _I64),
+                ("q", _P), ("q_stride", _I64), ("positions", _P), ("q_norm", _P), ("k_norm", _P), ("freq", _P),
+                ("eps", ctypes.c_float), ("rot_scale", ctypes.c_float), ("rot_dim", _I32), ("interleaved", _I32),
+                ("heads", _I32)]
+
+
+class wq_tree_attention(ctypes.Structure):
+    _fields_ = [("cache", wq_kv_cache), ("batch", wq_batch), ("q", _P), ("q_stride", _I64), ("y", _P),
+                ("y_stride", _I64), ("tree", _P), ("scale", ctypes.c_float), ("heads", _I32), ("max_tokens", _I32)]
+
+
+class wq_kv_accept(ctypes.Structure):
+    _fields_ = [("cache", wq_kv_cache), ("layers", _I64), ("layer_stride", _I64), ("requests", _I64), ("lengths", _P),
+                ("path", _P), ("path_width", _I64), ("path_stride", _I64), ("accepted", _P)]
+
+
+class wq_lora(ctypes.Structure):
+    _fields_ = [("x", _P), ("x_stride", _I64), ("base", _P), ("base_stride", _I64), ("y_f32", _P), ("y_bf16", _P),
+                ("y_stride", _I64), ("a", _P), ("b", _P), ("adapter", _P), ("ranks", _P), ("scale", _P),
+                ("tokens", _I64), ("k", _I64), ("n", _I64), ("adapters", _I64), ("rank", _I32)]
+
+
+# Plans: ctypes instances take further attributes, and `keep` holds the tensors
+# a plan's addresses point into for as long as the plan lives.
+class wq_qkv_rope_plan(ctypes.Structure):
+    _fields_ = [("made", _I64), ("device", _I32), ("split", _I32), ("a", wq_qkv_rope)]
+
+
+class wq_tree_attention_plan(ctypes.Structure):
+    _fields_ = [("made", _I64), ("device", _I32), ("variant", _I32), ("workspace", _P), ("a", wq_tree_attention)]
+
+
+class wq_kv_accept_plan(ctypes.Structure):
+    _fields_ = [("made", _I64), ("device", _I32), ("reserved", _I32), ("a", wq_kv_accept)]
+
+
+class wq_lora_plan(ctypes.Structure):
+    _fields_ = [("made", _I64), ("device", _I32), ("tiles", _I32), ("splits", _I32), ("reserved", _I32),
+                ("workspace", _P), ("a", wq_lora)]
+
+
+WQ_ROPE = {"plain": 0, "linear": 1, "bands": 2, "ramp": 3}
+
 WQ_STATUS = {0: "WQ_OK", 1: "WQ_ERR_NULL", 2: "WQ_ERR_SHAPE", 3: "WQ_ERR_ALIGN", 4: "WQ_ERR_DEVICE",
              5: "WQ_ERR_LAUNCH"}
 
@@ -97,6 +151,20 @@ def _load():
     lib.wq_moe_step_prepare.restype = ctypes.c_int
     lib.wq_moe_step_run.argtypes = [ctypes.POINTER(wq_moe_plan), _P]
     lib.wq_moe_step_run.restype = ctypes.c_int
+    lib.wq_rope_frequencies.argtypes = [_I32, _I32] + [ctypes.c_double] * 5 + [ctypes.POINTER(ctypes.c_float)] * 2
+    lib.wq_tree_attention_workspace_bytes.argtypes = [_I32] * 4
+    lib.wq_tree_attention_workspace_bytes.restype = _I64
+    lib.wq_lora_workspace_bytes.argtypes = [_I64, _I64, _I64, _I32]
+    lib.wq_lora_workspace_bytes.restype = _I64
+    # prepare and run are called with ctypes.byref of the structures above
+    lib.wq_qkv_rope_prepare.argtypes = [_P, _P]
+    lib.wq_qkv_rope_run.argtypes = [_P, _P]
+    lib.wq_tree_attention_prepare.argtypes = [_P, _P, _I64, _P]
+    lib.wq_tree_attention_run.argtypes = [_P, _P]
+    lib.wq_kv_accept_prepare.argtypes = [_P, _P]
+    lib.wq_kv_accept_run.argtypes = [_P, _P]
+    lib.wq_lora_prepare.argtypes = [_P, _P, _I64, _P]
+    lib.wq_lora_run.argtypes = [_P, _P]
     lib.wq_status_string.argtypes = [ctypes.c_int]
     lib.wq_status_string.restype = ctypes.c_char_p
     lib.wq_last_error.argtypes = []
@@ -343,3 +411,269 @@ def wq_moe_step_run(plan, stream=None):
     rc = lib.wq_moe_step_run(ctypes.byref(plan), _stream(stream))
     if rc != 0:
         raise WQError("wq_moe_step_run", rc, lib.wq_last_error().decode(errors="replace"))
+
+
+# ---------------------------------------------------------------------------
+# Between the linears of a verify pass, and the adapters beside them.  Sizes
+# and strides are read off the tensors; each *_prepare returns a plan that
+# keeps its tensors alive, each *_run enqueues it.
+
+
+def _view(t, what, dims, dtypes, device, unit=True):
+    """A GPU tensor of one of `dtypes` with `dims` axes on `device`, its last axis contiguous (`unit`)."""
+    if not hasattr(t, "data_ptr"):
+        raise ValueError(f"libwq: {what} must be a tensor")
+    names = [str(t.dtype).replace("torch.", "")]
+    if names[0] not in dtypes:
+        raise ValueError(f"libwq: {what} must be {' or '.join(dtypes)}, not {names[0]}")
+    if t.dim() != dims:
+        raise ValueError(f"libwq: {what} must have {dims} axes, not {t.dim()}")
+    if unit and dims and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"libwq: the last axis of {what} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError("libwq buffers must be GPU tensors (device memory)")
+    if device is not None and t.device != device:
+        raise ValueError(f"libwq: {what} is on {t.device}, the plan's other buffers on {device}")
+    return t
+
+
+_BF16 = ("bfloat16", "int16", "uint16")      # bf16 values, or their bit patterns
+
+
+def _at(t):
+    """Address of a tensor; an empty one has none, and its call touches nothing."""
+    return t.data_ptr() if t.numel() else 16
+
+
+def _heads_view(t, what, heads, device):
+    """[tokens, heads, dim] or [tokens, heads * dim] as (tensor, tokens, row stride, dim)."""
+    if hasattr(t, "dim") and t.dim() == 3:
+        _view(t, what, 3, _BF16, device)
+        if t.shape[1] > 1 and t.stride(1) != t.shape[2]:
+            raise ValueError(f"libwq: the heads of a row of {what} must be contiguous")
+        if heads is not None and t.shape[1] != heads:
+            raise ValueError(f"libwq: {what} has {t.shape[1]} heads, not {heads}")
+        width = t.shape[1] * t.shape[2]
+    else:
+        _view(t, what, 2, _BF16, device)
+        width = t.shape[1]
+    return t.shape[0], _row_stride(t, width)
+
+
+def _row_stride(t, width):
+    """Stride of the first axis; of a single row, any that holds it."""
+    return t.stride(0) if t.shape[0] > 1 else max(width, 8 * (-(-width // 8)))
+
+
+def _cache_struct(k, v, table, requests, device, layers=False):
+    dims = 5 if layers else 4
+    _view(k, "k", dims, _BF16, device)
+    _view(v, "v", dims, _BF16, device)
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("libwq: k and v must have the same shape and strides")
+    _view(table, "table", 2, ("int32",), device)
+    if table.shape[0] < requests:
+        raise ValueError(f"libwq: table holds {table.shape[0]} requests; {requests} are needed")
+    if any(s == 0 and n > 1 for n, s in zip(k.shape, k.stride())):
+        raise ValueError("libwq: k and v must not be expanded tensors")
+    pages, page_size, kv_heads, head_dim = k.shape[-4:]
+    # the stride of an axis of length one is never used
+    strides = [s if n > 1 else 0 for n, s in zip(k.shape[-4:-1], k.stride()[-4:-1])]
+    return wq_kv_cache(_at(k), _at(v), pages, page_size, *strides, _at(table), table.shape[1],
+                       table.stride(0) if table.shape[0] > 1 else table.shape[1], kv_heads, head_dim)
+
+
+def _batch_struct(starts, lengths, tokens, device):
+    _view(starts, "starts", 1, ("int32",), device)
+    _view(lengths, "lengths", 1, ("int32",), device)
+    if starts.shape[0] != lengths.shape[0] + 1:
+        raise ValueError(f"libwq: starts holds {starts.shape[0]} values; {lengths.shape[0] + 1} are needed")
+    return wq_batch(_at(starts), _at(lengths), tokens, lengths.shape[0])
+
+
+def _vector(t, what, length, dtypes, device):
+    """Address of an optional vector of at least `length` elements."""
+    if t is None:
+        return None
+    _view(t, what, 1, dtypes, device)
+    if t.shape[0] < length:
+        raise ValueError(f"libwq: {what} holds {t.shape[0]} values; {length} are needed")
+    return _at(t)
+
+
+def _workspace(workspace, nbytes, device):
+    if workspace is None:
+        import torch
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    _view(workspace, "workspace", 1, ("uint8",), device)
+    return workspace, workspace.numel()
+
+
+def _prepare(name, plan, device, keep, *args):
+    import torch
+    with torch.cuda.device(device):
+        rc = getattr(lib, name)(*args, ctypes.byref(plan))
+    if rc != 0:
+        raise WQError(name, rc, lib.wq_last_error().decode(errors="replace"))
+    plan.keep = keep
+    plan.at = ctypes.addressof(plan)
+    return plan
+
+
+def _run(name, fn, plan, stream):
+    rc = fn(plan.at, _stream(stream))
+    if rc != 0:
+        raise WQError(name, rc, lib.wq_last_error().decode(errors="replace"))
+
+
+def wq_rope_frequencies(rot_dim, base, kind="plain", factor=1.0, low=1.0, high=4.0, original=8192.0):
+    """Rotary frequencies as a CPU tensor fp32 [rot_dim / 2], and the rot_scale that goes with them.  kind:
+    "plain", "linear", "bands" or "ramp" (a WQ_ROPE name or code)."""
+    import torch
+    freq = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float32)
+    scale = ctypes.c_float()
+    rc = lib.wq_rope_frequencies(WQ_ROPE.get(kind, kind), rot_dim, base, factor, low, high, original,
+                                 ctypes.cast(freq.data_ptr() or None, ctypes.POINTER(ctypes.c_float)),
+                                 ctypes.byref(scale))
+    if rc != 0:
+        raise WQError("wq_rope_frequencies", rc, lib.wq_last_error().decode(errors="replace"))
+    return freq, scale.value
+
+
+def wq_qkv_rope_prepare(qkv, q, k, v, table, starts, lengths, freq=None, positions=None, q_norm=None, k_norm=None,
+                        eps=1e-6, rot_scale=1.0, interleaved=False):
+    """qkv [tokens, (heads + 2 kv_heads) * dim] fp32 or bf16; q out, bf16 [tokens, heads, dim]; k, v the layer's
+    cache [pages, page_size, kv_heads, dim]; table int32 [requests, pages per request]; freq fp32 [rot_dim / 2]."""
+    _view(qkv, "qkv", 2, ("float32",) + _BF16, None)
+    device = qkv.device
+    requests = lengths.shape[0] if hasattr(lengths, "shape") and lengths.dim() == 1 else 0
+    cache = _cache_struct(k, v, table, requests, device)
+    dim = cache.head_dim
+    tokens, q_stride = _heads_view(q, "q", None, device)
+    heads = (q.shape[1] * q.shape[2] if q.dim() == 3 else q.shape[1]) // dim
+    if qkv.shape[0] != tokens or qkv.shape[1] != (heads + 2 * cache.kv_heads) * dim or \
+            q.numel() != tokens * heads * dim:
+        raise ValueError(f"libwq: qkv {tuple(qkv.shape)} does not go with q {tuple(q.shape)} and "
+                         f"{cache.kv_heads} key heads of {dim}")
+    rot_dim = 0
+    if freq is not None:
+        _view(freq, "freq", 1, ("float32",), device)
+        rot_dim = 2 * freq.shape[0]
+    f32 = str(qkv.dtype) == "torch.float32"
+    a = wq_qkv_rope(cache, _batch_struct(starts, lengths, tokens, device), _at(qkv) if f32 else None,
+                    None if f32 else _at(qkv), _row_stride(qkv, qkv.shape[1]), _at(q), q_stride,
+                    _vector(positions, "positions", tokens, ("int32",), device),
+                    _vector(q_norm, "q_norm", dim, _BF16, device), _vector(k_norm, "k_norm", dim, _BF16, device),
+                    _at(freq) if rot_dim else None, eps, rot_scale, rot_dim, 1 if interleaved else 0, heads)
+    return _prepare("wq_qkv_rope_prepare", wq_qkv_rope_plan(), device,
+                    (qkv, q, k, v, table, starts, lengths, freq, positions, q_norm, k_norm), ctypes.byref(a))
+
+
+def wq_qkv_rope_run(plan, stream=None):
+    _run("wq_qkv_rope_run", lib.wq_qkv_rope_run, plan, stream)
+
+
+def wq_tree_attention_workspace_bytes(heads, kv_heads, head_dim, max_tokens):
+    return int(lib.wq_tree_attention_workspace_bytes(heads, kv_heads, head_dim, max_tokens))
+
+
+def wq_tree_attention_prepare(q, k, v, table, starts, lengths, y, tree=None, max_tokens=64, scale=None,
+                              workspace=None):
+    """q, y bf16 [tokens, heads, dim]; k, v, table as for wq_qkv_rope_prepare; tree int64 (or uint64) [tokens]; scale
+    None: dim ** -0.5; workspace None: allocated here."""
+    device = getattr(q, "device", None)
+    tokens, q_stride = _heads_view(q, "q", None, None)
+    requests = lengths.shape[0] if hasattr(lengths, "shape") and lengths.dim() == 1 else 0
+    cache = _cache_struct(k, v, table, requests, device)
+    dim = cache.head_dim
+    width = q.numel() // tokens if tokens else (q.shape[1] * q.shape[2] if q.dim() == 3 else q.shape[1])
+    heads = width // dim
+    _, y_stride = _heads_view(y, "y", None, device)
+    if heads * dim != width or y.shape[0] != tokens or y.numel() != q.numel():
+        raise ValueError(f"libwq: q {tuple(q.shape)} and y {tuple(y.shape)} do not hold heads of {dim}")
+    a = wq_tree_attention(cache, _batch_struct(starts, lengths, tokens, device), _at(q), q_stride, _at(y),
+                          y_stride, _vector(tree, "tree", tokens, ("int64", "uint64"), device),
+                          dim ** -0.5 if scale is None else scale, heads, max_tokens)
+    workspace, nbytes = _workspace(
+        workspace, wq_tree_attention_workspace_bytes(heads, cache.kv_heads, dim, max_tokens), device)
+    return _prepare("wq_tree_attention_prepare", wq_tree_attention_plan(), device,
+                    (q, k, v, table, starts, lengths, y, tree, workspace), ctypes.byref(a), _at(workspace),
+                    nbytes)
+
+
+def wq_tree_attention_run(plan, stream=None):
+    _run("wq_tree_attention_run", lib.wq_tree_attention_run, plan, stream)
+
+
+def wq_kv_accept_prepare(k, v, table, lengths, path, accepted):
+    """k, v [layers, pages, page_size, kv_heads, dim] (or one layer without the first axis); path int32 [requests, up
+    to 64]; accepted int32 [requests]."""
+    if hasattr(k, "dim") and k.dim() == 4:
+        return wq_kv_accept_prepare(k.unsqueeze(0), v.unsqueeze(0) if hasattr(v, "dim") else v, table, lengths, path,
+                                    accepted)
+    device = getattr(k, "device", None)
+    _view(lengths, "lengths", 1, ("int32",), device)
+    requests = lengths.shape[0]
+    cache = _cache_struct(k, v, table, requests, device, layers=True)
+    _view(path, "path", 2, ("int32",), device)
+    if path.shape[0] < requests:
+        raise ValueError(f"libwq: path holds {path.shape[0]} requests; {requests} are needed")
+    a = wq_kv_accept(cache, k.shape[0], k.stride(0) if k.shape[0] > 1 else 0, requests, _at(lengths),
+                     _at(path), path.shape[1], path.stride(0) if path.shape[0] > 1 else path.shape[1],
+                     _vector(accepted, "accepted", requests, ("int32",), device))
+    return _prepare("wq_kv_accept_prepare", wq_kv_accept_plan(), device, (k, v, table, lengths, path, accepted),
+                    ctypes.byref(a))
+
+
+def wq_kv_accept_run(plan, stream=None):
+    _run("wq_kv_accept_run", lib.wq_kv_accept_run, plan, stream)
+
+
+def wq_lora_workspace_bytes(tokens, k, adapters, rank):
+    return int(lib.wq_lora_workspace_bytes(tokens, k, adapters, rank))
+
+
+def wq_lora_prepare(x, a, b, adapter, y, y2=None, base=None, ranks=None, scale=None, workspace=None):
+    """x bf16 [tokens, k]; a bf16 [adapters, rank, k]; b bf16 [adapters, n, rank]; adapter int32 [tokens]; y fp32 or
+    bf16 [tokens, n], y2 the other of the two (same row stride) or None; base fp32 [tokens, n] or None."""
+    _view(x, "x", 2, _BF16, None)
+    device, (tokens, k) = x.device, x.shape
+    _view(a, "a", 3, _BF16, device)
+    _view(b, "b", 3, _BF16, device)
+    if not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("libwq: a and b must be contiguous")
+    adapters, rank, n = a.shape[0], a.shape[1], b.shape[1]
+    if a.shape[2] != k or b.shape[0] != adapters or b.shape[2] != rank:
+        raise ValueError(f"libwq: a {tuple(a.shape)} and b {tuple(b.shape)} do not go with x {tuple(x.shape)}")
+    out = {"f32": None, "bf16": None}
+    for t, what in ((y, "y"), (y2, "y2")):
+        if t is None:
+            continue
+        _view(t, what, 2, ("float32",) + _BF16, device)
+        if tuple(t.shape) != (tokens, n):
+            raise ValueError(f"libwq: {what} must be {(tokens, n)}, not {tuple(t.shape)}")
+        kind = "f32" if str(t.dtype) == "torch.float32" else "bf16"
+        if out[kind] is not None:
+            raise ValueError("libwq: y and y2 must be one fp32 and one bf16")
+        out[kind] = t
+    strides = {_row_stride(t, n) for t in out.values() if t is not None}
+    if len(strides) > 1:
+        raise ValueError("libwq: y and y2 must have the same row stride")
+    if base is not None:
+        _view(base, "base", 2, ("float32",), device)
+        if tuple(base.shape) != (tokens, n):
+            raise ValueError(f"libwq: base must be {(tokens, n)}, not {tuple(base.shape)}")
+    desc = wq_lora(_at(x), _row_stride(x, k), None if base is None else _at(base),
+                   0 if base is None else _row_stride(base, n), *(None if t is None else _at(t) for t in out.values()),
+                   max(strides, default=0), _at(a), _at(b),
+                   _vector(adapter, "adapter", tokens, ("int32",), device),
+                   _vector(ranks, "ranks", adapters, ("int32",), device),
+                   _vector(scale, "scale", adapters, ("float32",), device), tokens, k, n, adapters, rank)
+    workspace, nbytes = _workspace(workspace, wq_lora_workspace_bytes(tokens, k, adapters, rank), device)
+    return _prepare("wq_lora_prepare", wq_lora_plan(), device,
+                    (x, a, b, adapter, y, y2, base, ranks, scale, workspace), ctypes.byref(desc), _at(workspace),
+                    nbytes)
+
+
+def wq_lora_run(plan, stream=None):
+    _run("wq_lora_run", lib.wq_lora_run, plan, stream)

@@ -1,0 +1,78 @@
+// Paged key/value cache and batch descriptions on the device, and their
+// host-side checks (wq_kv_cache, wq_batch).
+#pragma once
+
+#include <stdint.h>
+
+#include "wq_device.hpp"
+#include "wq_host.hpp"
+
+namespace wq {
+
+struct KvCache {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  const int32_t* table;
+  int64_t table_stride;
+  uint64_t magic;      // page of a position: position * magic >> shift
+  int32_t shift;
+  uint32_t pages;
+  uint32_t page_size;
+  uint32_t limit;      // positions the table covers
+  int32_t kv_heads;
+  int32_t head_dim;
+};
+
+struct Batch {
+  const int32_t* starts;
+  const int32_t* lengths;
+  int32_t tokens;
+  int32_t requests;
+};
+
+// Page index of a position below 2^31.  magic = floor(2^shift / page_size) + 1
+// with shift = 31 + ceil(log2(page_size)): the quotient exceeds the true one
+// by less than position / 2^shift * page_size / page_size < 1 / page_size, so
+// its integer part is exact.
+__device__ __forceinline__ uint32_t page_of(const KvCache& c, uint32_t p) {
+  return (uint32_t)(((uint64_t)p * c.magic) >> c.shift);
+}
+
+// Element offset of position p's row in page `pid` (head 0).
+__device__ __forceinline__ int64_t row_offset(const KvCache& c, uint32_t pid, uint32_t row) {
+  return (int64_t)pid * c.page_stride + (int64_t)row * c.token_stride;
+}
+
+// Element offset of request r's position p (head 0), or -1 if it holds nothing.
+__device__ __forceinline__ int64_t position_offset(const KvCache& c, int r, int64_t p) {
+  if (p < 0 || p >= (int64_t)c.limit) return -1;
+  const uint32_t pg = page_of(c, (uint32_t)p);
+  const uint32_t pid = (uint32_t)gmem(c.table)[(int64_t)r * c.table_stride + pg];
+  if (pid >= c.pages) return -1;
+  return row_offset(c, pid, (uint32_t)p - pg * c.page_size);
+}
+
+// Host: checks (sizes, then alignment) and the device view.
+int check_cache_null(const char* name, const wq_kv_cache& c);
+int check_cache_sizes(const char* name, const wq_kv_cache& c);
+int check_cache_align(const char* name, const wq_kv_cache& c);
+int check_batch_sizes(const char* name, const wq_batch& b);
+KvCache device_cache(const wq_kv_cache& c);
+
+inline Batch device_batch(const wq_batch& b) {
+  return Batch{b.starts, b.lengths, (int32_t)b.tokens, (int32_t)b.requests};
+}
+
+// The device a plan is bound to: recorded by prepare, compared by run.
+int plan_device(const char* name, int32_t* device);
+int same_device(const char* name, int32_t device);
+
+constexpr int64_t kMaxBatchTokens = 1 << 20;
+constexpr int64_t kMaxRequests = 4096;
+constexpr int64_t kMaxPositions = 1 << 30;      // of one request: positions and tiles stay in 32 bits
+constexpr int32_t kMaxHeads = 1024;
+
+}  // namespace wq

@@ -1,0 +1,426 @@
+// Low-rank adapters of many requests beside a shared projection:
+//   y[t] = base[t] + scale[c] * B[c] (A[c] x[t]),  c = adapter[t].
+//
+// Rows of one adapter are put together on the device, wherever they stand in
+// the batch: a tile is up to 16 rows of one adapter (ranked by row index), and
+// every workgroup finds its own tile from a histogram of adapter[], so no
+// host pass and no extra launch are needed.  Two launches:
+//   1. lora_shrink_kernel: h = A x of a tile over a share of k, as matrix
+//      products (16 adapter rows x 16 token rows, v_mfma_f32_16x16x32_bf16);
+//      the waves' sums meet in LDS, the shares' in the second launch.
+//   2. lora_expand_kernel: adds the shares in order, scales, splits h into
+//      three bf16 parts (together all 24 bits, so that only fp32 sums round)
+//      and multiplies 16 rows of B at a time with them; base is added and the
+//      result stored from the accumulators.
+// Weights are read once per tile; with few rows per adapter both launches are
+// bound by them, and with one row by launch latency.
+#include <math.h>
+
+#include "wq_kv.hpp"
+
+namespace wq {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kLoraThreads = 256;
+constexpr int kLoraWaves = 4;
+constexpr int kLoraRows = 16;              // rows of a tile
+constexpr int kLoraStep = 128;             // inputs a wave takes at a time
+constexpr int64_t kLoraMaxTokens = 4096;
+constexpr int64_t kLoraMaxAdapters = 4096;
+
+struct LoraArgs {
+  const uint16_t* x;
+  int64_t x_stride;
+  const float* base;
+  int64_t base_stride;
+  float* y32;
+  uint16_t* y16;
+  int64_t y_stride;
+  const uint16_t* a;
+  const uint16_t* b;
+  const int32_t* adapter;
+  const int32_t* ranks;
+  const float* scale;
+  float* part;          // [splits][tiles][16][rank16]
+  int32_t tokens;
+  int32_t k;
+  int32_t n;
+  int32_t adapters;
+  int32_t rank;
+  int32_t tiles;        // most tiles the batch can have
+  int32_t splits;
+  int32_t chunk;        // inputs per split (shrink), B rows per workgroup (expand)
+  int32_t vec;          // base and y rows take 16-byte (8-byte bf16) accesses
+};
+
+struct Tile {
+  int adapter;          // == adapters: rows without one
+  int rows;             // 0: no such tile
+};
+
+// LDS of the search: counts [adapters + 1], ids [tokens] as 16 bits.
+__device__ __host__ inline size_t search_bytes(int64_t tokens, int64_t adapters) {
+  return (size_t)((adapters + 1) * 4 + tokens * 2 + 15) / 16 * 16;
+}
+
+// Tile `want` of the batch: tiles are ordered by adapter (rows without one
+// last), then by row.  Every thread takes part; row[] (LDS) gets its rows.
+__device__ Tile find_tile(const LoraArgs& a, int want, char* lds, int (&row)[kLoraRows]) {
+  __shared__ int wave_tot[kLoraThreads / kWave];
+  __shared__ int hit[3];
+  int* count = reinterpret_cast<int*>(lds);
+  uint16_t* id = reinterpret_cast<uint16_t*>(count + a.adapters + 1);
+  const int lane = lane_id(), wave = wave_id(), me = (int)threadIdx.x;
+  for (int i = me; i <= a.adapters; i += kLoraThreads) count[i] = 0;
+  if (me == 0) hit[0] = -1;
+  __syncthreads();
+  for (int t = me; t < a.tokens; t += kLoraThreads) {
+    const int c = gmem(a.adapter)[t];
+    const int i = (uint32_t)c < (uint32_t)a.adapters ? c : a.adapters;
+    id[t] = (uint16_t)i;
+    atomicAdd(&count[i], 1);
+  }
+  __syncthreads();
+  const auto scan = [&](int v) {          // exclusive, over the workgroup
+    int run = v;
+    for (int s = 1; s < kWave; s <<= 1) {
+      const int up = __shfl_up(run, s);
+      if (lane >= s) run += up;
+    }
+    if (lane == kWave - 1) wave_tot[wave] = run;
+    __syncthreads();
+    int before = run - v;
+    for (int w = 0; w < wave; ++w) before += wave_tot[w];
+    __syncthreads();
+    return before;
+  };
+  const int each = (a.adapters + kLoraThreads) / kLoraThreads;
+  int mine = 0;
+  for (int i = me * each; i < min((me + 1) * each, a.adapters + 1); ++i) mine += (count[i] + kLoraRows - 1) / kLoraRows;
+  int before = scan(mine);
+  if (want >= before && want < before + mine) {
+    for (int i = me * each; i < min((me + 1) * each, a.adapters + 1); ++i) {
+      const int tiles = (count[i] + kLoraRows - 1) / kLoraRows;
+      if (want < before + tiles) {
+        hit[0] = i;
+        hit[1] = (want - before) * kLoraRows;
+        hit[2] = count[i];
+        break;
+      }
+      before += tiles;
+    }
+  }
+  __syncthreads();
+  if (hit[0] < 0) return Tile{0, 0};
+  const int adapter = hit[0], skip = hit[1], rows = min(kLoraRows, hit[2] - skip);
+  const int per = (a.tokens + kLoraThreads - 1) / kLoraThreads;
+  int own = 0;
+  for (int t = me * per; t < min((me + 1) * per, a.tokens); ++t) own += id[t] == adapter;
+  int at = scan(own) - skip;
+  for (int t = me * per; t < min((me + 1) * per, a.tokens); ++t)
+    if (id[t] == adapter) {
+      if (at >= 0 && at < kLoraRows) row[at] = t;
+      ++at;
+    }
+  __syncthreads();
+  return Tile{adapter, rows};
+}
+
+__device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
+  return a.ranks ? min(max(gmem(a.ranks)[adapter], 0), a.rank) : a.rank;
+}
+
+template <int RT>
+__global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  __shared__ int row[kLoraRows];
+  __shared__ float sum[kLoraWaves][RT * 16][kLoraRows];
+  const Tile tile = find_tile(a, (int)blockIdx.x, lds, row);
+  if (tile.rows == 0 || tile.adapter == a.adapters) return;
+  const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
+  const int rank = rank_of(a, tile.adapter);
+  const int k0 = (int)blockIdx.y * a.chunk, k1 = min(k0 + a.chunk, a.k);
+  const bool has = c < tile.rows;
+  const uint16_t* xp = a.x + (int64_t)row[has ? c : 0] * a.x_stride;
+  const uint16_t* ap = a.a + (int64_t)tile.adapter * a.rank * a.k;
+  f32x4 acc[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // lane group g takes 32 inputs of a step of 128, as four pieces of 8
+  for (int kb = k0 + wave * kLoraStep; kb < k1; kb += kLoraWaves * kLoraStep) {
+    u32x4 xv[4], av[RT][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int kk = kb + g * 32 + s * 8;
+      const bool in = kk < k1;
+      xv[s] = has && in ? load16(xp + kk) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        av[r][s] = in && 16 * r + c < rank ? load_stream16(ap + (int64_t)(16 * r + c) * a.k + kk) : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[r][s]),
+                                                         __builtin_bit_cast(bf16x8, xv[s]), acc[r], 0, 0, 0);
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[wave][16 * r + 4 * g + i][c] = acc[r][i];
+  __syncthreads();
+  float* out = a.part + ((int64_t)blockIdx.y * a.tiles + blockIdx.x) * (kLoraRows * RT * 16);
+  for (int i = (int)threadIdx.x; i < kLoraRows * RT * 16; i += kLoraThreads) {
+    const int t = i / (RT * 16), j = i % (RT * 16);
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLoraWaves; ++w) v += sum[w][j][t];
+    gmem(out)[i] = v;
+  }
+}
+
+// x = hi + mid + lo to 24 bits, each part a bf16.
+__device__ __forceinline__ void split3(float x, __bf16& hi, __bf16& mid, __bf16& lo) {
+  hi = (__bf16)x;
+  const float r = x - (float)hi;
+  mid = (__bf16)r;
+  lo = (__bf16)(r - (float)mid);
+}
+
+template <int RT>
+__global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
+  constexpr int KS = (RT + 1) / 2;          // products of 32 ranks
+  extern __shared__ __align__(16) char lds[];
+  __shared__ int row[kLoraRows];
+  __shared__ float h[kLoraRows][KS * 32 + 4];
+  const Tile tile = find_tile(a, (int)blockIdx.x, lds, row);
+  if (tile.rows == 0) return;
+  const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
+  const bool bare = tile.adapter == a.adapters;
+  const int rank = bare ? 0 : rank_of(a, tile.adapter);
+  const float scale = bare || !a.scale ? 1.f : gmem(a.scale)[tile.adapter];
+  for (int i = (int)threadIdx.x; i < kLoraRows * KS * 32; i += kLoraThreads) {
+    const int t = i / (KS * 32), j = i % (KS * 32);
+    float v = 0.f;
+    if (j < rank && t < tile.rows)
+      for (int s = 0; s < a.splits; ++s)
+        v += gmem(a.part)[((int64_t)s * a.tiles + blockIdx.x) * (kLoraRows * RT * 16) + t * (RT * 16) + j];
+    h[t][j] = v * scale;
+  }
+  __syncthreads();
+  bf16x8 hv[KS][3];
+#pragma unroll
+  for (int s = 0; s < KS; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      __bf16 p, q, r;
+      split3(h[c][s * 32 + g * 8 + e], p, q, r);
+      hv[s][0][e] = p, hv[s][1][e] = q, hv[s][2][e] = r;
+    }
+  const uint16_t* bp = a.b + (int64_t)(bare ? 0 : tile.adapter) * a.n * a.rank;
+  const bool has = c < tile.rows;
+  const int t = row[has ? c : 0];
+  const float* base = a.base ? a.base + (int64_t)t * a.base_stride : nullptr;
+  const int n0 = (int)blockIdx.y * a.chunk, n1 = min(n0 + a.chunk, a.n);
+  for (int nb = n0 + wave * 16; nb < n1; nb += kLoraWaves * 16) {
+    u32x4 bv[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      bv[s] = nb + c < n1 && s * 32 + g * 8 < rank ? load_stream16(bp + (int64_t)(nb + c) * a.rank + s * 32 + g * 8)
+                                                   : u32x4{0, 0, 0, 0};
+    if (rank & 7) {
+      // columns of B past a rank that ends inside a piece of 8 do not count
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int left = rank - (s * 32 + g * 8 + 2 * i);
+          bv[s][i] = left <= 0 ? 0u : left == 1 ? bv[s][i] & 0xFFFFu : bv[s][i];
+        }
+    }
+    const int j = nb + 4 * g;             // the lane's outputs: j .. j + 3 of row t
+    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+    const bool full = a.vec && j + 4 <= n1;
+    if (has && base) {
+      if (full) {
+        v = __builtin_bit_cast(f32x4, load16(base + j));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < n1) v[i] = gmem(base)[j + i];
+      }
+    }
+    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bv[s]), hv[s][q], acc, 0, 0, 0);
+    if (!has) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += acc[i];
+    if (a.y32) {
+      float* y = a.y32 + (int64_t)t * a.y_stride + j;
+      if (full) {
+        *gmem(reinterpret_cast<u32x4*>(y)) = __builtin_bit_cast(u32x4, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < n1) gmem(y)[i] = v[i];
+      }
+    }
+    if (a.y16) {
+      uint16_t* y = a.y16 + (int64_t)t * a.y_stride + j;
+      if (full) {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        *gmem(reinterpret_cast<u32x2*>(y)) = u32x2{(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                                                   (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < n1) gmem(y)[i] = f32_to_bf16(v[i]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+
+constexpr int64_t kLoraMade = 0x77715f6c6f726131;
+
+static bool lora_sizes_ok(int64_t tokens, int64_t k, int64_t adapters, int32_t rank) {
+  return tokens >= 0 && tokens <= kLoraMaxTokens && k >= 8 && k <= 65536 && k % 8 == 0 && adapters >= 1 &&
+         adapters <= kLoraMaxAdapters && rank >= 8 && rank <= 128 && rank % 8 == 0;
+}
+
+static int lora_tiles(int64_t tokens, int64_t adapters) {
+  // at most one unfilled tile per adapter in use and one for rows without
+  const int64_t partly = adapters + 1 < tokens ? adapters + 1 : tokens;
+  const int64_t most = partly + (tokens - partly) / kLoraRows;
+  return (int)(most < 1 ? 1 : most);
+}
+
+// Shares of k: enough workgroups for the chip, each wave at least one step.
+static int lora_splits(int tiles, int64_t k) {
+  const int64_t most = (k + kLoraWaves * kLoraStep - 1) / (kLoraWaves * kLoraStep);
+  const int64_t want = (512 + tiles - 1) / tiles;
+  return (int)(want < most ? want : most);
+}
+
+static int rank16(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+static int lora_check(const char* name, const wq_lora& a) {
+  if (!a.x || !a.a || !a.b || !a.adapter) return fail(WQ_ERR_NULL, "%s: x, a, b and adapter must be non-null", name);
+  if (!a.y_f32 && !a.y_bf16) return fail(WQ_ERR_NULL, "%s: at least one of y_f32 / y_bf16 must be non-null", name);
+  if (!lora_sizes_ok(a.tokens, a.k, a.adapters, a.rank) || a.n < 0 || a.n > (1 << 20))
+    return fail(WQ_ERR_SHAPE,
+                "%s: tokens = %lld (0..4096), k = %lld (a multiple of 8 up to 65536), n = %lld (0..2^20), adapters = "
+                "%lld (1..4096), rank = %d (a multiple of 8 up to 128)",
+                name, (long long)a.tokens, (long long)a.k, (long long)a.n, (long long)a.adapters, a.rank);
+  const int64_t most = (int64_t)1 << 40;
+  if (a.x_stride < a.k || a.x_stride > most || a.x_stride % 8)
+    return fail(WQ_ERR_SHAPE, "%s: x_stride = %lld must be a multiple of 8 and hold a row", name, (long long)a.x_stride);
+  if (a.y_stride < a.n || a.y_stride > most || (a.base && (a.base_stride < a.n || a.base_stride > most)))
+    return fail(WQ_ERR_SHAPE, "%s: y_stride = %lld, base_stride = %lld must hold a row", name, (long long)a.y_stride,
+                (long long)a.base_stride);
+  if (a.base && a.base == a.y_f32 && a.base_stride != a.y_stride)
+    return fail(WQ_ERR_SHAPE, "%s: base is y_f32 but has another stride", name);
+  if (!aligned16(a.x) || !aligned16(a.a) || !aligned16(a.b))
+    return fail(WQ_ERR_ALIGN, "%s: x, a and b must be 16-byte aligned", name);
+  if (((uintptr_t)a.base & 3) || ((uintptr_t)a.y_f32 & 3) || ((uintptr_t)a.y_bf16 & 1) || ((uintptr_t)a.adapter & 3) ||
+      ((uintptr_t)a.ranks & 3) || ((uintptr_t)a.scale & 3))
+    return fail(WQ_ERR_ALIGN, "%s: base, y, adapter, ranks and scale must be aligned to their elements", name);
+  return WQ_OK;
+}
+
+template <int RT>
+static int lora_launch(const char* name, LoraArgs a, hipStream_t s) {
+  const size_t lds = search_bytes(a.tokens, a.adapters);
+  const int steps = (a.k + kLoraStep - 1) / kLoraStep;
+  const int rows = (a.n + 15) / 16;
+  a.chunk = (steps + a.splits - 1) / a.splits * kLoraStep;
+  hipLaunchKernelGGL((lora_shrink_kernel<RT>), dim3((unsigned)a.tiles, (unsigned)a.splits), dim3(kLoraThreads), lds, s, a);
+  // expand: workgroups of at least one row block per wave, about 1024 in all
+  int64_t parts = (1024 + a.tiles - 1) / a.tiles;
+  const int64_t most = (rows + kLoraWaves - 1) / kLoraWaves;
+  parts = parts < most ? parts : most;
+  a.chunk = (int)((rows + parts - 1) / parts) * 16;
+  parts = (a.n + a.chunk - 1) / a.chunk;
+  hipLaunchKernelGGL((lora_expand_kernel<RT>), dim3((unsigned)a.tiles, (unsigned)parts), dim3(kLoraThreads), lds, s, a);
+  return launch_status(name);
+}
+
+}  // namespace wq
+
+using namespace wq;
+
+extern "C" int64_t wq_lora_workspace_bytes(int64_t tokens, int64_t k, int64_t adapters, int32_t rank) {
+  if (!lora_sizes_ok(tokens, k, adapters, rank)) return 0;
+  const int tiles = lora_tiles(tokens, adapters);
+  return (int64_t)lora_splits(tiles, k) * tiles * kLoraRows * rank16(rank) * 4;
+}
+
+extern "C" int wq_lora_prepare(const wq_lora* a, void* workspace, int64_t workspace_bytes, wq_lora_plan* plan) {
+  const char* name = "wq_lora_prepare";
+  if (!a || !plan || !workspace) return fail(WQ_ERR_NULL, "%s: a, workspace and plan must be non-null", name);
+  int rc = lora_check(name, *a);
+  if (rc) return rc;
+  const int64_t need = wq_lora_workspace_bytes(a->tokens, a->k, a->adapters, a->rank);
+  if (workspace_bytes < need)
+    return fail(WQ_ERR_SHAPE, "%s: workspace_bytes = %lld, %lld are needed", name, (long long)workspace_bytes,
+                (long long)need);
+  if (!aligned16(workspace)) return fail(WQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", name);
+  wq_lora_plan p{};
+  if ((rc = plan_device(name, &p.device))) return rc;
+  p.made = kLoraMade;
+  p.tiles = lora_tiles(a->tokens, a->adapters);
+  p.splits = lora_splits(p.tiles, a->k);
+  p.workspace = workspace;
+  p.a = *a;
+  *plan = p;
+  return WQ_OK;
+}
+
+extern "C" int wq_lora_run(const wq_lora_plan* plan, void* stream) {
+  const char* name = "wq_lora_run";
+  if (!plan) return fail(WQ_ERR_NULL, "%s: plan must be non-null", name);
+  if (plan->made != kLoraMade) return fail(WQ_ERR_SHAPE, "%s: the plan was not made by wq_lora_prepare", name);
+  int rc = same_device(name, plan->device);
+  if (rc) return rc;
+  const wq_lora& l = plan->a;
+  if (l.tokens == 0 || l.n == 0) return WQ_OK;
+  LoraArgs a{};
+  a.x = l.x;
+  a.x_stride = l.x_stride;
+  a.base = l.base;
+  a.base_stride = l.base_stride;
+  a.y32 = l.y_f32;
+  a.y16 = l.y_bf16;
+  a.y_stride = l.y_stride;
+  a.a = l.a;
+  a.b = l.b;
+  a.adapter = l.adapter;
+  a.ranks = l.ranks;
+  a.scale = l.scale;
+  a.part = static_cast<float*>(plan->workspace);
+  a.tokens = (int32_t)l.tokens;
+  a.k = (int32_t)l.k;
+  a.n = (int32_t)l.n;
+  a.adapters = (int32_t)l.adapters;
+  a.rank = l.rank;
+  a.tiles = plan->tiles;
+  a.splits = plan->splits;
+  a.vec = l.y_stride % 4 == 0 && (!l.y_f32 || aligned16(l.y_f32)) && (!l.y_bf16 || !((uintptr_t)l.y_bf16 & 7)) &&
+          (!l.base || (l.base_stride % 4 == 0 && aligned16(l.base)));
+  hipStream_t s = (hipStream_t)stream;
+  switch (rank16(l.rank)) {
+    case 16: return lora_launch<1>(name, a, s);
+    case 32: return lora_launch<2>(name, a, s);
+    case 64: return lora_launch<4>(name, a, s);
+    default: return lora_launch<8>(name, a, s);
+  }
+}
