@@ -404,7 +404,7 @@ int wq_moe_step_run(const wq_moe_plan* plan, void* stream);
  * [0, pages), holds nothing: it is not read, attended to or written.
  *   k, v bf16, 16-byte aligned, strides multiples of 8, head_dim elements of
  *   one head contiguous; table int32 [requests][table_stride].
- * 1 <= page_size, table_width * page_size <= 2^30, 1 <= kv_heads <= 1024,
+ * 1 <= page_size, table_width * page_size <= 2^30, strides below 2^32, 1 <= kv_heads <= 1024,
  * head_dim a multiple of 8 up to 256 (wq_tree_attention: 64, 96, 128, 256).
  * Two positions in use must not share a cache row.
  */
@@ -525,16 +525,17 @@ int wq_qkv_rope_run(const wq_qkv_rope_plan* plan, void* stream);
  *   q, y  bf16 [tokens][q_stride / y_stride], rows of heads * head_dim,
  *         16-byte aligned, strides multiples of 8; y must not overlap q
  * A request brings at most max_tokens rows, 1 <= max_tokens <= 64; one that
- * brings more is left alone.  heads / kv_heads <= 64.  scale finite.
+ * brings more is left alone.  heads / kv_heads <= 64.  scale finite.  requests
+ * * kv_heads * row blocks (of 64 rows per key head) * positions / 32 stays
+ * below 2^31, with the positions that the table covers.
  * Scores and sums are fp32; the weights enter the second product as bf16.
  *
  * The positions of all requests are cut into equal shares for the launch's
  * workgroups and partial results joined in a fixed order: results are
  * bitwise reproducible.  `workspace` (device, 16-byte aligned,
- * wq_tree_attention_workspace_bytes long) holds the partial results and must
- * stay allocated and unmodified while the plan is used; prepare clears its
- * flags synchronously (call it outside graph capture).  Runs that share a
- * workspace must not overlap.
+ * wq_tree_attention_workspace_bytes long) holds the partial results between
+ * the launches of a run; nothing in it is kept from run to run.  Runs that
+ * share a workspace must not overlap.
  */
 typedef struct {
   wq_kv_cache cache;
@@ -557,9 +558,9 @@ typedef struct {
   wq_tree_attention a;
 } wq_tree_attention_plan;
 
-/* Workspace of a plan with these heads, head_dim and max_tokens (0 if they
- * are not supported). */
-int64_t wq_tree_attention_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_tokens);
+/* Workspace of a plan with these sizes (0 if they are not supported). */
+int64_t wq_tree_attention_workspace_bytes(int64_t requests, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                          int32_t max_tokens);
 int wq_tree_attention_prepare(const wq_tree_attention* a, void* workspace, int64_t workspace_bytes,
                               wq_tree_attention_plan* plan);
 int wq_tree_attention_run(const wq_tree_attention_plan* plan, void* stream);
@@ -620,7 +621,7 @@ int wq_kv_accept_run(const wq_kv_accept_plan* plan, void* stream);
  * parts (24 bits).  k % 8 == 0, 8 <= k <= 65536; rank % 8 == 0,
  * 8 <= rank <= 128; 0 <= n <= 2^20; 0 <= tokens <= 4096;
  * 1 <= adapters <= 4096; x, a, b 16-byte aligned, x_stride a multiple of 8.
- * `workspace` as for wq_tree_attention (prepare clears its flags).
+ * `workspace` as for wq_tree_attention.
  */
 typedef struct {
   const uint16_t* x;

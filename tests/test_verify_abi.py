@@ -110,6 +110,9 @@ def test_batch(call, kw, rc):
     ("rope", dict(q_stride=260), 2), ("rope", dict(eps=-1.0), 2), ("rope", dict(eps=float("nan")), 2),
     ("rope", dict(rot_scale=float("inf")), 2), ("rope", dict(q=OK, q_norm=BAD), 3),
     ("rope", dict(qkv_bf16=None, qkv_f32=OK, qkv_stride=514), 2),
+    ("attention", dict(batch=batch(requests=4096), cache=cache(kv_heads=1024, head_stride=64, table_width=1 << 16,
+                                                              table_stride=1 << 16), heads=1024, q_stride=65536,
+                       y_stride=65536), 2),
     ("attention", dict(q=None), 1), ("attention", dict(y=None), 1), ("attention", dict(heads=5), 2),
     ("attention", dict(heads=0), 2), ("attention", dict(heads=130), 2), ("attention", dict(max_tokens=0), 2),
     ("attention", dict(max_tokens=65), 2), ("attention", dict(cache=cache(head_dim=72)), 2),
@@ -143,13 +146,13 @@ def test_null_descriptions_and_foreign_plans():
 
 def test_workspace_sizes():
     d, p = attention(y=OK), wq.wq_tree_attention_plan()
-    need = wq.wq_tree_attention_workspace_bytes(4, 2, 64, 5)
+    need = wq.wq_tree_attention_workspace_bytes(2, 4, 2, 64, 5)
     assert need > 0
     assert lib.wq_tree_attention_prepare(ctypes.byref(d), OK, need - 1, ctypes.byref(p)) == 2
     assert lib.wq_tree_attention_prepare(ctypes.byref(d), BAD, need, ctypes.byref(p)) == 3
     assert lib.wq_tree_attention_prepare(ctypes.byref(d), None, need, ctypes.byref(p)) == 1
-    assert wq.wq_tree_attention_workspace_bytes(5, 2, 64, 5) == 0
-    assert wq.wq_tree_attention_workspace_bytes(4, 2, 80, 5) == 0
+    assert wq.wq_tree_attention_workspace_bytes(2, 5, 2, 64, 5) == 0
+    assert wq.wq_tree_attention_workspace_bytes(2, 4, 2, 80, 5) == 0
     d, p = lora(x=OK), wq.wq_lora_plan()
     need = wq.wq_lora_workspace_bytes(3, 64, 2, 8)
     assert need > 0

@@ -29,5 +29,6 @@ __all__ = list(_EXPORTS)
 def __getattr__(name):
     if name in _EXPORTS:
         from . import _binding
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)
+        return value
     raise AttributeError(name)

@@ -152,7 +152,7 @@ def _load():
     lib.wq_moe_step_run.argtypes = [ctypes.POINTER(wq_moe_plan), _P]
     lib.wq_moe_step_run.restype = ctypes.c_int
     lib.wq_rope_frequencies.argtypes = [_I32, _I32] + [ctypes.c_double] * 5 + [ctypes.POINTER(ctypes.c_float)] * 2
-    lib.wq_tree_attention_workspace_bytes.argtypes = [_I32] * 4
+    lib.wq_tree_attention_workspace_bytes.argtypes = [_I64] + [_I32] * 4
     lib.wq_tree_attention_workspace_bytes.restype = _I64
     lib.wq_lora_workspace_bytes.argtypes = [_I64, _I64, _I64, _I32]
     lib.wq_lora_workspace_bytes.restype = _I64
@@ -509,6 +509,16 @@ def _workspace(workspace, nbytes, device):
     return workspace, workspace.numel()
 
 
+def _raw_stream(device):
+    """Address of torch's current stream on `device`: what _stream returns, without building the Stream object (3 us
+    of a 6 us call)."""
+    global _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
+
+
 def _prepare(name, plan, device, keep, *args):
     import torch
     with torch.cuda.device(device):
@@ -521,7 +531,7 @@ def _prepare(name, plan, device, keep, *args):
 
 
 def _run(name, fn, plan, stream):
-    rc = fn(plan.at, _stream(stream))
+    rc = fn(plan.at, _raw_stream(plan.device) if stream is None else _stream(stream))
     if rc != 0:
         raise WQError(name, rc, lib.wq_last_error().decode(errors="replace"))
 
@@ -573,8 +583,8 @@ def wq_qkv_rope_run(plan, stream=None):
     _run("wq_qkv_rope_run", lib.wq_qkv_rope_run, plan, stream)
 
 
-def wq_tree_attention_workspace_bytes(heads, kv_heads, head_dim, max_tokens):
-    return int(lib.wq_tree_attention_workspace_bytes(heads, kv_heads, head_dim, max_tokens))
+def wq_tree_attention_workspace_bytes(requests, heads, kv_heads, head_dim, max_tokens):
+    return int(lib.wq_tree_attention_workspace_bytes(requests, heads, kv_heads, head_dim, max_tokens))
 
 
 def wq_tree_attention_prepare(q, k, v, table, starts, lengths, y, tree=None, max_tokens=64, scale=None,
@@ -595,7 +605,7 @@ def wq_tree_attention_prepare(q, k, v, table, starts, lengths, y, tree=None, max
                           y_stride, _vector(tree, "tree", tokens, ("int64", "uint64"), device),
                           dim ** -0.5 if scale is None else scale, heads, max_tokens)
     workspace, nbytes = _workspace(
-        workspace, wq_tree_attention_workspace_bytes(heads, cache.kv_heads, dim, max_tokens), device)
+        workspace, wq_tree_attention_workspace_bytes(requests, heads, cache.kv_heads, dim, max_tokens), device)
     return _prepare("wq_tree_attention_prepare", wq_tree_attention_plan(), device,
                     (q, k, v, table, starts, lengths, y, tree, workspace), ctypes.byref(a), _at(workspace),
                     nbytes)

@@ -1,0 +1,357 @@
+// The attention kernel: keys and values stream through LDS.
+//
+// A workgroup's share is a sequence of tiles, piece after piece.  Tiles travel
+// from memory to a ring of STAGES buffers in LDS without passing through
+// registers (global_load_lds: 64 lanes x 16 bytes to 1 KB of consecutive LDS),
+// requested STAGES - 1 tiles ahead of the products, across the borders of
+// pieces; the page numbers they need arrive the same way, STAGES - 1 tiles
+// earlier still.  Each wave requests a quarter of every tile's rows and counts
+// its own requests: before the barrier that opens a tile it waits until all but
+// the (STAGES - 2) newest tiles' requests are done.  (Ordinary loads and stores
+// in between only make that wait longer.)
+//
+// The waves share the tile in two ways, by the rows a launch can have per key
+// head:
+//   * WK = 1, blocks of 64 R rows: every wave owns 16 R rows from the first
+//     position of a piece to the last and reads the whole tile; nothing is
+//     joined inside the workgroup.
+//   * WK = 4, up to 16 rows: all waves have the same rows and take 32 positions
+//     of a tile of 128 each, so that a short context is a few steps long; they
+//     meet in LDS at the end of a piece.
+// K rows are stored with their 16-byte pieces exchanged by row (piece p of A
+// row m at p ^ m), so that the 16 lanes reading one piece of 16 rows hit
+// different banks; V rows are read along the row.
+#pragma once
+
+#include "wq_attention_shared.hpp"
+
+namespace wq {
+
+// Shape of a launch: positions of a tile, buffers of the ring, workgroups per
+// CU.  The ring holds up to 64 KB (two workgroups share a CU's 160 KB) or 128 KB,
+// with room for the deal of 4096 requests (512 with WK = 4) behind it; a wave's
+// quarter of a tile must be whole requests of 1 KB.
+template <int D, int WK>
+struct Shape {
+  static constexpr int TILE = WK == 4 ? 128 : D == 96 ? 64 : 32;
+  static constexpr int STAGES = WK == 4 ? 2 : D == 96 || D == 256 ? 3 : 4;
+  static constexpr int GROUPS = WK == 4 || D == 256 ? 1 : 2;
+};
+
+constexpr int kIdSlots = 8;           // page numbers: at most 2 STAGES - 2 tiles ahead
+
+template <int D, int WK>
+struct StreamLds {
+  using S = Shape<D, WK>;
+  alignas(16) uint16_t k[S::STAGES][S::TILE][D];
+  alignas(16) uint16_t v[S::STAGES][S::TILE][D];
+  alignas(16) uint32_t ids[kAttnWaves][kIdSlots][S::TILE / 4];
+  uint32_t live[S::STAGES][kAttnWaves];      // which of a wave's rows are in use and have a page
+};
+// Where the waves of WK = 4 meet.
+template <int D>
+struct MeetLds {
+  alignas(16) float o[2][16][D];
+  float m[kAttnWaves][16];
+  float l[kAttnWaves][16];
+  int special[kAttnWaves];
+};
+
+// Which piece of a K row stands at piece `p` (an involution).
+template <int D>
+__device__ __forceinline__ int k_piece(int p, int m) {
+  return D % 128 == 0 ? p ^ m : D == 64 ? p ^ (m >> 1) : p;
+}
+
+// Offset in LDS of a __shared__ object.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// Lane l's 16 (4) bytes at `from` to LDS at `to` + 16 (4) l.  In assembly so that
+// no wait is placed for it but those below.
+__device__ __forceinline__ void request16(const void* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+__device__ __forceinline__ void request4(const void* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
+}
+// All but the N newest requests of this wave are done, its LDS accesses too.
+template <int N>
+__device__ __forceinline__ void wait_requests() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
+
+template <int D, int R, int WK>
+__global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attention_stream_kernel(AttnArgs a) {
+  using S = Shape<D, WK>;
+  constexpr int TILE = S::TILE, STAGES = S::STAGES;
+  constexpr int ROWS = 16 * R * (kAttnWaves / WK);
+  constexpr int KS = D / 32, CW = D / 16, VW = CW / 2;
+  constexpr int CH = D / 8;                              // 16-byte pieces of a row
+  constexpr int TR = TILE / kAttnWaves;                  // a wave's rows of a tile
+  constexpr int NP = TR * CH / kWave;                    // its requests, each for keys and for values
+  constexpr int STEPS = TILE / 32 / WK;
+  static_assert(NP * kWave == TR * CH && STEPS >= 1 && (WK == 1 || R == 1), "tile does not divide");
+  extern __shared__ __align__(16) char lds[];
+  StreamLds<D, WK>& sh = *reinterpret_cast<StreamLds<D, WK>*>(lds);
+  constexpr int MEET = sizeof(StreamLds<D, WK>);
+  MeetLds<D>& mt = *reinterpret_cast<MeetLds<D>*>(lds + MEET);
+  const Deal d = deal_at(lds + MEET + (WK > 1 ? sizeof(MeetLds<D>) : 0), a.b.requests);
+  deal<ROWS, TILE>(a, d);
+  const int total = __builtin_amdgcn_readfirstlane(d.before[a.b.requests]);
+  const int per = share_of(a, total, (int)gridDim.x);
+  const int share = share_index((int)blockIdx.x, (int)gridDim.x);
+  if ((int64_t)share * per >= total) return;
+  const int at = share * per;
+  const int stop = (int)min((int64_t)at + per, (int64_t)total);
+  const int lane = lane_id(), wave = wave_id();
+  const int g = lane >> 4, c = lane & 15;
+  const int wr = wave / WK, wk = wave % WK;
+
+  Piece p = first_piece<ROWS, TILE>(a, d, at, stop);     // the products' piece
+  if (p.t0 >= p.t1) return;
+  Piece pi = p, pt = p;                                  // the page numbers', the tiles'
+  int ti = p.t0, tt = p.t0;
+
+  // page numbers of this wave's rows of the next tile
+  int slot_i = 0;
+  const auto request_ids = [&]() {
+    if (pi.t0 >= pi.t1) return;
+    if (lane < TR) {
+      const uint32_t pos = (uint32_t)(ti * TILE + wave * TR + lane);
+      const int32_t* from = a.c.table + (int64_t)pi.r * a.c.table_stride + (pos < a.c.limit ? page_of(a.c, pos) : 0u);
+      request4(from, lds_offset(&sh.ids[wave][slot_i][0]));
+    }
+    slot_i = (slot_i + 1) & (kIdSlots - 1);
+    if (++ti == pi.t1) {
+      next_piece<ROWS, TILE>(a, d, stop, pi);
+      ti = pi.t0;
+    }
+  };
+  // this wave's rows of the next tile; false where no tile is left
+  int slot_t = 0, stage_t = 0;
+  const auto request_tile = [&]() -> bool {
+    if (pt.t0 >= pt.t1) return false;
+    const int pl = lane & (TR - 1);
+    const uint32_t pos = (uint32_t)(tt * TILE + wave * TR + pl);
+    const uint32_t id = sh.ids[wave][slot_t][pl];
+    const bool has = pos < (uint32_t)(pt.length + pt.n) && pos < a.c.limit && id < a.c.pages;
+    // of a position that holds nothing: row 0 of the pool, never used
+    const uint64_t off = has ? row_offset(a.c, id, pos - page_of(a.c, pos) * a.c.page_size) : 0;
+    const uint32_t live = (uint32_t)__ballot(has);
+    if (lane == 0) sh.live[stage_t][wave] = live;
+    const uint64_t head = (uint64_t)pt.head * a.c.head_stride;
+    const uint16_t* from[NP][2];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int row = (i * kWave + lane) / CH, ch = (i * kWave + lane) % CH;
+      const int m = (row + wave * TR) & 31;              // its place in a step of 32
+      const uint64_t ro = __shfl(off, row) + head;
+      from[i][0] = a.c.k + ro + 8 * k_piece<D>(ch, (m & 3) | (m >> 3) << 2);
+      from[i][1] = a.c.v + ro + 8 * ch;
+    }
+    const uint32_t kto = lds_offset(&sh.k[stage_t][wave * TR][0]), vto = lds_offset(&sh.v[stage_t][wave * TR][0]);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      request16(from[i][0], __builtin_amdgcn_readfirstlane(kto + i * (kWave * 16)));
+      request16(from[i][1], __builtin_amdgcn_readfirstlane(vto + i * (kWave * 16)));
+    }
+    slot_t = (slot_t + 1) & (kIdSlots - 1);
+    stage_t = stage_t + 1 == STAGES ? 0 : stage_t + 1;
+    if (++tt == pt.t1) {
+      next_piece<ROWS, TILE>(a, d, stop, pt);
+      tt = pt.t0;
+    }
+    return true;
+  };
+
+  const int in0 = wr * 16 * R;                           // the wave's first row of a block
+  bf16x8 q[R][KS];
+  uint64_t seen[R];
+#pragma unroll
+  for (int t = 0; t < R; ++t) load_query<D>(a, p, p.block * ROWS + in0 + 16 * t + c, g, q[t], seen[t]);
+#pragma unroll 1
+  for (int i = 0; i < 2 * STAGES - 2; ++i) request_ids();
+  wait_requests<0>();
+#pragma unroll 1
+  for (int i = 0; i < STAGES - 1; ++i) request_tile();
+  // the share's first tile (fewer than STAGES - 1 may have been requested)
+  wait_requests<0>();
+  meet();
+
+  int stage = 0;
+  while (p.t0 < p.t1) {
+    const bool busy = p.block * ROWS + in0 < p.rows;     // else the wave only moves data
+    f32x4 o[R][CW];
+    float top[R], sum[R];
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      top[t] = -INFINITY;
+      sum[t] = 0.f;
+#pragma unroll
+      for (int j = 0; j < CW; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    bool special = false;
+#pragma unroll 1
+    for (int tile = p.t0; tile < p.t1; ++tile) {
+      const bool more = request_tile();
+      request_ids();
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        const int first = 32 * (wk + WK * st);           // the step's first position in the tile
+        const int base = tile * TILE + first;
+        if (busy && base < p.length + p.n) {
+          uint32_t live_step;
+          if constexpr (TR == 32) {
+            live_step = sh.live[stage][wk];
+          } else {
+            const uint32_t* lv = &sh.live[stage][first / TR];
+            live_step = 0;
+#pragma unroll
+            for (int i = 0; i < 32 / TR; ++i) live_step |= (lv[i] & ((1u << TR) - 1u)) << (TR * i);
+          }
+          live_step = __builtin_amdgcn_readfirstlane(live_step);
+          const bool whole = live_step == ~0u && base + 32 <= p.length;
+          f32x4 s[R][2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint16_t* row = sh.k[stage][first + 8 * (c >> 2) + 4 * u + (c & 3)];
+            bf16x8 kf[KS];
+#pragma unroll
+            for (int i = 0; i < KS; ++i) kf[i] = *reinterpret_cast<const bf16x8*>(row + 8 * k_piece<D>(g * KS + i, c));
+#pragma unroll
+            for (int t = 0; t < R; ++t) {
+              f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int i = 0; i < KS; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], q[t][i], acc, 0, 0, 0);
+              s[t][u] = acc;
+            }
+          }
+          uint32_t vw[8][VW];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t* row = reinterpret_cast<const uint32_t*>(&sh.v[stage][first + 8 * g + e][c * CW]);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) vw[e][i] = row[i];
+          }
+          uint32_t sees[R] = {};
+          if (!whole) {
+            const int past = base + 8 * g - p.length;    // drafts behind the context
+            const uint32_t live = live_step >> (8 * g) & 0xFFu;
+#pragma unroll
+            for (int t = 0; t < R; ++t) sees[t] = sees_of(past, seen[t]) & live;
+            // positions that hold nothing weigh nothing, whatever memory has
+            // there; a draft's infinities and NaN are added at the end
+            const uint32_t drafts = past >= 0 ? 0xFFu : past <= -8 ? 0u : 0xFFu << -past & 0xFFu;
+            bool found = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+              for (int i = 0; i < VW; ++i) {
+                const uint32_t x = live >> e & 1 ? vw[e][i] : 0u;
+                const uint32_t fine = (bf16_special(x) ? 0u : x & 0xFFFFu) | (bf16_special(x >> 16) ? 0u : x & 0xFFFF0000u);
+                const bool odd = (drafts >> e & 1) && fine != x;
+                vw[e][i] = odd ? fine : x;
+                found |= odd;
+              }
+            if (__any(found)) special = true;
+          }
+          bf16x8 w[R];
+          softmax_step<R, CW>(s, a.scale2, whole, sees, g, top, sum, o, w);
+#pragma unroll
+          for (int j = 0; j < CW; ++j) {
+            const bf16x8 b = v_column<VW>(vw, j);
+#pragma unroll
+            for (int t = 0; t < R; ++t) o[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[t], b, o[t][j], 0, 0, 0);
+          }
+        }
+      }
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      // opens the next tile: its requests are done, and everyone is through with this one's buffer
+      if (more)
+        wait_requests<(STAGES - 2) * 2 * NP>();
+      else
+        wait_requests<0>();
+      meet();
+    }
+
+    // the next piece's queries are under way while this one's results leave
+    const Piece now = p;
+    next_piece<ROWS, TILE>(a, d, stop, p);
+    if (p.t0 < p.t1) {
+#pragma unroll
+      for (int t = 0; t < R; ++t) load_query<D>(a, p, p.block * ROWS + in0 + 16 * t + c, g, q[t], seen[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      sum[t] += __shfl_xor(sum[t], 16);
+      sum[t] += __shfl_xor(sum[t], 32);
+    }
+    if constexpr (WK == 1) {
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        float most[4], all[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          most[i] = __shfl(top[t], 4 * g + i);
+          all[i] = __shfl(sum[t], 4 * g + i);
+        }
+        if (busy) {
+          write_rows<D, ROWS>(a, now, share, in0 + 16 * t, g, c, o[t], most, all);
+          if (special) add_special<D, ROWS>(a, now, share, now.t0 * TILE, now.t1 * TILE, in0 + 16 * t, g, c);
+        }
+      }
+    } else {
+      // the four waves meet: a common maximum, then (2, 3) -> (0, 1) -> 0
+      if (g == 0) {
+        mt.m[wave][c] = top[0];
+        mt.l[wave][c] = sum[0];
+      }
+      if (lane == 0) mt.special[wave] = special;
+      __syncthreads();
+      const bool any_special = (mt.special[0] | mt.special[1] | mt.special[2] | mt.special[3]) != 0;
+      float most[4], all[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * g + i;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) m = fmaxf(m, mt.m[w][row]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) l += mt.l[w][row] * __builtin_amdgcn_exp2f(mt.m[w][row] - ref);
+        const float f = __builtin_amdgcn_exp2f(mt.m[wave][row] - ref);
+        most[i] = m;
+        all[i] = l;
+#pragma unroll
+        for (int j = 0; j < CW; ++j) o[0][j][i] *= f;
+      }
+#pragma unroll
+      for (int half = 2; half >= 1; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < CW; ++j) mt.o[wave - half][4 * g + i][c * CW + j] = o[0][j][i];
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < CW; ++j) o[0][j][i] += mt.o[wave][4 * g + i][c * CW + j];
+        }
+        __syncthreads();
+      }
+      if (wave == 0) {
+        write_rows<D, ROWS>(a, now, share, 0, g, c, o[0], most, all);
+        if (any_special) add_special<D, ROWS>(a, now, share, now.t0 * TILE, now.t1 * TILE, 0, g, c);
+      }
+    }
+  }
+}
+
+}  // namespace wq

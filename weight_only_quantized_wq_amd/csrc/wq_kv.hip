@@ -29,10 +29,10 @@ int check_cache_sizes(const char* name, const wq_kv_cache& c) {
     return fail(WQ_ERR_SHAPE, "%s: kv_heads = %d must be in [1, %d]", name, c.kv_heads, kMaxHeads);
   if (c.head_dim < 8 || c.head_dim > 256 || c.head_dim % 8)
     return fail(WQ_ERR_SHAPE, "%s: head_dim = %d must be a multiple of 8 up to 256", name, c.head_dim);
-  const int64_t most = (int64_t)1 << 40;
+  const int64_t most = 0xFFFFFFFFll;
   for (int64_t s : {c.page_stride, c.token_stride, c.head_stride})
     if (s < 0 || s > most || s % 8)
-      return fail(WQ_ERR_SHAPE, "%s: cache strides (%lld, %lld, %lld) must be non-negative multiples of 8", name,
+      return fail(WQ_ERR_SHAPE, "%s: cache strides (%lld, %lld, %lld) must be multiples of 8 in [0, 2^32)", name,
                   (long long)c.page_stride, (long long)c.token_stride, (long long)c.head_stride);
   return WQ_OK;
 }
@@ -54,15 +54,17 @@ KvCache device_cache(const wq_kv_cache& c) {
   KvCache d{};
   d.k = c.k;
   d.v = c.v;
-  d.page_stride = c.page_stride;
-  d.token_stride = c.token_stride;
-  d.head_stride = c.head_stride;
+  d.page_stride = (uint32_t)c.page_stride;
+  d.token_stride = (uint32_t)c.token_stride;
+  d.head_stride = (uint32_t)c.head_stride;
   d.table = c.table;
   d.table_stride = c.table_stride;
-  int l = 0;
-  while (((int64_t)1 << l) < c.page_size) ++l;
-  d.shift = 31 + l;
-  d.magic = (((uint64_t)1 << d.shift) / (uint64_t)c.page_size) + 1;
+  if (c.page_size > 1) {
+    int l = 0;
+    while (((int64_t)1 << l) < c.page_size) ++l;
+    d.shift = l - 1;
+    d.magic = (uint32_t)(2 * ((((uint64_t)1 << (30 + l)) / (uint64_t)c.page_size) + 1));
+  }
   d.pages = (uint32_t)c.pages;
   d.page_size = (uint32_t)c.page_size;
   d.limit = (uint32_t)(c.table_width * c.page_size);

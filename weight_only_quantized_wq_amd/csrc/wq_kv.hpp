@@ -12,12 +12,12 @@ namespace wq {
 struct KvCache {
   uint16_t* k;
   uint16_t* v;
-  int64_t page_stride;
-  int64_t token_stride;
-  int64_t head_stride;
   const int32_t* table;
   int64_t table_stride;
-  uint64_t magic;      // page of a position: position * magic >> shift
+  uint32_t page_stride;
+  uint32_t token_stride;
+  uint32_t head_stride;
+  uint32_t magic;      // page of a position, see page_of
   int32_t shift;
   uint32_t pages;
   uint32_t page_size;
@@ -33,17 +33,18 @@ struct Batch {
   int32_t requests;
 };
 
-// Page index of a position below 2^31.  magic = floor(2^shift / page_size) + 1
-// with shift = 31 + ceil(log2(page_size)): the quotient exceeds the true one
-// by less than position / 2^shift * page_size / page_size < 1 / page_size, so
-// its integer part is exact.
+// Page index of a position below 2^30.  With l = ceil(log2(page_size)) >= 1,
+// magic = 2 (floor(2^(30 + l) / page_size) + 1) and shift = l - 1 the quotient
+// position * magic / 2^(31 + l) exceeds the true one by less than position /
+// 2^(30 + l) < 1 / page_size, so its integer part is exact.  (Pages of one
+// position: magic 0.)
 __device__ __forceinline__ uint32_t page_of(const KvCache& c, uint32_t p) {
-  return (uint32_t)(((uint64_t)p * c.magic) >> c.shift);
+  return c.magic ? __umulhi(p, c.magic) >> c.shift : p;
 }
 
-// Element offset of position p's row in page `pid` (head 0).
-__device__ __forceinline__ int64_t row_offset(const KvCache& c, uint32_t pid, uint32_t row) {
-  return (int64_t)pid * c.page_stride + (int64_t)row * c.token_stride;
+// Element offset of row `row` of page `pid` (head 0).
+__device__ __forceinline__ uint64_t row_offset(const KvCache& c, uint32_t pid, uint32_t row) {
+  return (uint64_t)pid * c.page_stride + (uint64_t)row * c.token_stride;
 }
 
 // Element offset of request r's position p (head 0), or -1 if it holds nothing.
@@ -52,7 +53,7 @@ __device__ __forceinline__ int64_t position_offset(const KvCache& c, int r, int6
   const uint32_t pg = page_of(c, (uint32_t)p);
   const uint32_t pid = (uint32_t)gmem(c.table)[(int64_t)r * c.table_stride + pg];
   if (pid >= c.pages) return -1;
-  return row_offset(c, pid, (uint32_t)p - pg * c.page_size);
+  return (int64_t)row_offset(c, pid, (uint32_t)p - pg * c.page_size);
 }
 
 // Host: checks (sizes, then alignment) and the device view.
