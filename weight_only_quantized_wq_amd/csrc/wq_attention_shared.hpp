@@ -60,7 +60,7 @@ struct AttnArgs {
 };
 
 // What a group costs besides its tiles, in tiles: queries in, results out.
-constexpr int kGroupCost = 1;
+constexpr int kGroupCost = 2;
 
 // The deal: per request its rows, length and the cost of all groups before it.
 struct Deal {
@@ -84,17 +84,6 @@ static size_t deal_bytes(int64_t requests) { return (size_t)((3 * requests + 1) 
 template <int TILE>
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int length, int count) {
   return (min(length + count, (int)a.c.limit) + TILE - 1) / TILE;
-}
-
-// Sum over the lanes up to and with this one (DPP, as wave_sum).
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast15 into rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast31 into rows 2 and 3
-  return v;
 }
 
 // Every thread of the workgroup; ends with a barrier.  A wave takes 64 requests
@@ -154,7 +143,7 @@ __device__ __forceinline__ int request_at(const Deal& d, int requests, int at) {
 // Tiles of a share: equal shares for the launch's workgroups, but not so small
 // that joining them costs more than streaming on.
 __device__ __forceinline__ int share_of(const AttnArgs& a, int total, int grid) {
-  const int even = (int)((uint32_t)(total + grid - 1) / (uint32_t)grid);
+  const int even = (total + grid - 1) >> (31 - __builtin_clz(grid));          // a power of two of workgroups
   return even > a.least ? even : a.least;
 }
 
@@ -215,7 +204,10 @@ __device__ __forceinline__ Piece first_piece(const AttnArgs& a, const Deal& d, i
   piece_request<ROWS, TILE>(a, d, r, p);
   const int before = __builtin_amdgcn_readfirstlane(d.before[r]);
   const int each = p.tiles + kGroupCost;
-  const int hb = (int)((uint32_t)(at - before) / (uint32_t)each);
+  // quotients below 2^16 from a reciprocal of 24 bits: off by one at most
+  int hb = (int)((float)(at - before) * __builtin_amdgcn_rcpf((float)each));
+  hb += (int64_t)hb * each > at - before ? -1 : (int64_t)(hb + 1) * each <= at - before ? 1 : 0;
+  hb = __builtin_amdgcn_readfirstlane(hb);
   p.head = p.blocks == 1 ? hb : (int)((uint32_t)hb / (uint32_t)p.blocks);
   p.block = hb - p.head * p.blocks;
   p.after = before + hb * each + kGroupCost;

@@ -3,12 +3,17 @@
 // A workgroup's share is a sequence of tiles, piece after piece.  Tiles travel
 // from memory to a ring of STAGES buffers in LDS without passing through
 // registers (global_load_lds: 64 lanes x 16 bytes to 1 KB of consecutive LDS),
-// requested STAGES - 1 tiles ahead of the products, across the borders of
-// pieces; the page numbers they need arrive the same way, STAGES - 1 tiles
-// earlier still.  Each wave requests a quarter of every tile's rows and counts
-// its own requests: before the barrier that opens a tile it waits until all but
-// the (STAGES - 2) newest tiles' requests are done.  (Ordinary loads and stores
+// STAGES of them under way before the first product and, across the borders of
+// pieces, one more requested into each buffer as it is done with.  Each wave
+// requests a quarter of every tile's rows and counts its own requests: before
+// the barrier that opens a tile it waits until all but the (STAGES - 2) newest
+// tiles' requests are done.  (Ordinary loads and stores
 // in between only make that wait longer.)
+//
+// With pages of a multiple of 8 positions (PAGE8) every 8 rows of a tile share a
+// page: its number is a scalar load, all address arithmetic is scalar, and a
+// request's lanes add offsets fixed for the whole launch.  Other pages look up
+// every row (and have their page numbers come through LDS like the tiles).
 //
 // The waves share the tile in two ways, by the rows a launch can have per key
 // head:
@@ -38,7 +43,7 @@ struct Shape {
   static constexpr int GROUPS = WK == 4 || D == 256 ? 1 : 2;
 };
 
-constexpr int kIdSlots = 8;           // page numbers: at most 2 STAGES - 2 tiles ahead
+constexpr int kIdSlots = 8;           // page numbers: requested STAGES tiles before the tile's own requests
 
 template <int D, int WK>
 struct StreamLds {
@@ -73,6 +78,10 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 __device__ __forceinline__ void request16(const void* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
 }
+// The same from lane offsets to a uniform address.
+__device__ __forceinline__ void request16(const void* base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
+}
 __device__ __forceinline__ void request4(const void* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
 }
@@ -83,7 +92,7 @@ __device__ __forceinline__ void wait_requests() {
 }
 __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
 
-template <int D, int R, int WK>
+template <int D, int R, int WK, bool PAGE8>
 __global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attention_stream_kernel(AttnArgs a) {
   using S = Shape<D, WK>;
   constexpr int TILE = S::TILE, STAGES = S::STAGES;
@@ -94,6 +103,7 @@ __global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attentio
   constexpr int NP = TR * CH / kWave;                    // its requests, each for keys and for values
   constexpr int STEPS = TILE / 32 / WK;
   static_assert(NP * kWave == TR * CH && STEPS >= 1 && (WK == 1 || R == 1), "tile does not divide");
+  static_assert(!PAGE8 || D != 96, "8 rows are no whole number of requests");
   extern __shared__ __align__(16) char lds[];
   StreamLds<D, WK>& sh = *reinterpret_cast<StreamLds<D, WK>*>(lds);
   constexpr int MEET = sizeof(StreamLds<D, WK>);
@@ -115,10 +125,41 @@ __global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attentio
   Piece pi = p, pt = p;                                  // the page numbers', the tiles'
   int ti = p.t0, tt = p.t0;
 
-  // page numbers of this wave's rows of the next tile
+  // PAGE8: lane offsets in bytes within 8 rows, keys (by the rows' place in a
+  // step) and values, and the page numbers of this wave's rows of tile tt
+  constexpr int GP = TR / 8;                             // a wave's groups of 8 rows
+  constexpr int N8 = 8 * CH / kWave;                     // requests of 8 rows
+  uint32_t koff[PAGE8 ? GP : 1][PAGE8 ? N8 : 1], voff[PAGE8 ? N8 : 1];
+  uint32_t id8[GP];
+  if constexpr (PAGE8) {
+#pragma unroll
+    for (int i = 0; i < N8; ++i) {
+      const int row = (i * kWave + lane) / CH, ch = (i * kWave + lane) % CH;
+      voff[i] = 2u * ((uint32_t)row * a.c.token_stride + 8 * ch);
+#pragma unroll
+      for (int j = 0; j < GP; ++j) {
+        const int m = (row & 3) | (GP == 1 ? wave & 3 : GP == 2 ? (2 * wave + j) & 3 : j) << 2;
+        koff[j][i] = 2u * ((uint32_t)row * a.c.token_stride + 8 * k_piece<D>(ch, m));
+      }
+    }
+  }
+  // the page numbers the next request_tile needs (scalar loads)
+  const auto look_ahead = [&]() {
+    if constexpr (PAGE8) {
+      if (pt.t0 >= pt.t1) return;
+      const int32_t* table = a.c.table + (int64_t)pt.r * a.c.table_stride;
+#pragma unroll
+      for (int j = 0; j < GP; ++j) {
+        const uint32_t pos = (uint32_t)(tt * TILE + wave * TR + 8 * j);
+        const int32_t* from = table + (pos < a.c.limit ? page_of(a.c, pos) : 0u);
+        id8[j] = (uint32_t)*(const __attribute__((address_space(4))) int32_t*)from;
+      }
+    }
+  };
+  // other pages: page numbers of this wave's rows of the next tile
   int slot_i = 0;
   const auto request_ids = [&]() {
-    if (pi.t0 >= pi.t1) return;
+    if (PAGE8 || pi.t0 >= pi.t1) return;
     if (lane < TR) {
       const uint32_t pos = (uint32_t)(ti * TILE + wave * TR + lane);
       const int32_t* from = a.c.table + (int64_t)pi.r * a.c.table_stride + (pos < a.c.limit ? page_of(a.c, pos) : 0u);
@@ -134,6 +175,35 @@ __global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attentio
   int slot_t = 0, stage_t = 0;
   const auto request_tile = [&]() -> bool {
     if (pt.t0 >= pt.t1) return false;
+    if constexpr (PAGE8) {
+      const uint32_t kto = lds_offset(&sh.k[stage_t][wave * TR][0]), vto = lds_offset(&sh.v[stage_t][wave * TR][0]);
+      const uint64_t head = (uint64_t)pt.head * a.c.head_stride;
+      const uint32_t end = min((uint32_t)(pt.length + pt.n), a.c.limit);
+      uint32_t live = 0;
+#pragma unroll
+      for (int j = 0; j < GP; ++j) {
+        const uint32_t pos = (uint32_t)(tt * TILE + wave * TR + 8 * j);
+        const bool has = pos < end && id8[j] < a.c.pages;
+        // of rows that hold nothing: the pool's first, never used
+        const uint64_t off = head + (has ? row_offset(a.c, id8[j], pos - page_of(a.c, pos) * a.c.page_size) : 0);
+        live |= (has ? end - pos >= 8 ? 0xFFu : (1u << (end - pos)) - 1u : 0u) << (8 * j);
+        const uint16_t* kp = (const uint16_t*)uniform_i64((int64_t)(a.c.k + off));
+        const uint16_t* vp = (const uint16_t*)uniform_i64((int64_t)(a.c.v + off));
+#pragma unroll
+        for (int i = 0; i < N8; ++i) {
+          request16(kp, koff[j][i], __builtin_amdgcn_readfirstlane(kto + (j * N8 + i) * (kWave * 16)));
+          request16(vp, voff[i], __builtin_amdgcn_readfirstlane(vto + (j * N8 + i) * (kWave * 16)));
+        }
+      }
+      if (lane == 0) sh.live[stage_t][wave] = live;
+      stage_t = stage_t + 1 == STAGES ? 0 : stage_t + 1;
+      if (++tt == pt.t1) {
+        next_piece<ROWS, TILE>(a, d, stop, pt);
+        tt = pt.t0;
+      }
+      look_ahead();
+      return true;
+    }
     const int pl = lane & (TR - 1);
     const uint32_t pos = (uint32_t)(tt * TILE + wave * TR + pl);
     const uint32_t id = sh.ids[wave][slot_t][pl];
@@ -172,13 +242,21 @@ __global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attentio
   uint64_t seen[R];
 #pragma unroll
   for (int t = 0; t < R; ++t) load_query<D>(a, p, p.block * ROWS + in0 + 16 * t + c, g, q[t], seen[t]);
+  if constexpr (PAGE8) {
+    look_ahead();
+  } else {
 #pragma unroll 1
-  for (int i = 0; i < 2 * STAGES - 2; ++i) request_ids();
-  wait_requests<0>();
+    for (int i = 0; i < 2 * STAGES; ++i) request_ids();
+    wait_requests<0>();
+  }
+  bool more = true;
 #pragma unroll 1
-  for (int i = 0; i < STAGES - 1; ++i) request_tile();
-  // the share's first tile (fewer than STAGES - 1 may have been requested)
-  wait_requests<0>();
+  for (int i = 0; i < STAGES; ++i) more = request_tile();
+  // opens the share's first tile (fewer than STAGES may be left to request)
+  if (more)
+    wait_requests<(STAGES - 1) * 2 * NP>();
+  else
+    wait_requests<0>();
   meet();
 
   int stage = 0;
@@ -196,8 +274,6 @@ __global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attentio
     bool special = false;
 #pragma unroll 1
     for (int tile = p.t0; tile < p.t1; ++tile) {
-      const bool more = request_tile();
-      request_ids();
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
         const int first = 32 * (wk + WK * st);           // the step's first position in the tile
@@ -275,6 +351,8 @@ __global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attentio
       else
         wait_requests<0>();
       meet();
+      more = request_tile();
+      request_ids();
     }
 
     // the next piece's queries are under way while this one's results leave

@@ -2,18 +2,19 @@
 //   y[t] = base[t] + scale[c] * B[c] (A[c] x[t]),  c = adapter[t].
 //
 // Rows of one adapter are put together on the device, wherever they stand in
-// the batch: a tile is up to 16 rows of one adapter (ranked by row index), and
-// every workgroup finds its own tile from a histogram of adapter[], so no
-// host pass and no extra launch are needed.  Two launches:
-//   1. lora_shrink_kernel: h = A x of a tile over a share of k, as matrix
-//      products (16 adapter rows x 16 token rows, v_mfma_f32_16x16x32_bf16);
-//      the waves' sums meet in LDS, the shares' in the second launch.
+// the batch: a tile is up to 16 rows of one adapter (ranked by row index), found
+// from a histogram of adapter[], so no host pass and no extra launch are
+// needed.  Two launches:
+//   1. lora_shrink_kernel: finds its tile, then h = A x over a share of k, as
+//      matrix products (16 adapter rows x 16 token rows,
+//      v_mfma_f32_16x16x32_bf16); the waves' sums meet in LDS, the shares' in
+//      the second launch.  The tile's rows are left in the workspace for it.
 //   2. lora_expand_kernel: adds the shares in order, scales, splits h into
 //      three bf16 parts (together all 24 bits, so that only fp32 sums round)
-//      and multiplies 16 rows of B at a time with them; base is added and the
+//      and multiplies 64 rows of B at a time with them; base is added and the
 //      result stored from the accumulators.
 // Weights are read once per tile; with few rows per adapter both launches are
-// bound by them, and with one row by launch latency.
+// bound by them, with many by base and y, and with one row by launch latency.
 #include <math.h>
 
 #include "wq_kv.hpp"
@@ -30,6 +31,14 @@ constexpr int kLoraStep = 128;             // inputs a wave takes at a time
 constexpr int64_t kLoraMaxTokens = 4096;
 constexpr int64_t kLoraMaxAdapters = 4096;
 
+// A tile as the first launch leaves it for the second.
+struct alignas(16) TileRows {
+  int32_t adapter;      // == adapters: rows without one
+  int32_t rows;         // 0: the batch has no such tile
+  int32_t unused[2];
+  int32_t row[kLoraRows];
+};
+
 struct LoraArgs {
   const uint16_t* x;
   int64_t x_stride;
@@ -43,6 +52,7 @@ struct LoraArgs {
   const int32_t* adapter;
   const int32_t* ranks;
   const float* scale;
+  TileRows* found;      // [tiles]
   float* part;          // [splits][tiles][16][rank16]
   int32_t tokens;
   int32_t k;
@@ -55,77 +65,97 @@ struct LoraArgs {
   int32_t vec;          // base and y rows take 16-byte (8-byte bf16) accesses
 };
 
-struct Tile {
-  int adapter;          // == adapters: rows without one
-  int rows;             // 0: no such tile
-};
-
 // LDS of the search: counts [adapters + 1], ids [tokens] as 16 bits.
-__device__ __host__ inline size_t search_bytes(int64_t tokens, int64_t adapters) {
+static size_t search_bytes(int64_t tokens, int64_t adapters) {
   return (size_t)((adapters + 1) * 4 + tokens * 2 + 15) / 16 * 16;
 }
 
-// Tile `want` of the batch: tiles are ordered by adapter (rows without one
-// last), then by row.  Every thread takes part; row[] (LDS) gets its rows.
-__device__ Tile find_tile(const LoraArgs& a, int want, char* lds, int (&row)[kLoraRows]) {
-  __shared__ int wave_tot[kLoraThreads / kWave];
-  __shared__ int hit[3];
+// Tile `want` of the batch into LDS.  Tiles are ordered by adapter (rows without
+// one last), then by row; with up to 16 rows by the adapter's first row.  Every
+// thread takes part.
+__device__ void find_tile(const LoraArgs& a, int want, char* lds, TileRows& tile) {
+  const int lane = lane_id(), wave = wave_id(), me = (int)threadIdx.x;
+  if (a.tokens <= kLoraRows) {
+    if (wave == 0) {
+      const int c = lane < a.tokens ? gmem(a.adapter)[lane] : 0;
+      const int id = (uint32_t)c < (uint32_t)a.adapters ? c : a.adapters;
+      uint32_t left = (1u << a.tokens) - 1u, mine = 0;
+      int adapter = 0;
+      for (int i = 0; i <= want && left; ++i) {
+        adapter = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+        mine = (uint32_t)__ballot(lane < a.tokens && id == adapter);
+        left &= ~mine;
+        if (i < want) mine = 0;
+      }
+      if (lane == 0) {
+        tile.adapter = adapter;
+        tile.rows = __popc(mine);
+      }
+      if (lane < kLoraRows && mine >> lane & 1) tile.row[__popc(mine & ((1u << lane) - 1u))] = lane;
+    }
+    __syncthreads();
+    return;
+  }
+  __shared__ int tot[2][kLoraThreads / kWave];
   int* count = reinterpret_cast<int*>(lds);
   uint16_t* id = reinterpret_cast<uint16_t*>(count + a.adapters + 1);
-  const int lane = lane_id(), wave = wave_id(), me = (int)threadIdx.x;
   for (int i = me; i <= a.adapters; i += kLoraThreads) count[i] = 0;
-  if (me == 0) hit[0] = -1;
+  if (me == 0) tile.rows = 0;
   __syncthreads();
-  for (int t = me; t < a.tokens; t += kLoraThreads) {
-    const int c = gmem(a.adapter)[t];
+  for (int base = wave * kWave; base < a.tokens; base += kLoraThreads) {
+    // rows of a request stand together: the first of a run counts for all of it
+    const int t = base + lane;
+    const int c = t < a.tokens ? gmem(a.adapter)[t] : 0;
     const int i = (uint32_t)c < (uint32_t)a.adapters ? c : a.adapters;
-    id[t] = (uint16_t)i;
-    atomicAdd(&count[i], 1);
+    if (t < a.tokens) id[t] = (uint16_t)i;
+    const int before = __shfl_up(i, 1);
+    const uint64_t heads = __ballot(t < a.tokens && (lane == 0 || before != i));
+    if (heads >> lane & 1) {
+      const uint64_t later = lane == kWave - 1 ? 0 : heads >> (lane + 1);
+      const int run = min(later ? __builtin_ctzll(later) + 1 : kWave - lane, a.tokens - t);
+      atomicAdd(&count[i], run);
+    }
   }
   __syncthreads();
-  const auto scan = [&](int v) {          // exclusive, over the workgroup
-    int run = v;
-    for (int s = 1; s < kWave; s <<= 1) {
-      const int up = __shfl_up(run, s);
-      if (lane >= s) run += up;
-    }
-    if (lane == kWave - 1) wave_tot[wave] = run;
+  const auto scan = [&](int v, int (&sums)[kLoraThreads / kWave]) {          // exclusive, over the workgroup
+    const int upto = wave_scan(v);
+    if (lane == kWave - 1) sums[wave] = upto;
     __syncthreads();
-    int before = run - v;
-    for (int w = 0; w < wave; ++w) before += wave_tot[w];
-    __syncthreads();
+    int before = upto - v;
+    for (int w = 0; w < wave; ++w) before += sums[w];
     return before;
   };
+  const auto tiles_of = [](int n) { return (n + kLoraRows - 1) / kLoraRows; };
   const int each = (a.adapters + kLoraThreads) / kLoraThreads;
   int mine = 0;
-  for (int i = me * each; i < min((me + 1) * each, a.adapters + 1); ++i) mine += (count[i] + kLoraRows - 1) / kLoraRows;
-  int before = scan(mine);
+  for (int i = me * each; i < min((me + 1) * each, a.adapters + 1); ++i) mine += tiles_of(count[i]);
+  int before = scan(mine, tot[0]);
   if (want >= before && want < before + mine) {
-    for (int i = me * each; i < min((me + 1) * each, a.adapters + 1); ++i) {
-      const int tiles = (count[i] + kLoraRows - 1) / kLoraRows;
+    for (int i = me * each;; ++i) {
+      const int tiles = tiles_of(count[i]);
       if (want < before + tiles) {
-        hit[0] = i;
-        hit[1] = (want - before) * kLoraRows;
-        hit[2] = count[i];
+        const int skip = (want - before) * kLoraRows;
+        tile.adapter = i;
+        tile.rows = min(kLoraRows, count[i] - skip);
+        tile.unused[0] = skip;
         break;
       }
       before += tiles;
     }
   }
   __syncthreads();
-  if (hit[0] < 0) return Tile{0, 0};
-  const int adapter = hit[0], skip = hit[1], rows = min(kLoraRows, hit[2] - skip);
+  if (tile.rows == 0) return;
+  const int adapter = tile.adapter;
   const int per = (a.tokens + kLoraThreads - 1) / kLoraThreads;
   int own = 0;
   for (int t = me * per; t < min((me + 1) * per, a.tokens); ++t) own += id[t] == adapter;
-  int at = scan(own) - skip;
-  for (int t = me * per; t < min((me + 1) * per, a.tokens); ++t)
+  int at = scan(own, tot[1]) - tile.unused[0];
+  for (int t = me * per; own && t < min((me + 1) * per, a.tokens); ++t)
     if (id[t] == adapter) {
-      if (at >= 0 && at < kLoraRows) row[at] = t;
+      if (at >= 0 && at < kLoraRows) tile.row[at] = t;
       ++at;
     }
   __syncthreads();
-  return Tile{adapter, rows};
 }
 
 __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
@@ -135,15 +165,17 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
 template <int RT>
 __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
   extern __shared__ __align__(16) char lds[];
-  __shared__ int row[kLoraRows];
+  __shared__ TileRows tile;
   __shared__ float sum[kLoraWaves][RT * 16][kLoraRows];
-  const Tile tile = find_tile(a, (int)blockIdx.x, lds, row);
+  find_tile(a, (int)blockIdx.x, lds, tile);
+  if (blockIdx.y == 0 && threadIdx.x < sizeof(TileRows) / 4)
+    gmem(reinterpret_cast<int32_t*>(a.found + blockIdx.x))[threadIdx.x] = reinterpret_cast<const int32_t*>(&tile)[threadIdx.x];
   if (tile.rows == 0 || tile.adapter == a.adapters) return;
   const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
   const int rank = rank_of(a, tile.adapter);
   const int k0 = (int)blockIdx.y * a.chunk, k1 = min(k0 + a.chunk, a.k);
   const bool has = c < tile.rows;
-  const uint16_t* xp = a.x + (int64_t)row[has ? c : 0] * a.x_stride;
+  const uint16_t* xp = a.x + (int64_t)tile.row[has ? c : 0] * a.x_stride;
   const uint16_t* ap = a.a + (int64_t)tile.adapter * a.rank * a.k;
   f32x4 acc[RT];
 #pragma unroll
@@ -158,7 +190,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
       xv[s] = has && in ? load16(xp + kk) : u32x4{0, 0, 0, 0};
 #pragma unroll
       for (int r = 0; r < RT; ++r)
-        av[r][s] = in && 16 * r + c < rank ? load_stream16(ap + (int64_t)(16 * r + c) * a.k + kk) : u32x4{0, 0, 0, 0};
+        av[r][s] = in && 16 * r + c < rank ? load16(ap + (int64_t)(16 * r + c) * a.k + kk) : u32x4{0, 0, 0, 0};
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
@@ -190,25 +222,78 @@ __device__ __forceinline__ void split3(float x, __bf16& hi, __bf16& mid, __bf16&
   lo = (__bf16)(r - (float)mid);
 }
 
+// B rows of 64 outputs go to four products of 16, output 4 c + j of the 64 to
+// column c of product j: lane (g, c) ends with four consecutive outputs of each
+// of the token rows 4 g .. 4 g + 3, and the 16 lanes of a row read base and write
+// y in one contiguous run.
 template <int RT>
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
   constexpr int KS = (RT + 1) / 2;          // products of 32 ranks
-  extern __shared__ __align__(16) char lds[];
-  __shared__ int row[kLoraRows];
+  constexpr int R16 = RT * 16;
   __shared__ float h[kLoraRows][KS * 32 + 4];
-  const Tile tile = find_tile(a, (int)blockIdx.x, lds, row);
-  if (tile.rows == 0) return;
+  const auto* tile = gmem(a.found + blockIdx.x);
+  const int rows = tile->rows, adapter = tile->adapter;
+  if (rows == 0) return;
   const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
-  const bool bare = tile.adapter == a.adapters;
-  const int rank = bare ? 0 : rank_of(a, tile.adapter);
-  const float scale = bare || !a.scale ? 1.f : gmem(a.scale)[tile.adapter];
-  for (int i = (int)threadIdx.x; i < kLoraRows * KS * 32; i += kLoraThreads) {
-    const int t = i / (KS * 32), j = i % (KS * 32);
-    float v = 0.f;
-    if (j < rank && t < tile.rows)
-      for (int s = 0; s < a.splits; ++s)
-        v += gmem(a.part)[((int64_t)s * a.tiles + blockIdx.x) * (kLoraRows * RT * 16) + t * (RT * 16) + j];
-    h[t][j] = v * scale;
+  const bool bare = adapter == a.adapters;
+  const int rank = bare ? 0 : rank_of(a, adapter);
+  const uint16_t* bp = a.b + (int64_t)(bare ? 0 : adapter) * a.n * a.rank;
+  int64_t row[4];
+  bool has[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    has[i] = 4 * g + i < rows;
+    row[i] = tile->row[has[i] ? 4 * g + i : 0];
+  }
+  const int n0 = (int)blockIdx.y * a.chunk, n1 = min(n0 + a.chunk, a.n);
+
+  u32x4 bv[4][KS];
+  f32x4 v[4];
+  // weights and base of outputs nb .. nb + 63, all requested before any is used
+  const auto request = [&](int nb) {
+    const int o = nb + 4 * c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        bv[j][s] = o + j < n1 && s * 32 + g * 8 < rank ? load16(bp + (int64_t)(o + j) * a.rank + s * 32 + g * 8)
+                                                       : u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (has[i] && a.base) {
+        const float* base = a.base + row[i] * a.base_stride + o;
+        if (a.vec && o + 4 <= n1) {
+          v[i] = __builtin_bit_cast(f32x4, load_stream16(base));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (o + j < n1) v[i][j] = gmem(base)[j];
+        }
+      }
+    }
+  };
+  int nb = n0 + wave * 64;
+  if (nb < n1) request(nb);
+
+  if (!bare) {
+    const float scale = a.scale ? gmem(a.scale)[adapter] : 1.f;
+    for (int i = (int)threadIdx.x; i < kLoraRows * KS * 32; i += kLoraThreads) {
+      const int tr = i / (KS * 32), j = i % (KS * 32);
+      float sum = 0.f;
+      if (j < rank && tr < rows) {
+        const float* from = a.part + (int64_t)blockIdx.x * (kLoraRows * R16) + tr * R16 + j;
+        const int64_t stride = (int64_t)a.tiles * (kLoraRows * R16);
+        for (int s = 0; s < a.splits; s += 8) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = gmem(from)[min(s + e, a.splits - 1) * stride];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum += s + e < a.splits ? x[e] : 0.f;
+        }
+      }
+      h[tr][j] = sum * scale;
+    }
   }
   __syncthreads();
   bf16x8 hv[KS][3];
@@ -217,71 +302,63 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       __bf16 p, q, r;
-      split3(h[c][s * 32 + g * 8 + e], p, q, r);
+      split3(bare ? 0.f : h[c][s * 32 + g * 8 + e], p, q, r);
       hv[s][0][e] = p, hv[s][1][e] = q, hv[s][2][e] = r;
     }
-  const uint16_t* bp = a.b + (int64_t)(bare ? 0 : tile.adapter) * a.n * a.rank;
-  const bool has = c < tile.rows;
-  const int t = row[has ? c : 0];
-  const float* base = a.base ? a.base + (int64_t)t * a.base_stride : nullptr;
-  const int n0 = (int)blockIdx.y * a.chunk, n1 = min(n0 + a.chunk, a.n);
-  for (int nb = n0 + wave * 16; nb < n1; nb += kLoraWaves * 16) {
-    u32x4 bv[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-      bv[s] = nb + c < n1 && s * 32 + g * 8 < rank ? load_stream16(bp + (int64_t)(nb + c) * a.rank + s * 32 + g * 8)
-                                                   : u32x4{0, 0, 0, 0};
+  for (; nb < n1; nb += kLoraWaves * 64) {
     if (rank & 7) {
       // columns of B past a rank that ends inside a piece of 8 do not count
 #pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int left = rank - (s * 32 + g * 8 + 2 * i);
+            bv[j][s][i] = left <= 0 ? 0u : left == 1 ? bv[j][s][i] & 0xFFFFu : bv[j][s][i];
+          }
+    }
+    f32x4 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = v[i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int left = rank - (s * 32 + g * 8 + 2 * i);
-          bv[s][i] = left <= 0 ? 0u : left == 1 ? bv[s][i] & 0xFFFFu : bv[s][i];
+        for (int q = 0; q < 3; ++q)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv[s][q], __builtin_bit_cast(bf16x8, bv[j][s]), acc, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i][j] += acc[i];
+    }
+    const int o = nb + 4 * c;
+    if (nb + kLoraWaves * 64 < n1) request(nb + kLoraWaves * 64);
+    const bool full = a.vec && o + 4 <= n1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!has[i]) continue;
+      if (a.y32) {
+        float* to = a.y32 + row[i] * a.y_stride + o;
+        if (full) {
+          *gmem(reinterpret_cast<u32x4*>(to)) = __builtin_bit_cast(u32x4, y[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (o + j < n1) gmem(to)[j] = y[i][j];
         }
-    }
-    const int j = nb + 4 * g;             // the lane's outputs: j .. j + 3 of row t
-    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
-    const bool full = a.vec && j + 4 <= n1;
-    if (has && base) {
-      if (full) {
-        v = __builtin_bit_cast(f32x4, load16(base + j));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j + i < n1) v[i] = gmem(base)[j + i];
       }
-    }
-    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (a.y16) {
+        uint16_t* to = a.y16 + row[i] * a.y_stride + o;
+        if (full) {
+          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+          *gmem(reinterpret_cast<u32x2*>(to)) = u32x2{(uint32_t)f32_to_bf16(y[i][0]) | (uint32_t)f32_to_bf16(y[i][1]) << 16,
+                                                      (uint32_t)f32_to_bf16(y[i][2]) | (uint32_t)f32_to_bf16(y[i][3]) << 16};
+        } else {
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int q = 0; q < 3; ++q)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bv[s]), hv[s][q], acc, 0, 0, 0);
-    if (!has) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += acc[i];
-    if (a.y32) {
-      float* y = a.y32 + (int64_t)t * a.y_stride + j;
-      if (full) {
-        *gmem(reinterpret_cast<u32x4*>(y)) = __builtin_bit_cast(u32x4, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j + i < n1) gmem(y)[i] = v[i];
-      }
-    }
-    if (a.y16) {
-      uint16_t* y = a.y16 + (int64_t)t * a.y_stride + j;
-      if (full) {
-        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-        *gmem(reinterpret_cast<u32x2*>(y)) = u32x2{(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
-                                                   (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j + i < n1) gmem(y)[i] = f32_to_bf16(v[i]);
+          for (int j = 0; j < 4; ++j)
+            if (o + j < n1) gmem(to)[j] = f32_to_bf16(y[i][j]);
+        }
       }
     }
   }
@@ -341,16 +418,16 @@ template <int RT>
 static int lora_launch(const char* name, LoraArgs a, hipStream_t s) {
   const size_t lds = search_bytes(a.tokens, a.adapters);
   const int steps = (a.k + kLoraStep - 1) / kLoraStep;
-  const int rows = (a.n + 15) / 16;
   a.chunk = (steps + a.splits - 1) / a.splits * kLoraStep;
   hipLaunchKernelGGL((lora_shrink_kernel<RT>), dim3((unsigned)a.tiles, (unsigned)a.splits), dim3(kLoraThreads), lds, s, a);
-  // expand: workgroups of at least one row block per wave, about 1024 in all
-  int64_t parts = (1024 + a.tiles - 1) / a.tiles;
+  // expand: 64 outputs per wave at a time, about 2048 workgroups in all
+  const int rows = (a.n + 63) / 64;
+  int64_t parts = (2048 + a.tiles - 1) / a.tiles;
   const int64_t most = (rows + kLoraWaves - 1) / kLoraWaves;
   parts = parts < most ? parts : most;
-  a.chunk = (int)((rows + parts - 1) / parts) * 16;
+  a.chunk = (int)((most + parts - 1) / parts) * kLoraWaves * 64;
   parts = (a.n + a.chunk - 1) / a.chunk;
-  hipLaunchKernelGGL((lora_expand_kernel<RT>), dim3((unsigned)a.tiles, (unsigned)parts), dim3(kLoraThreads), lds, s, a);
+  hipLaunchKernelGGL((lora_expand_kernel<RT>), dim3((unsigned)a.tiles, (unsigned)parts), dim3(kLoraThreads), 0, s, a);
   return launch_status(name);
 }
 
@@ -361,7 +438,7 @@ using namespace wq;
 extern "C" int64_t wq_lora_workspace_bytes(int64_t tokens, int64_t k, int64_t adapters, int32_t rank) {
   if (!lora_sizes_ok(tokens, k, adapters, rank)) return 0;
   const int tiles = lora_tiles(tokens, adapters);
-  return (int64_t)lora_splits(tiles, k) * tiles * kLoraRows * rank16(rank) * 4;
+  return (int64_t)tiles * sizeof(TileRows) + (int64_t)lora_splits(tiles, k) * tiles * kLoraRows * rank16(rank) * 4;
 }
 
 extern "C" int wq_lora_prepare(const wq_lora* a, void* workspace, int64_t workspace_bytes, wq_lora_plan* plan) {
@@ -406,7 +483,8 @@ extern "C" int wq_lora_run(const wq_lora_plan* plan, void* stream) {
   a.adapter = l.adapter;
   a.ranks = l.ranks;
   a.scale = l.scale;
-  a.part = static_cast<float*>(plan->workspace);
+  a.found = static_cast<TileRows*>(plan->workspace);
+  a.part = reinterpret_cast<float*>(a.found + plan->tiles);
   a.tokens = (int32_t)l.tokens;
   a.k = (int32_t)l.k;
   a.n = (int32_t)l.n;

@@ -153,7 +153,13 @@ static int attn_launch(const char* name, AttnArgs a, int grid, hipStream_t s) {
   const size_t lds = sizeof(StreamLds<D, WK>) + (WK > 1 ? sizeof(MeetLds<D>) : 0) + deal;
   a.least = kLeastPositions / TILE;
   a.uncut = kUncutPositions / TILE;
-  hipLaunchKernelGGL((attention_stream_kernel<D, R, WK>), dim3(grid), dim3(kAttnThreads), lds, s, a);
+  // lane offsets within 8 rows are 32-bit byte offsets
+  const bool page8 = a.c.page_size % 8 == 0 && a.c.token_stride < (1u << 28);
+  if constexpr (D != 96) {
+    if (page8) hipLaunchKernelGGL((attention_stream_kernel<D, R, WK, true>), dim3(grid), dim3(kAttnThreads), lds, s, a);
+  }
+  if (D == 96 || !page8)
+    hipLaunchKernelGGL((attention_stream_kernel<D, R, WK, false>), dim3(grid), dim3(kAttnThreads), lds, s, a);
   // a table that covers no more than an uncut group leaves nothing to join
   if ((int64_t)a.c.limit > kUncutPositions)
     hipLaunchKernelGGL((attention_join_kernel<D, ROWS, TILE>),
