@@ -617,8 +617,8 @@ int wq_kv_accept_run(const wq_kv_accept_plan* plan, void* stream);
  *   y_f32 / y_bf16 [tokens][y_stride], either may be NULL but not both; base
  *         may be y_f32 itself (then with the same stride)
  * Rows of one adapter share its weights, wherever they stand in the batch.
- * Sums are fp32, and A x is carried to the second product in three bf16
- * parts (24 bits).  k % 8 == 0, 8 <= k <= 65536; rank % 8 == 0,
+ * Sums are fp32, and A x is carried to the second product in bf16 parts: three
+ * (24 bits), or two (16 bits) where only y_bf16 is asked for.  k % 8 == 0, 8 <= k <= 65536; rank % 8 == 0,
  * 8 <= rank <= 128; 0 <= n <= 2^20; 0 <= tokens <= 4096;
  * 1 <= adapters <= 4096; x, a, b 16-byte aligned, x_stride a multiple of 8.
  * `workspace` as for wq_tree_attention.

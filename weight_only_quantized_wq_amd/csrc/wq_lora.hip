@@ -10,8 +10,8 @@
 //      v_mfma_f32_16x16x32_bf16); the waves' sums meet in LDS, the shares' in
 //      the second launch.  The tile's rows are left in the workspace for it.
 //   2. lora_expand_kernel: adds the shares in order, scales, splits h into
-//      three bf16 parts (together all 24 bits, so that only fp32 sums round)
-//      and multiplies 64 rows of B at a time with them; base is added and the
+//      bf16 parts -- three for fp32 results (together all 24 bits, so that only
+//      fp32 sums round), two for bf16 ones (16 bits) -- and multiplies 64 rows of B at a time with them; base is added and the
 //      result stored from the accumulators.
 // Weights are read once per tile; with few rows per adapter both launches are
 // bound by them, with many by base and y, and with one row by launch latency.
@@ -22,6 +22,8 @@
 namespace wq {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kLoraThreads = 256;
@@ -65,9 +67,10 @@ struct LoraArgs {
   int32_t vec;          // base and y rows take 16-byte (8-byte bf16) accesses
 };
 
-// LDS of the search: counts [adapters + 1], ids [tokens] as 16 bits.
+// LDS of the search: counts [adapters + 1], ids as 16 bits, padded to 512.
+__device__ __host__ inline size_t search_counts(int64_t adapters) { return (size_t)((adapters + 1) * 4 + 15) / 16 * 16; }
 static size_t search_bytes(int64_t tokens, int64_t adapters) {
-  return (size_t)((adapters + 1) * 4 + tokens * 2 + 15) / 16 * 16;
+  return search_counts(adapters) + (size_t)((tokens + 511) / 512 * 512) * 2;
 }
 
 // Tile `want` of the batch into LDS.  Tiles are ordered by adapter (rows without
@@ -96,19 +99,21 @@ __device__ void find_tile(const LoraArgs& a, int want, char* lds, TileRows& tile
     __syncthreads();
     return;
   }
-  __shared__ int tot[2][kLoraThreads / kWave];
   int* count = reinterpret_cast<int*>(lds);
-  uint16_t* id = reinterpret_cast<uint16_t*>(count + a.adapters + 1);
-  for (int i = me; i <= a.adapters; i += kLoraThreads) count[i] = 0;
-  if (me == 0) tile.rows = 0;
-  __syncthreads();
-  for (int base = wave * kWave; base < a.tokens; base += kLoraThreads) {
-    // rows of a request stand together: the first of a run counts for all of it
-    const int t = base + lane;
-    const int c = t < a.tokens ? gmem(a.adapter)[t] : 0;
+  uint16_t* id = reinterpret_cast<uint16_t*>(lds + search_counts(a.adapters));
+  // the workgroup builds the histogram (rows of a request stand together: the
+  // first of a run counts for all of it) ...
+  const int padded = (a.tokens + 511) / 512 * 512;
+  for (int base = 0; base < padded; base += kLoraThreads) {
+    const int t = base + me;
+    const int c = t < a.tokens ? gmem(a.adapter)[t] : -1;
+    if (base == 0) {
+      for (int i = me; i <= a.adapters; i += kLoraThreads) count[i] = 0;
+      __syncthreads();
+    }
     const int i = (uint32_t)c < (uint32_t)a.adapters ? c : a.adapters;
-    if (t < a.tokens) id[t] = (uint16_t)i;
-    const int before = __shfl_up(i, 1);
+    id[t] = (uint16_t)(t < a.tokens ? i : 0xFFFF);
+    const int before = __builtin_amdgcn_update_dpp(0, i, 0x138, 0xF, 0xF, false);       // wave_shr 1
     const uint64_t heads = __ballot(t < a.tokens && (lane == 0 || before != i));
     if (heads >> lane & 1) {
       const uint64_t later = lane == kWave - 1 ? 0 : heads >> (lane + 1);
@@ -117,44 +122,51 @@ __device__ void find_tile(const LoraArgs& a, int want, char* lds, TileRows& tile
     }
   }
   __syncthreads();
-  const auto scan = [&](int v, int (&sums)[kLoraThreads / kWave]) {          // exclusive, over the workgroup
-    const int upto = wave_scan(v);
-    if (lane == kWave - 1) sums[wave] = upto;
-    __syncthreads();
-    int before = upto - v;
-    for (int w = 0; w < wave; ++w) before += sums[w];
-    return before;
-  };
+  // ... and every wave reads it for itself: which adapter has the tile,
   const auto tiles_of = [](int n) { return (n + kLoraRows - 1) / kLoraRows; };
-  const int each = (a.adapters + kLoraThreads) / kLoraThreads;
+  const int each = a.adapters / kWave + 1;
   int mine = 0;
-  for (int i = me * each; i < min((me + 1) * each, a.adapters + 1); ++i) mine += tiles_of(count[i]);
-  int before = scan(mine, tot[0]);
-  if (want >= before && want < before + mine) {
-    for (int i = me * each;; ++i) {
+  for (int i = lane * each; i < min((lane + 1) * each, a.adapters + 1); ++i) mine += tiles_of(count[i]);
+  int before = wave_scan(mine) - mine;
+  const uint64_t holder = __ballot(want >= before && want < before + mine);
+  if (!holder) {
+    if (lane == 0) tile.rows = 0;
+    __syncthreads();
+    return;
+  }
+  int adapter = 0, skip = 0, rows = 0;
+  if (holder >> lane & 1) {
+    for (int i = lane * each;; ++i) {
       const int tiles = tiles_of(count[i]);
       if (want < before + tiles) {
-        const int skip = (want - before) * kLoraRows;
-        tile.adapter = i;
-        tile.rows = min(kLoraRows, count[i] - skip);
-        tile.unused[0] = skip;
+        adapter = i;
+        skip = (want - before) * kLoraRows;
+        rows = min(kLoraRows, count[i] - skip);
         break;
       }
       before += tiles;
     }
   }
-  __syncthreads();
-  if (tile.rows == 0) return;
-  const int adapter = tile.adapter;
-  const int per = (a.tokens + kLoraThreads - 1) / kLoraThreads;
-  int own = 0;
-  for (int t = me * per; t < min((me + 1) * per, a.tokens); ++t) own += id[t] == adapter;
-  int at = scan(own, tot[1]) - tile.unused[0];
-  for (int t = me * per; own && t < min((me + 1) * per, a.tokens); ++t)
-    if (id[t] == adapter) {
-      if (at >= 0 && at < kLoraRows) tile.row[at] = t;
-      ++at;
-    }
+  const int from = __builtin_ctzll(holder);
+  adapter = __builtin_amdgcn_readlane(adapter, from);
+  skip = __builtin_amdgcn_readlane(skip, from);
+  rows = __builtin_amdgcn_readlane(rows, from);
+  // and which rows, 8 ids a lane at a time (the waves write the same values)
+  for (int base = 0; base < padded; base += kWave * 8) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(id + base + lane * 8);
+    uint32_t hits = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hits |= ((w[e / 2] >> (e & 1 ? 16 : 0) & 0xFFFFu) == (uint32_t)adapter ? 1u : 0u) << e;
+    const int n = __popc(hits), upto = wave_scan(n);
+    int at = upto - n - skip;
+    for (; hits; hits &= hits - 1, ++at)
+      if (at >= 0 && at < kLoraRows) tile.row[at] = base + lane * 8 + __builtin_ctz(hits);
+    skip -= __builtin_amdgcn_readlane(upto, kWave - 1);
+  }
+  if (lane == 0) {
+    tile.adapter = adapter;
+    tile.rows = rows;
+  }
   __syncthreads();
 }
 
@@ -190,7 +202,16 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
       xv[s] = has && in ? load16(xp + kk) : u32x4{0, 0, 0, 0};
 #pragma unroll
       for (int r = 0; r < RT; ++r)
-        av[r][s] = in && 16 * r + c < rank ? load16(ap + (int64_t)(16 * r + c) * a.k + kk) : u32x4{0, 0, 0, 0};
+        av[r][s] = in && 16 * r + c < a.rank ? load16(ap + (int64_t)(16 * r + c) * a.k + kk) : u32x4{0, 0, 0, 0};
+    }
+    // rows past the adapter's own rank do not count, whatever they hold
+    if (rank < a.rank) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        if (16 * r + c >= rank) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) av[r][s] = u32x4{0, 0, 0, 0};
+        }
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
@@ -214,19 +235,11 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
   }
 }
 
-// x = hi + mid + lo to 24 bits, each part a bf16.
-__device__ __forceinline__ void split3(float x, __bf16& hi, __bf16& mid, __bf16& lo) {
-  hi = (__bf16)x;
-  const float r = x - (float)hi;
-  mid = (__bf16)r;
-  lo = (__bf16)(r - (float)mid);
-}
-
 // B rows of 64 outputs go to four products of 16, output 4 c + j of the 64 to
 // column c of product j: lane (g, c) ends with four consecutive outputs of each
 // of the token rows 4 g .. 4 g + 3, and the 16 lanes of a row read base and write
 // y in one contiguous run.
-template <int RT>
+template <int RT, int PARTS>
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
   constexpr int KS = (RT + 1) / 2;          // products of 32 ranks
   constexpr int R16 = RT * 16;
@@ -256,7 +269,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int s = 0; s < KS; ++s)
-        bv[j][s] = o + j < n1 && s * 32 + g * 8 < rank ? load16(bp + (int64_t)(o + j) * a.rank + s * 32 + g * 8)
+        bv[j][s] = !bare && o + j < n1 && s * 32 + g * 8 < a.rank ? load16(bp + (int64_t)(o + j) * a.rank + s * 32 + g * 8)
                                                        : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -281,7 +294,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
     for (int i = (int)threadIdx.x; i < kLoraRows * KS * 32; i += kLoraThreads) {
       const int tr = i / (KS * 32), j = i % (KS * 32);
       float sum = 0.f;
-      if (j < rank && tr < rows) {
+      if (j < R16 && tr < rows) {
         const float* from = a.part + (int64_t)blockIdx.x * (kLoraRows * R16) + tr * R16 + j;
         const int64_t stride = (int64_t)a.tiles * (kLoraRows * R16);
         for (int s = 0; s < a.splits; s += 8) {
@@ -292,31 +305,34 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
           for (int e = 0; e < 8; ++e) sum += s + e < a.splits ? x[e] : 0.f;
         }
       }
-      h[tr][j] = sum * scale;
+      h[tr][j] = j < rank ? sum * scale : 0.f;
     }
   }
   __syncthreads();
-  bf16x8 hv[KS][3];
+  bf16x8 hv[KS][PARTS];
 #pragma unroll
   for (int s = 0; s < KS; ++s)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      __bf16 p, q, r;
-      split3(bare ? 0.f : h[c][s * 32 + g * 8 + e], p, q, r);
-      hv[s][0][e] = p, hv[s][1][e] = q, hv[s][2][e] = r;
+      float left = bare ? 0.f : h[c][s * 32 + g * 8 + e];
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) {
+        hv[s][q][e] = (__bf16)left;
+        left -= (float)hv[s][q][e];
+      }
     }
   for (; nb < n1; nb += kLoraWaves * 64) {
-    if (rank & 7) {
-      // columns of B past a rank that ends inside a piece of 8 do not count
+    if (rank < a.rank) {
+      // columns of B past the adapter's own rank do not count
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+        for (int i = 0; i < 4; ++i) {
+          const int left = rank - (s * 32 + g * 8 + 2 * i);
+          const uint32_t keep = left <= 0 ? 0u : left == 1 ? 0xFFFFu : ~0u;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int left = rank - (s * 32 + g * 8 + 2 * i);
-            bv[j][s][i] = left <= 0 ? 0u : left == 1 ? bv[j][s][i] & 0xFFFFu : bv[j][s][i];
-          }
+          for (int j = 0; j < 4; ++j) bv[j][s][i] &= keep;
+        }
     }
     f32x4 y[4];
 #pragma unroll
@@ -327,7 +343,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+        for (int q = 0; q < PARTS; ++q)
           acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv[s][q], __builtin_bit_cast(bf16x8, bv[j][s]), acc, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i][j] += acc[i];
@@ -341,7 +357,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
       if (a.y32) {
         float* to = a.y32 + row[i] * a.y_stride + o;
         if (full) {
-          *gmem(reinterpret_cast<u32x4*>(to)) = __builtin_bit_cast(u32x4, y[i]);
+          __builtin_nontemporal_store(__builtin_bit_cast(u32x4, y[i]), gmem(reinterpret_cast<u32x4*>(to)));
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -351,9 +367,8 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
       if (a.y16) {
         uint16_t* to = a.y16 + row[i] * a.y_stride + o;
         if (full) {
-          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-          *gmem(reinterpret_cast<u32x2*>(to)) = u32x2{(uint32_t)f32_to_bf16(y[i][0]) | (uint32_t)f32_to_bf16(y[i][1]) << 16,
-                                                      (uint32_t)f32_to_bf16(y[i][2]) | (uint32_t)f32_to_bf16(y[i][3]) << 16};
+          const bf16x4 w = {(__bf16)y[i][0], (__bf16)y[i][1], (__bf16)y[i][2], (__bf16)y[i][3]};
+          __builtin_nontemporal_store(__builtin_bit_cast(u32x2, w), gmem(reinterpret_cast<u32x2*>(to)));
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -384,7 +399,7 @@ static int lora_tiles(int64_t tokens, int64_t adapters) {
 // Shares of k: enough workgroups for the chip, each wave at least one step.
 static int lora_splits(int tiles, int64_t k) {
   const int64_t most = (k + kLoraWaves * kLoraStep - 1) / (kLoraWaves * kLoraStep);
-  const int64_t want = (512 + tiles - 1) / tiles;
+  const int64_t want = (1024 + tiles - 1) / tiles;
   return (int)(want < most ? want : most);
 }
 
@@ -427,7 +442,11 @@ static int lora_launch(const char* name, LoraArgs a, hipStream_t s) {
   parts = parts < most ? parts : most;
   a.chunk = (int)((most + parts - 1) / parts) * kLoraWaves * 64;
   parts = (a.n + a.chunk - 1) / a.chunk;
-  hipLaunchKernelGGL((lora_expand_kernel<RT>), dim3((unsigned)a.tiles, (unsigned)parts), dim3(kLoraThreads), 0, s, a);
+  const dim3 grid((unsigned)a.tiles, (unsigned)parts);
+  if (a.y32)
+    hipLaunchKernelGGL((lora_expand_kernel<RT, 3>), grid, dim3(kLoraThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((lora_expand_kernel<RT, 2>), grid, dim3(kLoraThreads), 0, s, a);
   return launch_status(name);
 }
 
