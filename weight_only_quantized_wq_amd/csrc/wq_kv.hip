@@ -98,8 +98,9 @@ int same_device(const char* name, int32_t device) {
 // Norms, rotation, append
 //
 // One workgroup takes one token (with few tokens, a share of its heads).  The
-// token's rot_dim / 2 angles are reduced in fp64 and turned into (cos, sin)
-// once, in LDS; then every P = pow2(head_dim / 8) lanes take a head, 8
+// token's first heads are requested, its request is looked up and its rot_dim /
+// 2 angles are reduced in fp64 and turned into (cos, sin) once, in LDS; then
+// every P = pow2(head_dim / 8) lanes take a head, 8
 // elements a lane, so that a head is read and written in 16-byte pieces, its
 // square sum is a butterfly over P lanes and the partner of a rotated element
 // is in the lane itself (interleaved), in a lane a fixed distance away (halves
@@ -117,6 +118,7 @@ struct RopeArgs {
   const uint16_t* k_norm;
   const float* freq;
   float eps;
+  float per_dim;       // 1 / head_dim
   float rot_scale;
   int32_t rot_dim;
   int32_t heads;
@@ -125,24 +127,54 @@ struct RopeArgs {
 
 enum { kPairs = 0, kHalves = 1, kOddHalves = 2 };
 constexpr int kRopeThreads = 256;
+constexpr int kRopeHeads = 4;         // heads a lane group requests at once
 
+// Eight elements of a head as loaded.
 template <bool F32>
-__device__ __forceinline__ void load_head8(const void* qkv, int64_t at, float (&x)[8]) {
-  if (F32) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(qkv) + at);
-    const u32x4 a = load16(p), b = load16(p + 1);
+struct Head8 {
+  u32x4 w[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* qkv, int64_t at) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(F32 ? (const void*)(static_cast<const float*>(qkv) + at)
+                                                        : (const void*)(static_cast<const uint16_t*>(qkv) + at));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = __uint_as_float(a[e]);
-      x[4 + e] = __uint_as_float(b[e]);
-    }
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = load16(p + i);
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      x[e] = F32 ? __uint_as_float(w[F32 ? e / 4 : 0][e & 3]) : e & 1 ? bf16hi_to_f32(w[0][e / 2]) : bf16lo_to_f32(w[0][e / 2]);
+  }
+};
+
+// Sum over aligned groups of `lanes` lanes (a power of two up to 32).
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+  if (lanes >= 2) v += dpp_f<0xB1>(v);       // quad_perm [1,0,3,2]
+  if (lanes >= 4) v += dpp_f<0x4E>(v);       // quad_perm [2,3,0,1]
+  if (lanes >= 8) v += dpp_f<0x141>(v);      // row_half_mirror
+  if (lanes >= 16) v += dpp_f<0x140>(v);     // row_mirror
+  if (lanes >= 32) v += __shfl_xor(v, 16);
+  return v;
+}
+
+// other[e] = x[e] of the lane `far` on (the first `far` lanes of a head) or back
+// (the next `far`); without the LDS crossbar where that is an exchange of bits.
+__device__ __forceinline__ void partners(const float (&x)[8], float (&other)[8], int lane, int sub, int far) {
+  if (far == 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) other[e] = dpp_f<0x128>(x[e]);                 // row_ror 8
+  } else if (far == 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) other[e] = dpp_f<0x1B>(dpp_f<0x141>(x[e]));    // 7 - i, then 3 - i in each quad
+  } else if (far == 2) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) other[e] = dpp_f<0x4E>(x[e]);
+  } else if (far == 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) other[e] = dpp_f<0xB1>(x[e]);
   } else {
-    const u32x4 a = load16(static_cast<const uint16_t*>(qkv) + at);
+    const int from = lane + (sub < far ? far : sub < 2 * far ? -far : 0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = bf16lo_to_f32(a[e]);
-      x[2 * e + 1] = bf16hi_to_f32(a[e]);
-    }
+    for (int e = 0; e < 8; ++e) other[e] = __shfl(x[e], from);
   }
 }
 
@@ -152,6 +184,18 @@ __global__ __launch_bounds__(kRopeThreads) void qkv_rope_kernel(RopeArgs a) {
   __shared__ float exch[LAYOUT == kOddHalves ? kRopeThreads * 8 : 1];
   const int t = blockIdx.x;
   const int lane = lane_id();
+  const int dim = a.c.head_dim, kv = a.c.kv_heads, heads = a.heads, all = heads + 2 * kv;
+  const int sub = (int)threadIdx.x & (a.lanes - 1);        // lane within the head
+  const int step = (int)gridDim.y * (kRopeThreads / a.lanes);
+  const bool in = sub * 8 < dim;
+  const int h0 = (int)(blockIdx.y * (kRopeThreads / a.lanes) + threadIdx.x / a.lanes);
+  Head8<F32> raw[kRopeHeads];
+  const auto request = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kRopeHeads; ++i)
+      if (in && h + i * step < all) raw[i].load(a.qkv, (int64_t)t * a.qkv_stride + (int64_t)(h + i * step) * dim + sub * 8);
+  };
+  request(h0);
   // the token's request: how many of starts[1 ..] lie at or before it
   int r = 0;
   for (int i = 1 + lane; i - lane <= a.b.requests; i += kWave)
@@ -171,56 +215,59 @@ __global__ __launch_bounds__(kRopeThreads) void qkv_rope_kernel(RopeArgs a) {
     turn[threadIdx.x] = make_float2(c * a.rot_scale, s * a.rot_scale);
   }
   const int64_t cache_row = position_offset(a.c, r, slot);
+  Head8<false> weight[2];              // q_norm, k_norm
+  if (in && a.q_norm) weight[0].load(a.q_norm, sub * 8);
+  if (in && a.k_norm) weight[1].load(a.k_norm, sub * 8);
   __syncthreads();
+  // the lane's factors are the same for every head: o = x * cs + partner * sn
+  float cs[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int at = sub * 8 + e;
+    const bool first = LAYOUT == kPairs ? !(e & 1) : at < half;
+    const int i = LAYOUT == kPairs ? at / 2 : first ? at : at - half;
+    const float2 f = at < 2 * half ? turn[i] : make_float2(1.f, 0.f);
+    cs[e] = f.x;
+    sn[e] = first ? -f.y : f.y;
+  }
 
-  const int dim = a.c.head_dim, kv = a.c.kv_heads, heads = a.heads, all = heads + 2 * kv;
-  const int sub = (int)threadIdx.x & (a.lanes - 1);        // lane within the head
-  const int per_block = kRopeThreads / a.lanes;
-  const bool in = sub * 8 < dim;
-  for (int h = (int)(blockIdx.y * per_block + threadIdx.x / a.lanes); h - (int)(threadIdx.x / a.lanes) < all;
-       h += (int)gridDim.y * per_block) {
-    const bool on = in && h < all;
-    float x[8];
+  for (int hb = h0; hb - h0 < all; hb += kRopeHeads * step) {
+    if (hb != h0) request(hb);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (on) load_head8<F32>(a.qkv, (int64_t)t * a.qkv_stride + (int64_t)h * dim + sub * 8, x);
-    const bool key = h >= heads, value = h >= heads + kv;
-    const uint16_t* norm = key ? a.k_norm : a.q_norm;
-    if (a.q_norm || a.k_norm) {
-      float sq = 0.f;
+    for (int u = 0; u < kRopeHeads; ++u) {
+      const int h = hb + u * step;
+      if (h - h0 + (int)(blockIdx.y * (kRopeThreads / a.lanes)) >= all) break;      // the same for the whole workgroup
+      const bool on = in && h < all;
+      float x[8];
+      if (on) {
+        raw[u].values(x);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
-      for (int d = 1; d < a.lanes; d <<= 1) sq += __shfl_xor(sq, d);
-      if (on && norm && !value) {
-        const float f = 1.f / sqrtf(sq / (float)dim + a.eps);
-        float w[8];
-        load_head8<false>(norm, sub * 8, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * f * w[e];
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
       }
-    }
-    float o[8];
+      const bool key = h >= heads, value = h >= heads + kv;
+      if (a.q_norm || a.k_norm) {
+        float sq = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = x[e];
-    if (LAYOUT == kPairs) {
-      if (!value) {
+        for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
+        sq = group_sum(sq, a.lanes);
+        if (!value && (key ? a.k_norm : a.q_norm)) {
+          const float f = __builtin_amdgcn_rsqf(fmaf(sq, a.per_dim, a.eps));
+          Head8<false> ws;
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const int i = sub * 4 + e / 2;
-          if (i < half) {
-            const float2 cs = turn[i];
-            o[e] = x[e] * cs.x - x[e + 1] * cs.y;
-            o[e + 1] = x[e + 1] * cs.x + x[e] * cs.y;
-          }
+          for (int i = 0; i < 4; ++i) ws.w[0][i] = key ? weight[1].w[0][i] : weight[0].w[0][i];
+          float w[8];
+          ws.values(w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * f * w[e];
         }
       }
-    } else {
       float other[8];
-      if (LAYOUT == kHalves) {
-        const int first = sub * 8;
-        const int from = lane + (first < half ? half / 8 : first < 2 * half ? -(half / 8) : 0);
+      if (LAYOUT == kPairs) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) other[e] = __shfl(x[e], from);
+        for (int e = 0; e < 8; ++e) other[e] = x[e ^ 1];
+      } else if (LAYOUT == kHalves) {
+        partners(x, other, lane, sub, half / 8);
       } else {
         // a wave reads only what it wrote itself
         float* row = exch + ((int)threadIdx.x - sub) * 8;
@@ -237,30 +284,30 @@ __global__ __launch_bounds__(kRopeThreads) void qkv_rope_kernel(RopeArgs a) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
       }
-      if (!value) {
+      if (!on) continue;
+      u32x4 w;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int i = sub * 8 + e;
-          if (i < half) {
-            o[e] = x[e] * turn[i].x - other[e] * turn[i].y;
-          } else if (i < 2 * half) {
-            o[e] = x[e] * turn[i - half].x + other[e] * turn[i - half].y;
-          }
+      for (int e = 0; e < 4; ++e) {
+        float o[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int k = 2 * e + i;
+          // elements past rot_dim, and values, stay as they are (whatever the partner is)
+          const bool turns = !value && sub * 8 + k < 2 * half;
+          o[i] = turns ? fmaf(other[k], sn[k], x[k] * cs[k]) : x[k];
         }
+        const bf16x2 two = {(__bf16)o[0], (__bf16)o[1]};
+        w[e] = __builtin_bit_cast(uint32_t, two);
       }
+      uint16_t* to;
+      if (!key) {
+        to = a.q + (int64_t)t * a.q_stride + (int64_t)h * dim;
+      } else {
+        if (cache_row < 0) continue;
+        to = (value ? a.c.v : a.c.k) + cache_row + (int64_t)(h - heads - (value ? kv : 0)) * a.c.head_stride;
+      }
+      *gmem(reinterpret_cast<u32x4*>(to + sub * 8)) = w;
     }
-    if (!on) continue;
-    u32x4 w;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = (uint32_t)f32_to_bf16(o[2 * e]) | (uint32_t)f32_to_bf16(o[2 * e + 1]) << 16;
-    uint16_t* to;
-    if (!key) {
-      to = a.q + (int64_t)t * a.q_stride + (int64_t)h * dim;
-    } else {
-      if (cache_row < 0) continue;
-      to = (value ? a.c.v : a.c.k) + cache_row + (int64_t)(h - heads - (value ? kv : 0)) * a.c.head_stride;
-    }
-    *gmem(reinterpret_cast<u32x4*>(to + sub * 8)) = w;
   }
 }
 
@@ -461,6 +508,7 @@ extern "C" int wq_qkv_rope_run(const wq_qkv_rope_plan* plan, void* stream) {
   r.k_norm = a.k_norm;
   r.freq = a.freq;
   r.eps = a.eps;
+  r.per_dim = 1.f / (float)a.cache.head_dim;
   r.rot_scale = a.rot_scale;
   r.rot_dim = a.rot_dim;
   r.heads = a.heads;

@@ -2,7 +2,7 @@
 //   y[t] = base[t] + scale[c] * B[c] (A[c] x[t]),  c = adapter[t].
 //
 // Rows of one adapter are put together on the device, wherever they stand in
-// the batch: a tile is up to 16 rows of one adapter (ranked by row index), found
+// the batch: a tile is up to 32 rows of one adapter (ranked by row index), found
 // from a histogram of adapter[], so no host pass and no extra launch are
 // needed.  Two launches:
 //   1. lora_shrink_kernel: finds its tile, then h = A x over a share of k, as
@@ -28,7 +28,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWaves = 4;
-constexpr int kLoraRows = 16;              // rows of a tile
+constexpr int kLoraRows = 32;              // rows of a tile, two halves of 16
 constexpr int kLoraStep = 128;             // inputs a wave takes at a time
 constexpr int64_t kLoraMaxTokens = 4096;
 constexpr int64_t kLoraMaxAdapters = 4096;
@@ -55,7 +55,7 @@ struct LoraArgs {
   const int32_t* ranks;
   const float* scale;
   TileRows* found;      // [tiles]
-  float* part;          // [splits][tiles][16][rank16]
+  float* part;          // [splits][tiles][32][rank16]
   int32_t tokens;
   int32_t k;
   int32_t n;
@@ -74,7 +74,7 @@ static size_t search_bytes(int64_t tokens, int64_t adapters) {
 }
 
 // Tile `want` of the batch into LDS.  Tiles are ordered by adapter (rows without
-// one last), then by row; with up to 16 rows by the adapter's first row.  Every
+// one last), then by row; with up to 32 rows by the adapter's first row.  Every
 // thread takes part.
 __device__ void find_tile(const LoraArgs& a, int want, char* lds, TileRows& tile) {
   const int lane = lane_id(), wave = wave_id(), me = (int)threadIdx.x;
@@ -82,7 +82,7 @@ __device__ void find_tile(const LoraArgs& a, int want, char* lds, TileRows& tile
     if (wave == 0) {
       const int c = lane < a.tokens ? gmem(a.adapter)[lane] : 0;
       const int id = (uint32_t)c < (uint32_t)a.adapters ? c : a.adapters;
-      uint32_t left = (1u << a.tokens) - 1u, mine = 0;
+      uint32_t left = a.tokens == 32 ? ~0u : (1u << a.tokens) - 1u, mine = 0;
       int adapter = 0;
       for (int i = 0; i <= want && left; ++i) {
         adapter = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
@@ -103,22 +103,32 @@ __device__ void find_tile(const LoraArgs& a, int want, char* lds, TileRows& tile
   uint16_t* id = reinterpret_cast<uint16_t*>(lds + search_counts(a.adapters));
   // the workgroup builds the histogram (rows of a request stand together: the
   // first of a run counts for all of it) ...
+  constexpr int kBatch = 4;
   const int padded = (a.tokens + 511) / 512 * 512;
-  for (int base = 0; base < padded; base += kLoraThreads) {
-    const int t = base + me;
-    const int c = t < a.tokens ? gmem(a.adapter)[t] : -1;
-    if (base == 0) {
+  for (int first = 0; first < padded; first += kBatch * kLoraThreads) {
+    int c[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int t = first + b * kLoraThreads + me;
+      c[b] = t < a.tokens ? gmem(a.adapter)[t] : -1;
+    }
+    if (first == 0) {
       for (int i = me; i <= a.adapters; i += kLoraThreads) count[i] = 0;
       __syncthreads();
     }
-    const int i = (uint32_t)c < (uint32_t)a.adapters ? c : a.adapters;
-    id[t] = (uint16_t)(t < a.tokens ? i : 0xFFFF);
-    const int before = __builtin_amdgcn_update_dpp(0, i, 0x138, 0xF, 0xF, false);       // wave_shr 1
-    const uint64_t heads = __ballot(t < a.tokens && (lane == 0 || before != i));
-    if (heads >> lane & 1) {
-      const uint64_t later = lane == kWave - 1 ? 0 : heads >> (lane + 1);
-      const int run = min(later ? __builtin_ctzll(later) + 1 : kWave - lane, a.tokens - t);
-      atomicAdd(&count[i], run);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int t = first + b * kLoraThreads + me;
+      if (t - lane >= padded) break;
+      const int i = (uint32_t)c[b] < (uint32_t)a.adapters ? c[b] : a.adapters;
+      id[t] = (uint16_t)(t < a.tokens ? i : 0xFFFF);
+      const int before = __builtin_amdgcn_update_dpp(0, i, 0x138, 0xF, 0xF, false);     // wave_shr 1
+      const uint64_t heads = __ballot(t < a.tokens && (lane == 0 || before != i));
+      if (heads >> lane & 1) {
+        const uint64_t later = lane == kWave - 1 ? 0 : heads >> (lane + 1);
+        const int run = min(later ? __builtin_ctzll(later) + 1 : kWave - lane, a.tokens - t);
+        atomicAdd(&count[i], run);
+      }
     }
   }
   __syncthreads();
@@ -178,7 +188,7 @@ template <int RT>
 __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
   extern __shared__ __align__(16) char lds[];
   __shared__ TileRows tile;
-  __shared__ float sum[kLoraWaves][RT * 16][kLoraRows];
+  __shared__ float sum[kLoraWaves][RT * 16][17];
   find_tile(a, (int)blockIdx.x, lds, tile);
   if (blockIdx.y == 0 && threadIdx.x < sizeof(TileRows) / 4)
     gmem(reinterpret_cast<int32_t*>(a.found + blockIdx.x))[threadIdx.x] = reinterpret_cast<const int32_t*>(&tile)[threadIdx.x];
@@ -186,23 +196,32 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
   const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
   const int rank = rank_of(a, tile.adapter);
   const int k0 = (int)blockIdx.y * a.chunk, k1 = min(k0 + a.chunk, a.k);
-  const bool has = c < tile.rows;
-  const uint16_t* xp = a.x + (int64_t)tile.row[has ? c : 0] * a.x_stride;
-  const uint16_t* ap = a.a + (int64_t)tile.adapter * a.rank * a.k;
-  f32x4 acc[RT];
+  const int halves = tile.rows > 16 ? 2 : 1;
+  const uint16_t* xp[2];
+  bool has[2];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // lane group g takes 32 inputs of a step of 128, as four pieces of 8
+  for (int h = 0; h < 2; ++h) {
+    has[h] = 16 * h + c < tile.rows;
+    xp[h] = a.x + (int64_t)tile.row[has[h] ? 16 * h + c : 0] * a.x_stride;
+  }
+  const uint16_t* ap = a.a + (int64_t)tile.adapter * a.rank * a.k;
+  f32x4 acc[2][RT];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[h][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // of each 32 inputs lane group g takes 8: a row's 64 bytes are one run
   for (int kb = k0 + wave * kLoraStep; kb < k1; kb += kLoraWaves * kLoraStep) {
-    u32x4 xv[4], av[RT][4];
+    u32x4 xv[2][4], av[RT][4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int kk = kb + g * 32 + s * 8;
+      const int kk = kb + s * 32 + g * 8;
       const bool in = kk < k1;
-      xv[s] = has && in ? load16(xp + kk) : u32x4{0, 0, 0, 0};
 #pragma unroll
       for (int r = 0; r < RT; ++r)
         av[r][s] = in && 16 * r + c < a.rank ? load16(ap + (int64_t)(16 * r + c) * a.k + kk) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) xv[h][s] = has[h] && in ? load16(xp[h] + kk) : u32x4{0, 0, 0, 0};
     }
     // rows past the adapter's own rank do not count, whatever they hold
     if (rank < a.rank) {
@@ -214,36 +233,48 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
         }
     }
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int h = 0; h < 2; ++h) {
+      if (h == halves) break;
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[r][s]),
-                                                         __builtin_bit_cast(bf16x8, xv[s]), acc[r], 0, 0, 0);
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          acc[h][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[r][s]),
+                                                              __builtin_bit_cast(bf16x8, xv[h][s]), acc[h][r], 0, 0, 0);
+    }
   }
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[wave][16 * r + 4 * g + i][c] = acc[r][i];
-  __syncthreads();
   float* out = a.part + ((int64_t)blockIdx.y * a.tiles + blockIdx.x) * (kLoraRows * RT * 16);
-  for (int i = (int)threadIdx.x; i < kLoraRows * RT * 16; i += kLoraThreads) {
-    const int t = i / (RT * 16), j = i % (RT * 16);
-    float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kLoraWaves; ++w) v += sum[w][j][t];
-    gmem(out)[i] = v;
+  for (int h = 0; h < 2; ++h) {
+    if (h == halves) break;
+    if (h) __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[wave][16 * r + 4 * g + i][c] = acc[h][r][i];
+    __syncthreads();
+    for (int i = (int)threadIdx.x; i < 16 * RT * 16; i += kLoraThreads) {
+      const int t = i / (RT * 16), j = i % (RT * 16);
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kLoraWaves; ++w) v += sum[w][j][t];
+      gmem(out)[h * 16 * RT * 16 + i] = v;
+    }
   }
 }
 
 // B rows of 64 outputs go to four products of 16, output 4 c + j of the 64 to
 // column c of product j: lane (g, c) ends with four consecutive outputs of each
-// of the token rows 4 g .. 4 g + 3, and the 16 lanes of a row read base and write
-// y in one contiguous run.
+// of the token rows 4 g .. 4 g + 3 of a half, and the 16 lanes of a row read base
+// and write y in one contiguous run.  What bounds it is the latency of those
+// reads, so 32 rows share the weights of 64 outputs: twice the bytes of base in
+// flight for the same weights.
 template <int RT, int PARTS>
 __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
   constexpr int KS = (RT + 1) / 2;          // products of 32 ranks
   constexpr int R16 = RT * 16;
-  __shared__ float h[kLoraRows][KS * 32 + 4];
+  // h as the products take it: [half][product][part][lane][8]
+  __shared__ __align__(16) __bf16 hs[2][KS][PARTS][kWave][8];
   const auto* tile = gmem(a.found + blockIdx.x);
   const int rows = tile->rows, adapter = tile->adapter;
   if (rows == 0) return;
@@ -251,76 +282,75 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
   const bool bare = adapter == a.adapters;
   const int rank = bare ? 0 : rank_of(a, adapter);
   const uint16_t* bp = a.b + (int64_t)(bare ? 0 : adapter) * a.n * a.rank;
-  int64_t row[4];
-  bool has[4];
+  const int halves = rows > 16 ? 2 : 1;
+  int row[2][4];
+  bool has[2][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    has[i] = 4 * g + i < rows;
-    row[i] = tile->row[has[i] ? 4 * g + i : 0];
-  }
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      has[h][i] = 16 * h + 4 * g + i < rows;
+      row[h][i] = tile->row[has[h][i] ? 16 * h + 4 * g + i : 0];
+    }
   const int n0 = (int)blockIdx.y * a.chunk, n1 = min(n0 + a.chunk, a.n);
 
   u32x4 bv[4][KS];
-  f32x4 v[4];
+  f32x4 v[2][4];
   // weights and base of outputs nb .. nb + 63, all requested before any is used
   const auto request = [&](int nb) {
     const int o = nb + 4 * c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[h][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (has[h][i] && a.base) {
+          const float* base = a.base + (int64_t)row[h][i] * a.base_stride + o;
+          if (a.vec && o + 4 <= n1) {
+            v[h][i] = __builtin_bit_cast(f32x4, load_stream16(base));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (o + j < n1) v[h][i][j] = gmem(base)[j];
+          }
+        }
+      }
+      if (halves == 1) break;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int s = 0; s < KS; ++s)
         bv[j][s] = !bare && o + j < n1 && s * 32 + g * 8 < a.rank ? load16(bp + (int64_t)(o + j) * a.rank + s * 32 + g * 8)
-                                                       : u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (has[i] && a.base) {
-        const float* base = a.base + row[i] * a.base_stride + o;
-        if (a.vec && o + 4 <= n1) {
-          v[i] = __builtin_bit_cast(f32x4, load_stream16(base));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (o + j < n1) v[i][j] = gmem(base)[j];
-        }
-      }
-    }
+                                                                : u32x4{0, 0, 0, 0};
   };
   int nb = n0 + wave * 64;
   if (nb < n1) request(nb);
 
-  if (!bare) {
-    const float scale = a.scale ? gmem(a.scale)[adapter] : 1.f;
-    for (int i = (int)threadIdx.x; i < kLoraRows * KS * 32; i += kLoraThreads) {
-      const int tr = i / (KS * 32), j = i % (KS * 32);
-      float sum = 0.f;
-      if (j < R16 && tr < rows) {
-        const float* from = a.part + (int64_t)blockIdx.x * (kLoraRows * R16) + tr * R16 + j;
-        const int64_t stride = (int64_t)a.tiles * (kLoraRows * R16);
-        for (int s = 0; s < a.splits; s += 8) {
-          float x[8];
+  const float scale = bare || !a.scale ? 1.f : gmem(a.scale)[adapter];
+  for (int i = (int)threadIdx.x; i < halves * 16 * KS * 32; i += kLoraThreads) {
+    const int tr = i / (KS * 32), j = i % (KS * 32);
+    float sum = 0.f;
+    if (j < R16 && tr < rows && !bare) {
+      const float* from = a.part + (int64_t)blockIdx.x * (kLoraRows * R16) + tr * R16 + j;
+      const int64_t stride = (int64_t)a.tiles * (kLoraRows * R16);
+      for (int s = 0; s < a.splits; s += 8) {
+        float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = gmem(from)[min(s + e, a.splits - 1) * stride];
+        for (int e = 0; e < 8; ++e) x[e] = gmem(from)[min(s + e, a.splits - 1) * stride];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum += s + e < a.splits ? x[e] : 0.f;
-        }
+        for (int e = 0; e < 8; ++e) sum += s + e < a.splits ? x[e] : 0.f;
       }
-      h[tr][j] = j < rank ? sum * scale : 0.f;
+    }
+    float left = j < rank ? sum * scale : 0.f;
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      const __bf16 part = (__bf16)left;
+      hs[tr >> 4][j >> 5][q][(j >> 3 & 3) * 16 + (tr & 15)][j & 7] = part;
+      left -= (float)part;
     }
   }
   __syncthreads();
-  bf16x8 hv[KS][PARTS];
-#pragma unroll
-  for (int s = 0; s < KS; ++s)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float left = bare ? 0.f : h[c][s * 32 + g * 8 + e];
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        hv[s][q][e] = (__bf16)left;
-        left -= (float)hv[s][q][e];
-      }
-    }
   for (; nb < n1; nb += kLoraWaves * 64) {
     if (rank < a.rank) {
       // columns of B past the adapter's own rank do not count
@@ -334,45 +364,59 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
           for (int j = 0; j < 4; ++j) bv[j][s][i] &= keep;
         }
     }
-    f32x4 y[4];
+    const int o = nb + 4 * c;
+    const bool full = a.vec && o + 4 <= n1;
+    f32x4 y[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = v[i];
+    for (int h = 0; h < 2; ++h) {
+      if (h == halves) break;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < 4; ++i) y[h][i] = v[h][i];
+      bf16x8 hv[KS][PARTS];
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv[s][q], __builtin_bit_cast(bf16x8, bv[j][s]), acc, 0, 0, 0);
+        for (int q = 0; q < PARTS; ++q) hv[s][q] = *reinterpret_cast<const bf16x8*>(hs[h][s][q][lane]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i][j] += acc[i];
-    }
-    const int o = nb + 4 * c;
-    if (nb + kLoraWaves * 64 < n1) request(nb + kLoraWaves * 64);
-    const bool full = a.vec && o + 4 <= n1;
+      for (int j = 0; j < 4; ++j) {
+        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!has[i]) continue;
-      if (a.y32) {
-        float* to = a.y32 + row[i] * a.y_stride + o;
-        if (full) {
-          __builtin_nontemporal_store(__builtin_bit_cast(u32x4, y[i]), gmem(reinterpret_cast<u32x4*>(to)));
-        } else {
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (o + j < n1) gmem(to)[j] = y[i][j];
-        }
+          for (int q = 0; q < PARTS; ++q)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv[s][q], __builtin_bit_cast(bf16x8, bv[j][s]), acc, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[h][i][j] += acc[i];
       }
-      if (a.y16) {
-        uint16_t* to = a.y16 + row[i] * a.y_stride + o;
-        if (full) {
-          const bf16x4 w = {(__bf16)y[i][0], (__bf16)y[i][1], (__bf16)y[i][2], (__bf16)y[i][3]};
-          __builtin_nontemporal_store(__builtin_bit_cast(u32x2, w), gmem(reinterpret_cast<u32x2*>(to)));
-        } else {
+    }
+    if (nb + kLoraWaves * 64 < n1) request(nb + kLoraWaves * 64);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (o + j < n1) gmem(to)[j] = f32_to_bf16(y[i][j]);
+    for (int h = 0; h < 2; ++h) {
+      if (h == halves) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!has[h][i]) continue;
+        const int64_t at = (int64_t)row[h][i] * a.y_stride + o;
+        if (a.y32) {
+          float* to = a.y32 + at;
+          if (full) {
+            __builtin_nontemporal_store(__builtin_bit_cast(u32x4, y[h][i]), gmem(reinterpret_cast<u32x4*>(to)));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (o + j < n1) gmem(to)[j] = y[h][i][j];
+          }
+        }
+        if (a.y16) {
+          uint16_t* to = a.y16 + at;
+          if (full) {
+            const bf16x4 w = {(__bf16)y[h][i][0], (__bf16)y[h][i][1], (__bf16)y[h][i][2], (__bf16)y[h][i][3]};
+            __builtin_nontemporal_store(__builtin_bit_cast(u32x2, w), gmem(reinterpret_cast<u32x2*>(to)));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (o + j < n1) gmem(to)[j] = f32_to_bf16(y[h][i][j]);
+          }
         }
       }
     }
@@ -435,9 +479,9 @@ static int lora_launch(const char* name, LoraArgs a, hipStream_t s) {
   const int steps = (a.k + kLoraStep - 1) / kLoraStep;
   a.chunk = (steps + a.splits - 1) / a.splits * kLoraStep;
   hipLaunchKernelGGL((lora_shrink_kernel<RT>), dim3((unsigned)a.tiles, (unsigned)a.splits), dim3(kLoraThreads), lds, s, a);
-  // expand: 64 outputs per wave at a time, about 2048 workgroups in all
+  // expand: 64 outputs per wave at a time, about 1024 workgroups in all
   const int rows = (a.n + 63) / 64;
-  int64_t parts = (2048 + a.tiles - 1) / a.tiles;
+  int64_t parts = (1024 + a.tiles - 1) / a.tiles;
   const int64_t most = (rows + kLoraWaves - 1) / kLoraWaves;
   parts = parts < most ? parts : most;
   a.chunk = (int)((most + parts - 1) / parts) * kLoraWaves * 64;
