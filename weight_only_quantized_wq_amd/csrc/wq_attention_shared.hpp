@@ -60,7 +60,7 @@ struct AttnArgs {
 };
 
 // What a group costs besides its tiles, in tiles: queries in, results out.
-constexpr int kGroupCost = 2;
+constexpr int kGroupCost = 4;
 
 // The deal: per request its rows, length and the cost of all groups before it.
 struct Deal {
@@ -93,7 +93,7 @@ template <int ROWS, int TILE>
 __device__ __forceinline__ void deal(const AttnArgs& a, const Deal& d) {
   __shared__ int chunk_sum[kMaxRequests / kWave];
   const int n = a.b.requests, lane = lane_id(), wave = wave_id();
-  for (int base = wave * kWave; base < n; base += kAttnThreads) {
+  for (int base = wave * kWave; base < n; base += (int)blockDim.x) {
     const int r = base + lane;
     int cost = 0;
     if (r < n) {
@@ -118,7 +118,7 @@ __device__ __forceinline__ void deal(const AttnArgs& a, const Deal& d) {
     const int chunks = (n + kWave - 1) / kWave;
     const int sum = lane < chunks ? chunk_sum[lane] : 0;
     const int upto = wave_scan(sum);
-    for (int base = wave * kWave; base < n; base += kAttnThreads) {
+    for (int base = wave * kWave; base < n; base += (int)blockDim.x) {
       const int add = __shfl(upto - sum, base / kWave);
       if (base + lane < n) d.before[base + lane] += add;
     }

@@ -5,7 +5,7 @@
 // registers (global_load_lds: 64 lanes x 16 bytes to 1 KB of consecutive LDS),
 // STAGES of them under way before the first product and, across the borders of
 // pieces, one more requested into each buffer as it is done with.  Each wave
-// requests a quarter of every tile's rows and counts its own requests: before
+// requests its share of every tile's rows and counts its own requests: before
 // the barrier that opens a tile it waits until all but the (STAGES - 2) newest
 // tiles' requests are done.  (Ordinary loads and stores
 // in between only make that wait longer.)
@@ -17,9 +17,11 @@
 //
 // The waves share the tile in two ways, by the rows a launch can have per key
 // head:
-//   * WK = 1, blocks of 64 R rows: every wave owns 16 R rows from the first
+//   * WK = 1, blocks of 16 R W rows: every wave owns 16 R rows from the first
 //     position of a piece to the last and reads the whole tile; nothing is
-//     joined inside the workgroup.
+//     joined inside the workgroup.  Two workgroups of W = 4 waves share a CU, or
+//     one of 8 waves with R = 2, whose blocks of 256 rows pay half as much for
+//     each tile's way to LDS.
 //   * WK = 4, up to 16 rows: all waves have the same rows and take 32 positions
 //     of a tile of 128 each, so that a short context is a few steps long; they
 //     meet in LDS at the end of a piece.
@@ -35,23 +37,23 @@ namespace wq {
 // Shape of a launch: positions of a tile, buffers of the ring, workgroups per
 // CU.  The ring holds up to 64 KB (two workgroups share a CU's 160 KB) or 128 KB,
 // with room for the deal of 4096 requests (512 with WK = 4) behind it; a wave's
-// quarter of a tile must be whole requests of 1 KB.
-template <int D, int WK>
+// share of a tile must be whole requests of 1 KB.
+template <int D, int WK, int W>
 struct Shape {
-  static constexpr int TILE = WK == 4 ? 128 : D == 96 ? 64 : 32;
+  static constexpr int TILE = WK == 4 ? 128 : D == 96 || W == 8 ? 64 : 32;
   static constexpr int STAGES = WK == 4 ? 2 : D == 96 || D == 256 ? 3 : 4;
-  static constexpr int GROUPS = WK == 4 || D == 256 ? 1 : 2;
+  static constexpr int GROUPS = WK == 4 || W == 8 || D == 256 ? 1 : 2;
 };
 
 constexpr int kIdSlots = 8;           // page numbers: requested STAGES tiles before the tile's own requests
 
-template <int D, int WK>
+template <int D, int WK, int W>
 struct StreamLds {
-  using S = Shape<D, WK>;
+  using S = Shape<D, WK, W>;
   alignas(16) uint16_t k[S::STAGES][S::TILE][D];
   alignas(16) uint16_t v[S::STAGES][S::TILE][D];
-  alignas(16) uint32_t ids[kAttnWaves][kIdSlots][S::TILE / 4];
-  uint32_t live[S::STAGES][kAttnWaves];      // which of a wave's rows are in use and have a page
+  alignas(16) uint32_t ids[W][kIdSlots][S::TILE / W];
+  uint32_t live[S::STAGES][W];      // which of a wave's rows are in use and have a page
 };
 // Where the waves of WK = 4 meet.
 template <int D>
@@ -92,21 +94,21 @@ __device__ __forceinline__ void wait_requests() {
 }
 __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
 
-template <int D, int R, int WK, bool PAGE8>
-__global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attention_stream_kernel(AttnArgs a) {
-  using S = Shape<D, WK>;
+template <int D, int R, int WK, int W, bool PAGE8>
+__global__ __launch_bounds__(W * kWave, (Shape<D, WK, W>::GROUPS)) void attention_stream_kernel(AttnArgs a) {
+  using S = Shape<D, WK, W>;
   constexpr int TILE = S::TILE, STAGES = S::STAGES;
-  constexpr int ROWS = 16 * R * (kAttnWaves / WK);
+  constexpr int ROWS = 16 * R * (W / WK);
   constexpr int KS = D / 32, CW = D / 16, VW = CW / 2;
   constexpr int CH = D / 8;                              // 16-byte pieces of a row
-  constexpr int TR = TILE / kAttnWaves;                  // a wave's rows of a tile
+  constexpr int TR = TILE / W;                  // a wave's rows of a tile
   constexpr int NP = TR * CH / kWave;                    // its requests, each for keys and for values
   constexpr int STEPS = TILE / 32 / WK;
-  static_assert(NP * kWave == TR * CH && STEPS >= 1 && (WK == 1 || R == 1), "tile does not divide");
+  static_assert(NP * kWave == TR * CH && STEPS >= 1 && (WK == 1 || (R == 1 && W == WK)), "tile does not divide");
   static_assert(!PAGE8 || D != 96, "8 rows are no whole number of requests");
   extern __shared__ __align__(16) char lds[];
-  StreamLds<D, WK>& sh = *reinterpret_cast<StreamLds<D, WK>*>(lds);
-  constexpr int MEET = sizeof(StreamLds<D, WK>);
+  StreamLds<D, WK, W>& sh = *reinterpret_cast<StreamLds<D, WK, W>*>(lds);
+  constexpr int MEET = sizeof(StreamLds<D, WK, W>);
   MeetLds<D>& mt = *reinterpret_cast<MeetLds<D>*>(lds + MEET);
   const Deal d = deal_at(lds + MEET + (WK > 1 ? sizeof(MeetLds<D>) : 0), a.b.requests);
   deal<ROWS, TILE>(a, d);
@@ -290,28 +292,35 @@ __global__ __launch_bounds__(kAttnThreads, (Shape<D, WK>::GROUPS)) void attentio
           }
           live_step = __builtin_amdgcn_readfirstlane(live_step);
           const bool whole = live_step == ~0u && base + 32 <= p.length;
-          f32x4 s[R][2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint16_t* row = sh.k[stage][first + 8 * (c >> 2) + 4 * u + (c & 3)];
-            bf16x8 kf[KS];
-#pragma unroll
-            for (int i = 0; i < KS; ++i) kf[i] = *reinterpret_cast<const bf16x8*>(row + 8 * k_piece<D>(g * KS + i, c));
-#pragma unroll
-            for (int t = 0; t < R; ++t) {
-              f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int i = 0; i < KS; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], q[t][i], acc, 0, 0, 0);
-              s[t][u] = acc;
-            }
-          }
+          // all of the step's reads from LDS first, so that the products wait once
+          bf16x8 kf[2][KS];
           uint32_t vw[8][VW];
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint16_t* row = sh.k[stage][first + 8 * (c >> 2) + 4 * u + (c & 3)];
+              kf[u][i] = *reinterpret_cast<const bf16x8*>(row + 8 * k_piece<D>(g * KS + i, c));
+            }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const uint32_t* row = reinterpret_cast<const uint32_t*>(&sh.v[stage][first + 8 * g + e][c * CW]);
 #pragma unroll
             for (int i = 0; i < VW; ++i) vw[e][i] = row[i];
           }
+          if constexpr (R == 1) __builtin_amdgcn_sched_barrier(0);
+          f32x4 s[R][2];
+#pragma unroll
+          for (int t = 0; t < R; ++t)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) s[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int t = 0; t < R; ++t)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                s[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[u][i], q[t][i], s[t][u], 0, 0, 0);
           uint32_t sees[R] = {};
           if (!whole) {
             const int past = base + 8 * g - p.length;    // drafts behind the context

@@ -98,16 +98,22 @@ constexpr int64_t kAttnMade = 0x77715f6174746e31;
 // (with more than 512 requests the deal does not fit LDS beside its ring, nor
 // is there need to share a row tile), up to 64, more (head_dim 256: blocks of 64
 // for all, as its buffers and accumulators fill LDS and the registers).
-enum { kRows16 = 0, kRows64 = 1, kRows128 = 2 };
+enum { kRows16 = 0, kRows64 = 1, kRowsMany = 2 };
 
 static int attn_variant(int64_t requests, int group, int head_dim, int max_tokens) {
   const int rows = group * max_tokens;
   if (head_dim == 256) return kRows64;
-  return rows <= 16 && requests <= 512 ? kRows16 : rows <= 64 ? kRows64 : kRows128;
+  return rows <= 16 && requests <= 512 ? kRows16 : rows <= 64 ? kRows64 : kRowsMany;
 }
 
 // Workgroups of a launch: as many as are resident.
-static int attn_grid(int variant, int head_dim) { return variant == kRows16 || head_dim == 256 ? 256 : 512; }
+static int attn_grid(int variant, int head_dim) {
+  return variant == kRows16 || (variant == kRowsMany && head_dim != 96) || head_dim == 256 ? 256 : 512;
+}
+// Rows of a block.
+static int attn_rows(int variant, int head_dim) {
+  return variant == kRows16 ? 16 : variant == kRows64 ? 64 : head_dim == 96 ? 128 : 256;
+}
 
 // Positions of a share at least, and of a group that is not cut.
 constexpr int kLeastPositions = 256;
@@ -145,21 +151,22 @@ static int attn_check(const char* name, const wq_tree_attention& a) {
   return WQ_OK;
 }
 
-template <int D, int R, int WK>
+template <int D, int R, int WK, int W>
 static int attn_launch(const char* name, AttnArgs a, int grid, hipStream_t s) {
-  constexpr int ROWS = 16 * R * (kAttnWaves / WK);
-  constexpr int TILE = Shape<D, WK>::TILE;
+  constexpr int ROWS = 16 * R * (W / WK);
+  constexpr int TILE = Shape<D, WK, W>::TILE;
   const size_t deal = deal_bytes(a.b.requests);
-  const size_t lds = sizeof(StreamLds<D, WK>) + (WK > 1 ? sizeof(MeetLds<D>) : 0) + deal;
+  const size_t lds = sizeof(StreamLds<D, WK, W>) + (WK > 1 ? sizeof(MeetLds<D>) : 0) + deal;
   a.least = kLeastPositions / TILE;
   a.uncut = kUncutPositions / TILE;
   // lane offsets within 8 rows are 32-bit byte offsets
   const bool page8 = a.c.page_size % 8 == 0 && a.c.token_stride < (1u << 28);
   if constexpr (D != 96) {
-    if (page8) hipLaunchKernelGGL((attention_stream_kernel<D, R, WK, true>), dim3(grid), dim3(kAttnThreads), lds, s, a);
+    if (page8)
+      hipLaunchKernelGGL((attention_stream_kernel<D, R, WK, W, true>), dim3(grid), dim3(W * kWave), lds, s, a);
   }
   if (D == 96 || !page8)
-    hipLaunchKernelGGL((attention_stream_kernel<D, R, WK, false>), dim3(grid), dim3(kAttnThreads), lds, s, a);
+    hipLaunchKernelGGL((attention_stream_kernel<D, R, WK, W, false>), dim3(grid), dim3(W * kWave), lds, s, a);
   // a table that covers no more than an uncut group leaves nothing to join
   if ((int64_t)a.c.limit > kUncutPositions)
     hipLaunchKernelGGL((attention_join_kernel<D, ROWS, TILE>),
@@ -171,10 +178,10 @@ static int attn_launch(const char* name, AttnArgs a, int grid, hipStream_t s) {
 template <int D>
 static int attn_launch_d(const char* name, const AttnArgs& a, int variant, hipStream_t s) {
   const int grid = attn_grid(variant, D);
-  if (variant == kRows64) return attn_launch<D, 1, 1>(name, a, grid, s);
+  if (variant == kRows64) return attn_launch<D, 1, 1, 4>(name, a, grid, s);
   if constexpr (D <= 128) {
-    if (variant == kRows16) return attn_launch<D, 1, 4>(name, a, grid, s);
-    if (variant == kRows128) return attn_launch<D, 2, 1>(name, a, grid, s);
+    if (variant == kRows16) return attn_launch<D, 1, 4, 4>(name, a, grid, s);
+    if (variant == kRowsMany) return attn_launch<D, 2, 1, D == 96 ? 4 : 8>(name, a, grid, s);
   }
   return fail(WQ_ERR_SHAPE, "%s: no kernel for this plan", name);
 }
@@ -187,8 +194,7 @@ extern "C" int64_t wq_tree_attention_workspace_bytes(int64_t requests, int32_t h
                                                      int32_t head_dim, int32_t max_tokens) {
   if (requests < 0 || requests > kMaxRequests || !attn_dims_ok(heads, kv_heads, head_dim, max_tokens)) return 0;
   const int variant = attn_variant(requests, heads / kv_heads, head_dim, max_tokens);
-  const int rows = variant == kRows16 ? 16 : variant == kRows64 ? 64 : 128;
-  return (int64_t)attn_grid(variant, head_dim) * 2 * rows * (head_dim + 2) * 4;
+  return (int64_t)attn_grid(variant, head_dim) * 2 * attn_rows(variant, head_dim) * (head_dim + 2) * 4;
 }
 
 extern "C" int wq_tree_attention_prepare(const wq_tree_attention* a, void* workspace, int64_t workspace_bytes,
