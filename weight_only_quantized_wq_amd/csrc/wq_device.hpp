@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace wq {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -131,6 +133,22 @@ __device__ __forceinline__ int wave_scan(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast15 into rows 1 and 3
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast31 into rows 2 and 3
   return v;
+}
+
+// Wave-wide maximum (lanes a step does not reach see -inf).
+__device__ __forceinline__ float wave_max(float v) {
+  const auto step = [](float x, auto ctrl, auto rows) {
+    return fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp((int)0xFF800000, __float_as_int(x), decltype(ctrl)::value,
+                                                               decltype(rows)::value, 0xF, false)));
+  };
+  using std::integral_constant;
+  v = step(v, integral_constant<int, 0xB1>{}, integral_constant<int, 0xF>{});
+  v = step(v, integral_constant<int, 0x4E>{}, integral_constant<int, 0xF>{});
+  v = step(v, integral_constant<int, 0x141>{}, integral_constant<int, 0xF>{});
+  v = step(v, integral_constant<int, 0x140>{}, integral_constant<int, 0xF>{});
+  v = step(v, integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});
+  v = step(v, integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 // Wave-wide maximum of non-negative values (rows the broadcasts skip see 0).

@@ -4,10 +4,9 @@
 
 namespace wq {
 
-// Joins the parts of groups that shares cut.  A wave takes one row: lanes read
-// the parts' maxima and sums at once, then 16-byte pieces of the parts' rows,
-// as many parts side by side as fit the wave and 8 deep, independent of each
-// other.
+// Joins the parts of groups that shares cut.  A wave takes one row: 16-byte
+// pieces of the parts' rows, as many parts side by side as fit the wave and 8
+// deep, and meanwhile, a lane per part, their maxima and sums.
 template <int D, int ROWS, int TILE>
 __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttnArgs a, int grid) {
   constexpr int LP = D / 4 <= 16 ? 16 : D / 4 <= 32 ? 32 : 64;    // lanes per part
@@ -43,29 +42,32 @@ __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttnArgs a
   const bool has = piece * 4 < D;
   float top = -INFINITY, sum = 0.f;
   f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int base = s0; base <= s1; base += kWave) {
-    const int count = min(kWave, s1 - base + 1);
+  const int last = s1 - s0;
+  f32x4 x[BATCH];
+  const auto request = [&](int from) {
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const float* part = part_of(s0 + min(from + b * SIDE + side, last)) + in * D + piece * 4;
+      x[b] = has ? *gmem(reinterpret_cast<const f32x4*>(part)) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+  for (int base = 0; base <= last; base += kWave) {
     float m = -INFINITY, l = 0.f;
-    if (lane < count) {
-      const float* part = part_of(base + lane);
+    if (base + lane <= last) {
+      const float* part = part_of(s0 + base + lane);
       m = gmem(part)[ROWS * D + in];
       l = gmem(part)[ROWS * (D + 1) + in];
     }
-    float now = m;
-    for (int s = 1; s < kWave; s <<= 1) now = fmaxf(now, __shfl_xor(now, s));
-    now = fmaxf(now, top);
+    request(base);
+    const float now = fmaxf(wave_max(m), top);
     const float ref = now == -INFINITY ? 0.f : now;
     const float fo = __builtin_amdgcn_exp2f(top - ref), f = __builtin_amdgcn_exp2f(m - ref);
     top = now;
     sum = sum * fo + wave_sum(l * f);
     o *= fo;
+    const int count = min(kWave, last - base + 1);
     for (int i = 0; i < count; i += BATCH * SIDE) {
-      f32x4 x[BATCH];
-#pragma unroll
-      for (int b = 0; b < BATCH; ++b) {
-        const float* part = part_of(base + min(i + b * SIDE + side, count - 1)) + in * D + piece * 4;
-        x[b] = has ? *gmem(reinterpret_cast<const f32x4*>(part)) : f32x4{0.f, 0.f, 0.f, 0.f};
-      }
+      if (i) request(base + i);
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
         const int s = i + b * SIDE + side;
