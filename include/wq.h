@@ -406,7 +406,8 @@ int wq_moe_step_run(const wq_moe_plan* plan, void* stream);
  *   one head contiguous; table int32 [requests][table_stride].
  * 1 <= page_size, table_width * page_size <= 2^30, strides below 2^32, 1 <= kv_heads <= 1024,
  * head_dim a multiple of 8 up to 256 (wq_tree_attention: 64, 96, 128, 256).
- * Two positions in use must not share a cache row.
+ * Requests may share pages that no call writes; a row that a call writes must
+ * be one position only.
  */
 typedef struct {
   uint16_t* k;
@@ -504,7 +505,7 @@ typedef struct {
 typedef struct {
   int64_t made;        /* set by prepare */
   int32_t device;
-  int32_t split;
+  int32_t reserved;
   wq_qkv_rope a;
 } wq_qkv_rope_plan;
 

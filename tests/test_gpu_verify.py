@@ -812,3 +812,144 @@ def test_two_adapter_plans_on_two_streams(wq):
             wq.wq_lora_run(two, t)
         torch.cuda.synchronize()
         assert torch.equal(y, wy) and torch.equal(z, wz)
+
+
+# --- further shapes ----------------------------------------------------------
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+@pytest.mark.parametrize("heads,n", [(4, 2), (16, 30)])
+def test_attention_scales(wq, scale, heads, n):
+    # a negative scale turns the order round, a zero one leaves the mean
+    rng = np.random.default_rng(100)
+    p = Attn(rng, [200, 3], [n, n], heads, 2, 64, 16, scale=scale, tree=lambda m: random_tree(rng, m))
+    run(wq, p)
+    p.check()
+
+
+@pytest.mark.parametrize("requests", [65, 130, 600])
+@pytest.mark.parametrize("heads", [2, 40])
+def test_attention_many_requests(wq, requests, heads):
+    rng = np.random.default_rng(requests)
+    lengths = [int(rng.integers(0, 40)) for _ in range(requests)]
+    lengths[requests // 2] = 1500
+    counts = [int(rng.integers(0, 3)) for _ in range(requests)]
+    counts[requests // 2] = 2
+    p = Attn(rng, lengths, counts, heads, 2, 64, 16, pad_rows=1)
+    run(wq, p)
+    p.check()
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("page", [16, 11, 24])
+def test_attention_wide_trees(wq, dim, page):
+    rng = np.random.default_rng(dim + page)
+    p = Attn(rng, [700, 0, 129], [64, 40, 1], 16, 2, dim, page, tree=lambda m: random_tree(rng, m))
+    run(wq, p)
+    p.check()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("heads,dim,page", [(4, 128, 16), (16, 128, 16), (64, 64, 16), (16, 96, 16), (8, 256, 16), (16, 128, 9)])
+def test_attention_unseen_specials_in_every_kernel(wq, bad, heads, dim, page):
+    """Draft 2 holds infinities or NaN that only its own row sees; 1200 positions cut the groups."""
+    import torch
+    rng = np.random.default_rng(dim + heads)
+    p = Attn(rng, [1200], [6], heads, 2, dim, page, tree=lambda n: [1, 3, 5, 9, 27, 33])
+    run(wq, p)
+    clean = p.y.clone()
+    at = int(p.table[0, 1202 // page]), 1202 % page
+    p.k[at], p.v[at] = bad, bad
+    p.y.fill_(7.0)
+    run(wq, p)
+    same = [0, 1, 3, 4, 5]
+    assert torch.equal(p.y[same], clean[same])
+    assert not torch.isfinite(p.y[2]).any()
+
+
+def test_attention_shares_pages_between_requests(wq):
+    rng = np.random.default_rng(101)
+    p = Attn(rng, [160, 160], [2, 2], 4, 2, 64, 16)
+    p.table[1, :10] = p.table[0, :10]        # a common prefix
+    run(wq, p)
+    p.check()
+
+
+def test_attention_capture_with_a_workspace_of_its_own(wq):
+    """A captured run and eager runs of another plan between its replays."""
+    import torch
+    rng = np.random.default_rng(102)
+    a, b = Attn(rng, [3000], [5], 8, 2, 128, 16), Attn(rng, [2000, 40], [3, 8], 16, 2, 64, 16)
+    need = wq.wq_tree_attention_workspace_bytes(1, 8, 2, 128, 5)
+    pa = a.plan(wq, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    pb = b.plan(wq)
+    wq.wq_tree_attention_run(pa)
+    torch.cuda.synchronize()
+    first = a.y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        wq.wq_tree_attention_run(pa)
+    for _ in range(4):
+        a.y.fill_(7.0)
+        graph.replay()
+        wq.wq_tree_attention_run(pb)
+        torch.cuda.synchronize()
+        assert torch.equal(a.y, first)
+        b.check()
+
+
+def test_a_plan_of_another_device_is_refused(wq):
+    rng = np.random.default_rng(103)
+    p = Attn(rng, [20], [2], 2, 2, 64, 16)
+    plan = p.plan(wq)
+    plan.device = 7                          # as if prepared on device 7
+    with pytest.raises(wq.WQError, match="DEVICE"):
+        wq.wq_tree_attention_run(plan, stream=0)
+    with pytest.raises(wq.WQError, match="SHAPE"):
+        wq.wq_tree_attention_prepare(p.q, p.k, p.v, i32(p.table), i32(p.starts), i32(p.lengths), p.q)
+
+
+def test_rope_rows_of_no_request_and_queries_in_wide_rows(wq):
+    import torch
+    rng = np.random.default_rng(104)
+    k = torch.full((3, 16, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide = torch.full((5, 4 * 64 + 40), 7.0, dtype=torch.bfloat16, device="cuda")
+    raw = torch.randn(5, 8 * 64 + 16, device="cuda")
+    plan = wq.wq_qkv_rope_prepare(raw[:, 4:4 + 512], wide[:, 16:272], k, k.clone(), i32([[1, 2]]), i32([1, 4]), i32([3]))
+    wq.wq_qkv_rope_run(plan)
+    torch.cuda.synchronize()
+    assert torch.equal(wide[1:4, 16:272], raw[1:4, 4:260].to(torch.bfloat16))
+    assert torch.all(wide[0] == 7.0) and torch.all(wide[4] == 7.0)
+    assert torch.all(wide[:, :16] == 7.0) and torch.all(wide[:, 272:] == 7.0)
+    want = torch.full_like(k, 7.0)
+    want[1, 3:6] = raw[1:4, 260:388].to(torch.bfloat16).view(3, 2, 64)
+    assert torch.equal(k, want)
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 17, 31, 32, 33])
+@pytest.mark.parametrize("rank,k", [(8, 64), (16, 1024), (16, 2048), (32, 1024), (16, 2056), (32, 4096)])
+def test_lora_one_launch_and_two(wq, tokens, rank, k):
+    # both sides of the rule that chooses one launch: 32 rows, rank * k of 32768
+    rng = np.random.default_rng(tokens * rank + k)
+    lora_case(wq, rng, rng.integers(-1, 5, tokens), 5, rank, k, 600, out=("f32", "bf16"), pad=1, ranks=[rank, 3, 8, 0, 99])
+
+
+def test_lora_graph_follows_changed_adapters(wq):
+    import torch
+    rng = np.random.default_rng(105)
+    for rank, k in ((16, 512), (32, 4096)):
+        plan, (y, _) = lora_case(wq, rng, [0, 1, 2, 0, -1, 2, 1], 3, rank, k, 900)
+        adapter = plan.keep[3]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            wq.wq_lora_run(plan)
+        for _ in range(4):
+            adapter.copy_(i32(rng.integers(-1, 3, 7)))
+            y.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            got = y.clone()
+            y.zero_()
+            wq.wq_lora_run(plan)
+            torch.cuda.synchronize()
+            assert torch.equal(got, y)

@@ -117,7 +117,7 @@ def test_batch(call, kw, rc):
     ("attention", dict(heads=0), 2), ("attention", dict(heads=130), 2), ("attention", dict(max_tokens=0), 2),
     ("attention", dict(max_tokens=65), 2), ("attention", dict(cache=cache(head_dim=72)), 2),
     ("attention", dict(q_stride=248), 2), ("attention", dict(y_stride=252), 2),
-    ("attention", dict(scale=float("nan")), 2), ("attention", dict(y=OK, tree=BAD), 3),
+    ("attention", dict(scale=float("nan")), 2), ("attention", dict(y=OK), 2), ("attention", dict(y=0x3000, tree=BAD), 3),
     ("accept", dict(lengths=None), 1), ("accept", dict(path=None), 1), ("accept", dict(accepted=None), 1),
     ("accept", dict(layers=0), 2), ("accept", dict(layers=4097), 2), ("accept", dict(layer_stride=4), 2),
     ("accept", dict(requests=4097), 2), ("accept", dict(path_width=0), 2), ("accept", dict(path_width=65, path_stride=65), 2),
@@ -145,7 +145,7 @@ def test_null_descriptions_and_foreign_plans():
 
 
 def test_workspace_sizes():
-    d, p = attention(y=OK), wq.wq_tree_attention_plan()
+    d, p = attention(y=0x3000), wq.wq_tree_attention_plan()
     need = wq.wq_tree_attention_workspace_bytes(2, 4, 2, 64, 5)
     assert need > 0
     assert lib.wq_tree_attention_prepare(ctypes.byref(d), OK, need - 1, ctypes.byref(p)) == 2

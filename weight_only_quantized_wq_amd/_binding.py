@@ -97,7 +97,7 @@ class wq_lora(ctypes.Structure):
 # Plans: ctypes instances take further attributes, and `keep` holds the tensors
 # a plan's addresses point into for as long as the plan lives.
 class wq_qkv_rope_plan(ctypes.Structure):
-    _fields_ = [("made", _I64), ("device", _I32), ("split", _I32), ("a", wq_qkv_rope)]
+    _fields_ = [("made", _I64), ("device", _I32), ("reserved", _I32), ("a", wq_qkv_rope)]
 
 
 class wq_tree_attention_plan(ctypes.Structure):
@@ -416,7 +416,8 @@ def wq_moe_step_run(plan, stream=None):
 # ---------------------------------------------------------------------------
 # Between the linears of a verify pass, and the adapters beside them.  Sizes
 # and strides are read off the tensors; each *_prepare returns a plan that
-# keeps its tensors alive, each *_run enqueues it.
+# keeps its tensors alive, each *_run enqueues it.  Keep a plan (and with it its
+# workspace) until its runs on every stream are done.
 
 
 def _view(t, what, dims, dtypes, device, unit=True):

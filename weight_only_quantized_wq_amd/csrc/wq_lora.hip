@@ -11,10 +11,16 @@
 //      the second launch.  The tile's rows are left in the workspace for it.
 //   2. lora_expand_kernel: adds the shares in order, scales, splits h into
 //      bf16 parts -- three for fp32 results (together all 24 bits, so that only
-//      fp32 sums round), two for bf16 ones (16 bits) -- and multiplies 64 rows of B at a time with them; base is added and the
-//      result stored from the accumulators.
-// Weights are read once per tile; with few rows per adapter both launches are
-// bound by them, with many by base and y, and with one row by launch latency.
+//      fp32 sums round), two for bf16 ones (16 bits) -- and multiplies 64 rows
+//      of B at a time with them; base is added and the result stored from the
+//      accumulators.
+// lora_one_kernel does both for few rows and a small A.
+//
+// Weights are read once per tile.  Measured (MI355X): 32 x 5 rows of 28 adapters,
+// rank 32, k = 8192, n = 10240: 19.6 us, 43 MB, of which the two launches' own
+// cost is about 5; 8 x 128 rows of 4 adapters, rank 64, k = 4096, n = 22016: 59 us,
+// 157 MB, bound by the latency of base and B under the registers' two waves per
+// SIMD (without base 44 us, without B 50, without stores 50); one row: launches.
 #include <math.h>
 
 #include "wq_kv.hpp"
@@ -184,18 +190,12 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
   return a.ranks ? min(max(gmem(a.ranks)[adapter], 0), a.rank) : a.rank;
 }
 
-template <int RT>
-__global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
-  extern __shared__ __align__(16) char lds[];
-  __shared__ TileRows tile;
-  __shared__ float sum[kLoraWaves][RT * 16][17];
-  find_tile(a, (int)blockIdx.x, lds, tile);
-  if (blockIdx.y == 0 && threadIdx.x < sizeof(TileRows) / 4)
-    gmem(reinterpret_cast<int32_t*>(a.found + blockIdx.x))[threadIdx.x] = reinterpret_cast<const int32_t*>(&tile)[threadIdx.x];
-  if (tile.rows == 0 || tile.adapter == a.adapters) return;
+// h = A x of a tile over inputs [k0, k1), this wave's steps of it (every W-th):
+// acc[half][r] holds ranks 16 r + 4 g + i of token row 16 half + c.
+template <int RT, int W>
+__device__ __forceinline__ void shrink_products(const LoraArgs& a, const TileRows& tile, int rank, int k0, int k1,
+                                                f32x4 (&acc)[2][RT]) {
   const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
-  const int rank = rank_of(a, tile.adapter);
-  const int k0 = (int)blockIdx.y * a.chunk, k1 = min(k0 + a.chunk, a.k);
   const int halves = tile.rows > 16 ? 2 : 1;
   const uint16_t* xp[2];
   bool has[2];
@@ -205,13 +205,12 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
     xp[h] = a.x + (int64_t)tile.row[has[h] ? 16 * h + c : 0] * a.x_stride;
   }
   const uint16_t* ap = a.a + (int64_t)tile.adapter * a.rank * a.k;
-  f32x4 acc[2][RT];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[h][r] = f32x4{0.f, 0.f, 0.f, 0.f};
   // of each 32 inputs lane group g takes 8: a row's 64 bytes are one run
-  for (int kb = k0 + wave * kLoraStep; kb < k1; kb += kLoraWaves * kLoraStep) {
+  for (int kb = k0 + wave * kLoraStep; kb < k1; kb += W * kLoraStep) {
     u32x4 xv[2][4], av[RT][4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -243,62 +242,104 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
                                                               __builtin_bit_cast(bf16x8, xv[h][s]), acc[h][r], 0, 0, 0);
     }
   }
-  float* out = a.part + ((int64_t)blockIdx.y * a.tiles + blockIdx.x) * (kLoraRows * RT * 16);
+}
+
+// The waves' sums of one half added up in wave order: use(t, j, sum) for token
+// row t of the half and rank j, shared out over the workgroup.
+template <int RT, int W, class Use>
+__device__ __forceinline__ void shrink_sums(float (&sum)[W][RT * 16][17], const f32x4 (&acc)[RT], Use use) {
+  const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (h == halves) break;
-    if (h) __syncthreads();
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int i = 0; i < 4; ++i) sum[wave][16 * r + 4 * g + i][c] = acc[r][i];
+  __syncthreads();
+  for (int i = (int)threadIdx.x; i < 16 * RT * 16; i += W * kWave) {
+    const int t = i / (RT * 16), j = i % (RT * 16);
+    float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[wave][16 * r + 4 * g + i][c] = acc[h][r][i];
-    __syncthreads();
-    for (int i = (int)threadIdx.x; i < 16 * RT * 16; i += kLoraThreads) {
-      const int t = i / (RT * 16), j = i % (RT * 16);
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kLoraWaves; ++w) v += sum[w][j][t];
-      gmem(out)[h * 16 * RT * 16 + i] = v;
-    }
+    for (int w = 0; w < W; ++w) v += sum[w][j][t];
+    use(t, j, v);
   }
 }
 
-// B rows of 64 outputs go to four products of 16, output 4 c + j of the 64 to
-// column c of product j: lane (g, c) ends with four consecutive outputs of each
-// of the token rows 4 g .. 4 g + 3 of a half, and the 16 lanes of a row read base
-// and write y in one contiguous run.  What bounds it is the latency of those
-// reads, so 32 rows share the weights of 64 outputs: twice the bytes of base in
-// flight for the same weights.
+template <int RT>
+__global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  __shared__ TileRows tile;
+  __shared__ float sum[kLoraWaves][RT * 16][17];
+  find_tile(a, (int)blockIdx.x, lds, tile);
+  if (blockIdx.y == 0 && threadIdx.x < sizeof(TileRows) / 4)
+    gmem(reinterpret_cast<int32_t*>(a.found + blockIdx.x))[threadIdx.x] = reinterpret_cast<const int32_t*>(&tile)[threadIdx.x];
+  if (tile.rows == 0 || tile.adapter == a.adapters) return;
+  const int rank = rank_of(a, tile.adapter);
+  const int k0 = (int)blockIdx.y * a.chunk, k1 = min(k0 + a.chunk, a.k);
+  f32x4 acc[2][RT];
+  shrink_products<RT, kLoraWaves>(a, tile, rank, k0, k1, acc);
+  float* out = a.part + ((int64_t)blockIdx.y * a.tiles + blockIdx.x) * (kLoraRows * RT * 16);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h && tile.rows <= 16) break;
+    if (h) __syncthreads();
+    shrink_sums<RT, kLoraWaves>(sum, acc[h], [&](int t, int j, float v) { gmem(out)[(h * 16 + t) * (RT * 16) + j] = v; });
+  }
+}
+
+// h as the second product takes it: [half][product of 32 ranks][part][lane][8].
 template <int RT, int PARTS>
-__global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
-  constexpr int KS = (RT + 1) / 2;          // products of 32 ranks
-  constexpr int R16 = RT * 16;
-  // h as the products take it: [half][product][part][lane][8]
-  __shared__ __align__(16) __bf16 hs[2][KS][PARTS][kWave][8];
-  const auto* tile = gmem(a.found + blockIdx.x);
-  const int rows = tile->rows, adapter = tile->adapter;
-  if (rows == 0) return;
-  const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
-  const bool bare = adapter == a.adapters;
-  const int rank = bare ? 0 : rank_of(a, adapter);
-  const uint16_t* bp = a.b + (int64_t)(bare ? 0 : adapter) * a.n * a.rank;
-  const int halves = rows > 16 ? 2 : 1;
+struct SplitH {
+  static constexpr int KS = (RT + 1) / 2;
+  __bf16 at[2][KS][PARTS][kWave][8];
+  // Rank j of token row t, as PARTS bf16 parts.
+  __device__ __forceinline__ void put(int t, int j, float v) {
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) {
+      const __bf16 part = (__bf16)v;
+      at[t >> 4][j >> 5][q][(j >> 3 & 3) * 16 + (t & 15)][j & 7] = part;
+      v -= (float)part;
+    }
+  }
+};
+
+// y of a tile's rows, outputs [n0, n1).  B rows of 64 outputs go to four products
+// of 16, output 4 c + j of the 64 to column c of product j: lane (g, c) ends with
+// four consecutive outputs of each of the token rows 4 g .. 4 g + 3 of a half, and
+// the 16 lanes of a row read base and write y in one contiguous run.  What
+// bounds it is the latency of those reads, so 32 rows share the weights of 64
+// outputs: twice the bytes of base in flight for the same weights.
+template <int RT, int PARTS, int W>
+struct Expand {
+  static constexpr int KS = (RT + 1) / 2;
+  const LoraArgs& a;
+  const uint16_t* bp;
+  int rank, halves, n1, nb;
+  bool bare;
   int row[2][4];
   bool has[2][4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      has[h][i] = 16 * h + 4 * g + i < rows;
-      row[h][i] = tile->row[has[h][i] ? 16 * h + 4 * g + i : 0];
-    }
-  const int n0 = (int)blockIdx.y * a.chunk, n1 = min(n0 + a.chunk, a.n);
-
   u32x4 bv[4][KS];
   f32x4 v[2][4];
-  // weights and base of outputs nb .. nb + 63, all requested before any is used
-  const auto request = [&](int nb) {
-    const int o = nb + 4 * c;
+
+  template <class T>
+  __device__ __forceinline__ Expand(const LoraArgs& args, const T& tile, int rank_, int n0, int n1_)
+      : a(args), rank(rank_), n1(n1_) {
+    const int lane = lane_id(), g = lane >> 4;
+    bare = tile.adapter == a.adapters;
+    bp = a.b + (int64_t)(bare ? 0 : tile.adapter) * a.n * a.rank;
+    halves = tile.rows > 16 ? 2 : 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        has[h][i] = 16 * h + 4 * g + i < tile.rows;
+        row[h][i] = tile.row[has[h][i] ? 16 * h + 4 * g + i : 0];
+      }
+    nb = n0 + wave_id() * 64;
+    if (nb < n1) request(nb);
+  }
+
+  // Weights and base of outputs first .. first + 63, all requested before any is used.
+  __device__ __forceinline__ void request(int first) {
+    const int lane = lane_id(), g = lane >> 4, c = lane & 15, o = first + 4 * c;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -323,104 +364,149 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
       for (int s = 0; s < KS; ++s)
         bv[j][s] = !bare && o + j < n1 && s * 32 + g * 8 < a.rank ? load16(bp + (int64_t)(o + j) * a.rank + s * 32 + g * 8)
                                                                 : u32x4{0, 0, 0, 0};
-  };
-  int nb = n0 + wave * 64;
-  if (nb < n1) request(nb);
-
-  const float scale = bare || !a.scale ? 1.f : gmem(a.scale)[adapter];
-  for (int i = (int)threadIdx.x; i < halves * 16 * KS * 32; i += kLoraThreads) {
-    const int tr = i / (KS * 32), j = i % (KS * 32);
-    float sum = 0.f;
-    if (j < R16 && tr < rows && !bare) {
-      const float* from = a.part + (int64_t)blockIdx.x * (kLoraRows * R16) + tr * R16 + j;
-      const int64_t stride = (int64_t)a.tiles * (kLoraRows * R16);
-      for (int s = 0; s < a.splits; s += 8) {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = gmem(from)[min(s + e, a.splits - 1) * stride];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += s + e < a.splits ? x[e] : 0.f;
-      }
-    }
-    float left = j < rank ? sum * scale : 0.f;
-#pragma unroll
-    for (int q = 0; q < PARTS; ++q) {
-      const __bf16 part = (__bf16)left;
-      hs[tr >> 4][j >> 5][q][(j >> 3 & 3) * 16 + (tr & 15)][j & 7] = part;
-      left -= (float)part;
-    }
   }
-  __syncthreads();
-  for (; nb < n1; nb += kLoraWaves * 64) {
-    if (rank < a.rank) {
-      // columns of B past the adapter's own rank do not count
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int left = rank - (s * 32 + g * 8 + 2 * i);
-          const uint32_t keep = left <= 0 ? 0u : left == 1 ? 0xFFFFu : ~0u;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) bv[j][s][i] &= keep;
-        }
-    }
-    const int o = nb + 4 * c;
-    const bool full = a.vec && o + 4 <= n1;
-    f32x4 y[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == halves) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[h][i] = v[h][i];
-      bf16x8 hv[KS][PARTS];
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q) hv[s][q] = *reinterpret_cast<const bf16x8*>(hs[h][s][q][lane]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  __device__ __forceinline__ void run(const SplitH<RT, PARTS>& hs) {
+    const int lane = lane_id(), g = lane >> 4, c = lane & 15;
+    for (; nb < n1; nb += W * 64) {
+      if (rank < a.rank) {
+        // columns of B past the adapter's own rank do not count
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int q = 0; q < PARTS; ++q)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv[s][q], __builtin_bit_cast(bf16x8, bv[j][s]), acc, 0, 0, 0);
+          for (int i = 0; i < 4; ++i) {
+            const int left = rank - (s * 32 + g * 8 + 2 * i);
+            const uint32_t keep = left <= 0 ? 0u : left == 1 ? 0xFFFFu : ~0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[h][i][j] += acc[i];
-      }
-    }
-    if (nb + kLoraWaves * 64 < n1) request(nb + kLoraWaves * 64);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == halves) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!has[h][i]) continue;
-        const int64_t at = (int64_t)row[h][i] * a.y_stride + o;
-        if (a.y32) {
-          float* to = a.y32 + at;
-          if (full) {
-            __builtin_nontemporal_store(__builtin_bit_cast(u32x4, y[h][i]), gmem(reinterpret_cast<u32x4*>(to)));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (o + j < n1) gmem(to)[j] = y[h][i][j];
+            for (int j = 0; j < 4; ++j) bv[j][s][i] &= keep;
           }
-        }
-        if (a.y16) {
-          uint16_t* to = a.y16 + at;
-          if (full) {
-            const bf16x4 w = {(__bf16)y[h][i][0], (__bf16)y[h][i][1], (__bf16)y[h][i][2], (__bf16)y[h][i][3]};
-            __builtin_nontemporal_store(__builtin_bit_cast(u32x2, w), gmem(reinterpret_cast<u32x2*>(to)));
-          } else {
+      }
+      const int o = nb + 4 * c;
+      const bool full = a.vec && o + 4 <= n1;
+      f32x4 y[2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (o + j < n1) gmem(to)[j] = f32_to_bf16(y[h][i][j]);
+      for (int h = 0; h < 2; ++h) {
+        if (h == halves) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[h][i] = v[h][i];
+        if (bare) continue;
+        bf16x8 hv[KS][PARTS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q) hv[s][q] = *reinterpret_cast<const bf16x8*>(hs.at[h][s][q][lane]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+              acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hv[s][q], __builtin_bit_cast(bf16x8, bv[j][s]), acc, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[h][i][j] += acc[i];
+        }
+      }
+      if (nb + W * 64 < n1) request(nb + W * 64);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == halves) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!has[h][i]) continue;
+          const int64_t at = (int64_t)row[h][i] * a.y_stride + o;
+          if (a.y32) {
+            float* to = a.y32 + at;
+            if (full) {
+              __builtin_nontemporal_store(__builtin_bit_cast(u32x4, y[h][i]), gmem(reinterpret_cast<u32x4*>(to)));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (o + j < n1) gmem(to)[j] = y[h][i][j];
+            }
+          }
+          if (a.y16) {
+            uint16_t* to = a.y16 + at;
+            if (full) {
+              const bf16x4 w = {(__bf16)y[h][i][0], (__bf16)y[h][i][1], (__bf16)y[h][i][2], (__bf16)y[h][i][3]};
+              __builtin_nontemporal_store(__builtin_bit_cast(u32x2, w), gmem(reinterpret_cast<u32x2*>(to)));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (o + j < n1) gmem(to)[j] = f32_to_bf16(y[h][i][j]);
+            }
           }
         }
       }
     }
   }
+};
+
+template <int RT, int PARTS>
+__global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
+  constexpr int KS = (RT + 1) / 2;          // products of 32 ranks
+  constexpr int R16 = RT * 16;
+  __shared__ __align__(16) SplitH<RT, PARTS> hs;
+  const auto& tile = *gmem(a.found + blockIdx.x);
+  const int rows = tile.rows, adapter = tile.adapter;
+  if (rows == 0) return;
+  const bool bare = adapter == a.adapters;
+  const int rank = bare ? a.rank : rank_of(a, adapter);
+  const int n0 = (int)blockIdx.y * a.chunk, n1 = min(n0 + a.chunk, a.n);
+  Expand<RT, PARTS, kLoraWaves> expand(a, tile, rank, n0, n1);
+  if (!bare) {
+    const float scale = a.scale ? gmem(a.scale)[adapter] : 1.f;
+    for (int i = (int)threadIdx.x; i < expand.halves * 16 * KS * 32; i += kLoraThreads) {
+      const int t = i / (KS * 32), j = i % (KS * 32);
+      float sum = 0.f;
+      if (j < R16 && t < rows) {
+        const float* from = a.part + (int64_t)blockIdx.x * (kLoraRows * R16) + t * R16 + j;
+        const int64_t stride = (int64_t)a.tiles * (kLoraRows * R16);
+        for (int s = 0; s < a.splits; s += 8) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = gmem(from)[min(s + e, a.splits - 1) * stride];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum += s + e < a.splits ? x[e] : 0.f;
+        }
+      }
+      hs.put(t, j, j < rank ? sum * scale : 0.f);
+    }
+  }
+  __syncthreads();
+  expand.run(hs);
+}
+
+// Both steps in one launch, for few rows and a small A: every workgroup of a tile
+// computes the whole h again (from L2) rather than wait for a second launch.
+constexpr int kOneWaves = 8;
+template <int RT, int PARTS>
+__global__ __launch_bounds__(kOneWaves * kWave) void lora_one_kernel(LoraArgs a) {
+  __shared__ TileRows tile;
+  __shared__ float sum[kOneWaves][RT * 16][17];
+  __shared__ __align__(16) SplitH<RT, PARTS> hs;
+  find_tile(a, (int)blockIdx.x, nullptr, tile);
+  if (tile.rows == 0) return;
+  const bool bare = tile.adapter == a.adapters;
+  const int rank = bare ? a.rank : rank_of(a, tile.adapter);
+  const int n0 = (int)blockIdx.y * a.chunk, n1 = min(n0 + a.chunk, a.n);
+  Expand<RT, PARTS, kOneWaves> expand(a, tile, rank, n0, n1);
+  if (!bare) {
+    const float scale = a.scale ? gmem(a.scale)[tile.adapter] : 1.f;
+    f32x4 acc[2][RT];
+    shrink_products<RT, kOneWaves>(a, tile, rank, 0, a.k, acc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h && tile.rows <= 16) break;
+      if (h) __syncthreads();
+      shrink_sums<RT, kOneWaves>(sum, acc[h], [&](int t, int j, float v) {
+        hs.put(h * 16 + t, j, j < rank ? v * scale : 0.f);
+        if (RT == 1) hs.put(h * 16 + t, 16 + j, 0.f);
+      });
+    }
+  }
+  __syncthreads();
+  expand.run(hs);
 }
 
 // ---------------------------------------------------------------------------
@@ -446,6 +532,12 @@ static int lora_splits(int tiles, int64_t k) {
   const int64_t want = (1024 + tiles - 1) / tiles;
   return (int)(want < most ? want : most);
 }
+
+// One launch instead of two: up to 32 rows, and an A of up to 64 KB, which a
+// workgroup reads in less time than a second launch takes.  Measured, one / two
+// launches, rank 16, n = 4096: one row k = 1024 5.4 / 7.3 us, k = 2048 6.6 / 7.4,
+// k = 4096 8.7 / 7.6; 32 rows of 32 adapters k = 1024 7.5 / 9.1.
+static bool lora_in_one(int64_t tokens, int64_t k, int32_t rank) { return tokens <= kLoraRows && rank <= 32 && rank * k <= 32768; }
 
 static int rank16(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
@@ -475,6 +567,21 @@ static int lora_check(const char* name, const wq_lora& a) {
 
 template <int RT>
 static int lora_launch(const char* name, LoraArgs a, hipStream_t s) {
+  if constexpr (RT <= 2) {
+    if (lora_in_one(a.tokens, a.k, a.rank)) {
+      // 64 outputs per wave at a time, about 256 workgroups in all
+      const int most = (a.n + kOneWaves * 64 - 1) / (kOneWaves * 64);
+      int parts = 256 / a.tiles;
+      parts = parts < 1 ? 1 : parts < most ? parts : most;
+      a.chunk = (most + parts - 1) / parts * kOneWaves * 64;
+      const dim3 grid((unsigned)a.tiles, (unsigned)((a.n + a.chunk - 1) / a.chunk));
+      if (a.y32)
+        hipLaunchKernelGGL((lora_one_kernel<RT, 3>), grid, dim3(kOneWaves * kWave), 0, s, a);
+      else
+        hipLaunchKernelGGL((lora_one_kernel<RT, 2>), grid, dim3(kOneWaves * kWave), 0, s, a);
+      return launch_status(name);
+    }
+  }
   const size_t lds = search_bytes(a.tokens, a.adapters);
   const int steps = (a.k + kLoraStep - 1) / kLoraStep;
   a.chunk = (steps + a.splits - 1) / a.splits * kLoraStep;

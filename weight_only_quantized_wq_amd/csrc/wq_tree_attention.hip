@@ -142,6 +142,7 @@ static int attn_check(const char* name, const wq_tree_attention& a) {
     return fail(WQ_ERR_SHAPE, "%s: q_stride = %lld, y_stride = %lld must be multiples of 8 and hold a row", name,
                 (long long)a.q_stride, (long long)a.y_stride);
   if (!(fabsf(a.scale) < INFINITY)) return fail(WQ_ERR_SHAPE, "%s: scale must be finite", name);
+  if (a.q == a.y && a.batch.tokens > 0) return fail(WQ_ERR_SHAPE, "%s: y must not be q", name);
   const int64_t blocks = ((int64_t)(a.heads / a.cache.kv_heads) * a.max_tokens + 63) / 64;
   const int64_t tiles = (a.cache.table_width * a.cache.page_size + a.max_tokens) / 32 + 2;
   if (a.batch.requests * a.cache.kv_heads * blocks * tiles > 0x7FFFFFFF)
