@@ -953,3 +953,16 @@ def test_lora_graph_follows_changed_adapters(wq):
             wq.wq_lora_run(plan)
             torch.cuda.synchronize()
             assert torch.equal(got, y)
+
+
+@pytest.mark.parametrize("dim,max_tokens", [(64, 1), (64, 64), (96, 64), (128, 8), (128, 64), (256, 64)])
+def test_attention_of_the_most_requests(wq, dim, max_tokens):
+    # whatever the number of requests leaves of LDS
+    rng = np.random.default_rng(dim + max_tokens)
+    lengths = [int(rng.integers(0, 9)) for _ in range(4096)]
+    lengths[77] = 900
+    counts = [int(rng.integers(0, 2)) for _ in range(4096)]
+    counts[77], counts[4095] = 1, max_tokens
+    p = Attn(rng, lengths, counts, 4, 2, dim, 8)
+    run(wq, p, max_tokens=max_tokens)
+    p.check()

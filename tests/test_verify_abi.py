@@ -182,3 +182,10 @@ def test_the_binding_refuses_host_tensors_types_and_shapes():
         wq.wq_lora_prepare(x[:, ::2], x, x, x, x)
     with pytest.raises(ValueError, match="tensor"):
         wq.wq_kv_accept_prepare(None, None, None, None, None, None)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_many_requests_take_a_kernel_whose_buffers_leave_room(dim):
+    # beside the largest blocks' buffers there is LDS for the sums of 2048 requests: more take blocks of 64 rows
+    assert wq.wq_tree_attention_workspace_bytes(2049, 32, 4, dim, 64) == wq.wq_tree_attention_workspace_bytes(
+        2049, 4, 4, dim, 64) == wq.wq_tree_attention_workspace_bytes(4096, 32, 4, dim, 64)

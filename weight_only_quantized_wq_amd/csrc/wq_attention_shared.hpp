@@ -78,7 +78,7 @@ __device__ __forceinline__ Deal deal_at(char* lds, int requests) {
   d.length = reinterpret_cast<int32_t*>(d.where + requests);
   return d;
 }
-static size_t deal_bytes(int64_t requests) { return (size_t)((3 * requests + 1) * 4 + 15) / 16 * 16; }
+constexpr size_t deal_bytes(int64_t requests) { return (size_t)((3 * requests + 1) * 4 + 15) / 16 * 16; }
 
 // Tiles of a group: positions past the table hold nothing.
 template <int TILE>

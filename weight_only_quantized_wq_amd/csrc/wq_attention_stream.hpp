@@ -35,9 +35,9 @@
 namespace wq {
 
 // Shape of a launch: positions of a tile, buffers of the ring, workgroups per
-// CU.  The ring holds up to 64 KB (two workgroups share a CU's 160 KB) or 128 KB,
-// with room for the deal of 4096 requests (512 with WK = 4) behind it; a wave's
-// share of a tile must be whole requests of 1 KB.
+// CU.  The ring holds up to 64 KB (two workgroups share a CU's 160 KB), 96 KB with
+// room for the deal of 4096 requests behind it, or 128 KB for fewer; a wave's share
+// of a tile must be whole requests of 1 KB.
 template <int D, int WK, int W>
 struct Shape {
   static constexpr int TILE = WK == 4 ? 128 : D == 96 || W == 8 ? 64 : 32;

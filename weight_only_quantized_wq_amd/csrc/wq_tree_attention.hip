@@ -96,16 +96,20 @@ __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttnArgs a
 
 constexpr int64_t kAttnMade = 0x77715f6174746e31;
 
-// Which kernel, by the rows per key head that max_tokens can make: up to 16
-// (with more than 512 requests the deal does not fit LDS beside its ring, nor
-// is there need to share a row tile), up to 64, more (head_dim 256: blocks of 64
-// for all, as its buffers and accumulators fill LDS and the registers).
+// Which kernel, by the rows per key head that max_tokens can make: up to 16, up
+// to 64, more.  With more than 512 (2048) requests the deal does not fit LDS
+// beside the first (last) one's ring; blocks of 64 rows take any number of both.
+// (head_dim 256: these for all, as its buffers and accumulators fill LDS and the
+// registers.)
 enum { kRows16 = 0, kRows64 = 1, kRowsMany = 2 };
+constexpr int64_t kRequests16 = 512;
+constexpr int64_t kRequestsMany = 2048;
 
 static int attn_variant(int64_t requests, int group, int head_dim, int max_tokens) {
   const int rows = group * max_tokens;
   if (head_dim == 256) return kRows64;
-  return rows <= 16 && requests <= 512 ? kRows16 : rows <= 64 ? kRows64 : kRowsMany;
+  if (rows <= 16 && requests <= kRequests16) return kRows16;
+  return rows <= 64 || requests > kRequestsMany ? kRows64 : kRowsMany;
 }
 
 // Workgroups of a launch: as many as are resident.
@@ -158,8 +162,11 @@ template <int D, int R, int WK, int W>
 static int attn_launch(const char* name, AttnArgs a, int grid, hipStream_t s) {
   constexpr int ROWS = 16 * R * (W / WK);
   constexpr int TILE = Shape<D, WK, W>::TILE;
+  constexpr size_t ring = sizeof(StreamLds<D, WK, W>) + (WK > 1 ? sizeof(MeetLds<D>) : 0);
+  constexpr int64_t most = WK > 1 ? kRequests16 : R > 1 ? kRequestsMany : kMaxRequests;
+  static_assert(ring + deal_bytes(most) + 512 <= 160 * 1024, "ring and deal do not fit LDS");
   const size_t deal = deal_bytes(a.b.requests);
-  const size_t lds = sizeof(StreamLds<D, WK, W>) + (WK > 1 ? sizeof(MeetLds<D>) : 0) + deal;
+  const size_t lds = ring + deal;
   a.least = kLeastPositions / TILE;
   a.uncut = kUncutPositions / TILE;
   // lane offsets within 8 rows are 32-bit byte offsets
