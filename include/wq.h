@@ -527,8 +527,8 @@ int wq_qkv_rope_run(const wq_qkv_rope_plan* plan, void* stream);
  *         16-byte aligned, strides multiples of 8; y must not overlap q
  * A request brings at most max_tokens rows, 1 <= max_tokens <= 64; one that
  * brings more is left alone.  heads / kv_heads <= 64.  scale finite.  requests
- * * kv_heads * row blocks (of 64 rows per key head) * positions / 32 stays
- * below 2^31, with the positions that the table covers.
+ * * kv_heads * row blocks (of 64 rows per key head) * (positions / 32 + 4)
+ * stays below 2^31, with the positions that the table covers.
  * Scores and sums are fp32; the weights enter the second product as bf16.
  *
  * The positions of all requests are cut into equal shares for the launch's

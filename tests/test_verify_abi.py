@@ -189,3 +189,10 @@ def test_many_requests_take_a_kernel_whose_buffers_leave_room(dim):
     # beside the largest blocks' buffers there is LDS for the sums of 2048 requests: more take blocks of 64 rows
     assert wq.wq_tree_attention_workspace_bytes(2049, 32, 4, dim, 64) == wq.wq_tree_attention_workspace_bytes(
         2049, 4, 4, dim, 64) == wq.wq_tree_attention_workspace_bytes(4096, 32, 4, dim, 64)
+
+
+@pytest.mark.parametrize("width,rc", [(507 * 32, 3), (507 * 32 + 1, 2), (509 * 32, 2)])
+def test_the_deal_of_the_largest_batches_stays_in_32_bits(width, rc):
+    # 4096 requests x 1024 key heads x (tiles + 4) < 2^31, so fewer than 508 tiles of 32 positions; y is misaligned
+    assert status("attention", batch=batch(requests=4096), heads=1024, q_stride=65536, y_stride=65536, max_tokens=1,
+                  cache=cache(kv_heads=1024, head_stride=64, page_size=1, table_width=width, table_stride=width)) == rc

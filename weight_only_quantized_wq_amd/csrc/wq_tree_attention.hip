@@ -148,8 +148,9 @@ static int attn_check(const char* name, const wq_tree_attention& a) {
   if (!(fabsf(a.scale) < INFINITY)) return fail(WQ_ERR_SHAPE, "%s: scale must be finite", name);
   if (a.q == a.y && a.batch.tokens > 0) return fail(WQ_ERR_SHAPE, "%s: y must not be q", name);
   const int64_t blocks = ((int64_t)(a.heads / a.cache.kv_heads) * a.max_tokens + 63) / 64;
-  const int64_t tiles = (a.cache.table_width * a.cache.page_size + a.max_tokens) / 32 + 2;
-  if (a.batch.requests * a.cache.kv_heads * blocks * tiles > 0x7FFFFFFF)
+  // the deal's costs (and a group past their end) are 32-bit sums
+  const int64_t tiles = (a.cache.table_width * a.cache.page_size + 31) / 32 + kGroupCost;
+  if (a.batch.requests * a.cache.kv_heads * blocks * tiles + tiles + 1024 > 0x7FFFFFFF)
     return fail(WQ_ERR_SHAPE, "%s: %lld requests of %lld positions are more than 2^31 tiles", name,
                 (long long)a.batch.requests, (long long)(a.cache.table_width * a.cache.page_size));
   if ((rc = check_cache_align(name, a.cache))) return rc;
