@@ -966,3 +966,29 @@ def test_attention_of_the_most_requests(wq, dim, max_tokens):
     p = Attn(rng, lengths, counts, 4, 2, dim, 8)
     run(wq, p, max_tokens=max_tokens)
     p.check()
+
+
+@pytest.mark.parametrize("rank,out", [(16, "f32"), (16, "bf16"), (64, "f32"), (64, "bf16")])
+def test_lora_sums_that_are_infinite_or_nearly(wq, rank, out):
+    import torch
+    rng = np.random.default_rng(rank)
+    x, a = np.zeros((3, 64)), np.zeros((1, rank, 64))
+    x[0, 0], x[1, 0], x[2, 0] = np.inf, -np.inf, 2.0 ** 127
+    x[2, 1] = 2.0 ** 126
+    a[0, :, 0], a[0, :, 1] = 1.0, 1.9921875            # row 2: A x = 1.99609375 * 2^127 rounds to no finite bf16
+    b = rng.uniform(1, 2, size=(1, 40, rank)) * 2.0 ** -100
+    b[0, 7], b[0, 8, 3] = -b[0, 7], -b[0, 8, 3]        # -inf, and inf - inf
+    a64, at = bf16(a)
+    b64, bt = bf16(b)
+    y = torch.zeros(3, 40, device="cuda", dtype=torch.float32 if out == "f32" else torch.bfloat16)
+    wq.wq_lora_run(wq.wq_lora_prepare(torch.from_numpy(x).to(torch.bfloat16).cuda(), at, bt, i32([0, 0, 0]), y))
+    torch.cuda.synchronize()
+    got = f64(y)
+    h = 1.99609375 * 2.0 ** 127
+    want = np.stack([np.inf * np.sign(b64[0]).sum(1), -np.inf * np.sign(b64[0]).sum(1), h * b64[0].sum(1)])
+    want[:2, 8] = np.nan
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[:2, [i for i in range(40) if i != 8]], want[:2, [i for i in range(40) if i != 8]])
+    reach = h * np.abs(b64[0]).sum(1)
+    tol = (3 * rank + 8) * 2.0 ** -24 * reach + (BF16 * np.abs(want[2]) + 2.0 ** -16 * reach if out == "bf16" else 0)
+    assert np.all(np.abs(got[2] - want[2]) <= tol)

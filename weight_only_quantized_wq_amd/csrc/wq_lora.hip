@@ -290,13 +290,15 @@ template <int RT, int PARTS>
 struct SplitH {
   static constexpr int KS = (RT + 1) / 2;
   __bf16 at[2][KS][PARTS][kWave][8];
-  // Rank j of token row t, as PARTS bf16 parts.
+  // Rank j of token row t, as PARTS bf16 parts.  What would round to infinity is cut
+  // off instead (the rest follows in the next part); infinity has no rest.
   __device__ __forceinline__ void put(int t, int j, float v) {
 #pragma unroll
     for (int q = 0; q < PARTS; ++q) {
-      const __bf16 part = (__bf16)v;
+      __bf16 part = (__bf16)v;
+      if (fabsf((float)part) == INFINITY) part = (__bf16)__uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
       at[t >> 4][j >> 5][q][(j >> 3 & 3) * 16 + (t & 15)][j & 7] = part;
-      v -= (float)part;
+      v = (float)part == v ? 0.f : v - (float)part;
     }
   }
 };
