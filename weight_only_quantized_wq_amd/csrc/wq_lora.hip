@@ -17,10 +17,10 @@
 // lora_one_kernel does both for few rows and a small A.
 //
 // Weights are read once per tile.  Measured (MI355X): 32 x 5 rows of 28 adapters,
-// rank 32, k = 8192, n = 10240: 19.6 us, 43 MB, of which the two launches' own
-// cost is about 5; 8 x 128 rows of 4 adapters, rank 64, k = 4096, n = 22016: 59 us,
-// 157 MB, bound by the latency of base and B under the registers' two waves per
-// SIMD (without base 44 us, without B 50, without stores 50); one row: launches.
+// rank 32, k = 8192, n = 10240: 18.1 us, 43 MB, of which the two launches' own
+// cost and the search are about 8; 8 x 128 rows of 4 adapters, rank 64, k = 4096, n =
+// 22016: 48.5 us, 157 MB (of it the second launch 39 us, 135 MB, 3.5 TB/s under the
+// registers' two waves per SIMD); one row: launches.
 #include <math.h>
 
 #include "wq_kv.hpp"
@@ -68,7 +68,8 @@ struct LoraArgs {
   int32_t adapters;
   int32_t rank;
   int32_t tiles;        // most tiles the batch can have
-  int32_t splits;
+  int32_t splits;       // shares of k (shrink)
+  int32_t shares;       // of n (expand)
   int32_t chunk;        // inputs per split (shrink), B rows per workgroup (expand)
   int32_t vec;          // base and y rows take 16-byte (8-byte bf16) accesses
 };
@@ -186,6 +187,23 @@ __device__ void find_tile(const LoraArgs& a, int want, char* lds, TileRows& tile
   __syncthreads();
 }
 
+// Workgroup -> (tile, share of the outputs or inputs).  Workgroups are dispatched
+// round robin over the 8 XCDs; an XCD takes a contiguous run of the units in
+// share-major order, so that tiles of one adapter read a share of its weights
+// through one L2 (1024 rows of 4 adapters, rank 64, n = 22016: 48.5 us; with tiles
+// dealt round robin, every XCD reading all of B, 53.7).
+struct Unit {
+  int tile, share;
+};
+__device__ __forceinline__ Unit unit_of(const LoraArgs& a, int shares) {
+  const int total = a.tiles * shares, each = (total + 7) >> 3, block = (int)blockIdx.x;
+  const int u = (block & 7) * each + (block >> 3);
+  if (u >= total) return Unit{-1, 0};
+  const int share = (int)((uint32_t)u / (uint32_t)a.tiles);
+  return Unit{u - share * a.tiles, share};
+}
+static dim3 unit_grid(int tiles, int shares) { return dim3((unsigned)((tiles * shares + 7) / 8 * 8)); }
+
 __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter) {
   return a.ranks ? min(max(gmem(a.ranks)[adapter], 0), a.rank) : a.rank;
 }
@@ -268,15 +286,17 @@ __global__ __launch_bounds__(kLoraThreads) void lora_shrink_kernel(LoraArgs a) {
   extern __shared__ __align__(16) char lds[];
   __shared__ TileRows tile;
   __shared__ float sum[kLoraWaves][RT * 16][17];
-  find_tile(a, (int)blockIdx.x, lds, tile);
-  if (blockIdx.y == 0 && threadIdx.x < sizeof(TileRows) / 4)
-    gmem(reinterpret_cast<int32_t*>(a.found + blockIdx.x))[threadIdx.x] = reinterpret_cast<const int32_t*>(&tile)[threadIdx.x];
+  const Unit u = unit_of(a, a.splits);
+  if (u.tile < 0) return;
+  find_tile(a, u.tile, lds, tile);
+  if (u.share == 0 && threadIdx.x < sizeof(TileRows) / 4)
+    gmem(reinterpret_cast<int32_t*>(a.found + u.tile))[threadIdx.x] = reinterpret_cast<const int32_t*>(&tile)[threadIdx.x];
   if (tile.rows == 0 || tile.adapter == a.adapters) return;
   const int rank = rank_of(a, tile.adapter);
-  const int k0 = (int)blockIdx.y * a.chunk, k1 = min(k0 + a.chunk, a.k);
+  const int k0 = u.share * a.chunk, k1 = min(k0 + a.chunk, a.k);
   f32x4 acc[2][RT];
   shrink_products<RT, kLoraWaves>(a, tile, rank, k0, k1, acc);
-  float* out = a.part + ((int64_t)blockIdx.y * a.tiles + blockIdx.x) * (kLoraRows * RT * 16);
+  float* out = a.part + ((int64_t)u.share * a.tiles + u.tile) * (kLoraRows * RT * 16);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h && tile.rows <= 16) break;
@@ -449,12 +469,14 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
   constexpr int KS = (RT + 1) / 2;          // products of 32 ranks
   constexpr int R16 = RT * 16;
   __shared__ __align__(16) SplitH<RT, PARTS> hs;
-  const auto& tile = *gmem(a.found + blockIdx.x);
+  const Unit u = unit_of(a, a.shares);
+  if (u.tile < 0) return;
+  const auto& tile = *gmem(a.found + u.tile);
   const int rows = tile.rows, adapter = tile.adapter;
   if (rows == 0) return;
   const bool bare = adapter == a.adapters;
   const int rank = bare ? a.rank : rank_of(a, adapter);
-  const int n0 = (int)blockIdx.y * a.chunk, n1 = min(n0 + a.chunk, a.n);
+  const int n0 = u.share * a.chunk, n1 = min(n0 + a.chunk, a.n);
   Expand<RT, PARTS, kLoraWaves> expand(a, tile, rank, n0, n1);
   if (!bare) {
     const float scale = a.scale ? gmem(a.scale)[adapter] : 1.f;
@@ -462,7 +484,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_expand_kernel(LoraArgs a) {
       const int t = i / (KS * 32), j = i % (KS * 32);
       float sum = 0.f;
       if (j < R16 && t < rows) {
-        const float* from = a.part + (int64_t)blockIdx.x * (kLoraRows * R16) + t * R16 + j;
+        const float* from = a.part + (int64_t)u.tile * (kLoraRows * R16) + t * R16 + j;
         const int64_t stride = (int64_t)a.tiles * (kLoraRows * R16);
         for (int s = 0; s < a.splits; s += 8) {
           float x[8];
@@ -587,15 +609,19 @@ static int lora_launch(const char* name, LoraArgs a, hipStream_t s) {
   const size_t lds = search_bytes(a.tokens, a.adapters);
   const int steps = (a.k + kLoraStep - 1) / kLoraStep;
   a.chunk = (steps + a.splits - 1) / a.splits * kLoraStep;
-  hipLaunchKernelGGL((lora_shrink_kernel<RT>), dim3((unsigned)a.tiles, (unsigned)a.splits), dim3(kLoraThreads), lds, s, a);
-  // expand: 64 outputs per wave at a time, about 1024 workgroups in all
+  hipLaunchKernelGGL((lora_shrink_kernel<RT>), unit_grid(a.tiles, a.splits), dim3(kLoraThreads), lds, s, a);
+  // expand: 64 outputs per wave at a time, as many workgroups as are resident (two
+  // per CU), so that each reads its tile's h once; twice as many where most tiles
+  // may be empty (few rows for each of many adapters).  Measured, 512 / 1024: 1024
+  // rows of 4 adapters 48.5 / 54.5 us, 160 rows of 64 adapters 22.0 / 19.4.
   const int rows = (a.n + 63) / 64;
-  int64_t parts = (1024 + a.tiles - 1) / a.tiles;
+  const int target = a.tiles > 2 * ((a.tokens + kLoraRows - 1) / kLoraRows) ? 1024 : 512;
+  int64_t parts = (target + a.tiles - 1) / a.tiles;
   const int64_t most = (rows + kLoraWaves - 1) / kLoraWaves;
   parts = parts < most ? parts : most;
   a.chunk = (int)((most + parts - 1) / parts) * kLoraWaves * 64;
-  parts = (a.n + a.chunk - 1) / a.chunk;
-  const dim3 grid((unsigned)a.tiles, (unsigned)parts);
+  a.shares = (a.n + a.chunk - 1) / a.chunk;
+  const dim3 grid = unit_grid(a.tiles, a.shares);
   if (a.y32)
     hipLaunchKernelGGL((lora_expand_kernel<RT, 3>), grid, dim3(kLoraThreads), 0, s, a);
   else
