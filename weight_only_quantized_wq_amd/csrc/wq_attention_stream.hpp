@@ -113,7 +113,7 @@ __global__ __launch_bounds__(W * kWave, (Shape<D, WK, W>::GROUPS)) void attentio
   const Deal d = deal_at(lds + MEET + (WK > 1 ? sizeof(MeetLds<D>) : 0), a.b.requests);
   deal<ROWS, TILE>(a, d);
   const int total = __builtin_amdgcn_readfirstlane(d.before[a.b.requests]);
-  const int per = share_of(a, total, (int)gridDim.x);
+  const int per = share_of(total, (int)gridDim.x);
   const int share = share_index((int)blockIdx.x, (int)gridDim.x);
   if ((int64_t)share * per >= total) return;
   const int at = share * per;

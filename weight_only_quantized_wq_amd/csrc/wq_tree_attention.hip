@@ -17,77 +17,76 @@ __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttnArgs a
   deal<ROWS, TILE>(a, d);
   const int total = d.before[a.b.requests];
   if (total == 0) return;
-  const int per = share_of(a, total, grid);
+  const int per = share_of(total, grid);
   const int lane = lane_id();
-  const int token = (int)blockIdx.x;
-  int lo = 0, hi = a.b.requests - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (d.start(mid) <= token) lo = mid; else hi = mid - 1;
-  }
-  const int r = __builtin_amdgcn_readfirstlane(lo);
-  const int n = d.count(r), tok = token - d.start(r);
-  const int qh = (int)blockIdx.y * kAttnWaves + wave_id();
-  if (tok < 0 || tok >= n || qh >= a.heads) return;
-  const int rows = n * a.group, blocks = (rows + ROWS - 1) / ROWS;
-  const int tiles = tiles_of<TILE>(a, d.length[r], n);
-  if (tiles <= a.uncut) return;
-  const int head = token_of(a, qh), row = tok * a.group + qh - head * a.group;
-  const int first = d.before[r] + (head * blocks + row / ROWS) * (tiles + kGroupCost) + kGroupCost;
-  const int s0 = first / per, s1 = (first + tiles - 1) / per;
-  if (s0 == s1) return;
-  const int in = row % ROWS;
-  const auto part_of = [&](int s) { return a.parts + ((int64_t)s * 2 + (s == s0)) * (ROWS * (D + 2)); };
-  const int side = lane / LP, piece = lane % LP;
-  const bool has = piece * 4 < D;
-  float top = -INFINITY, sum = 0.f;
-  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int last = s1 - s0;
-  f32x4 x[BATCH];
-  const auto request = [&](int from) {
-#pragma unroll
-    for (int b = 0; b < BATCH; ++b) {
-      const float* part = part_of(s0 + min(from + b * SIDE + side, last)) + in * D + piece * 4;
-      x[b] = has ? *gmem(reinterpret_cast<const f32x4*>(part)) : f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-  };
-  for (int base = 0; base <= last; base += kWave) {
-    float m = -INFINITY, l = 0.f;
-    if (base + lane <= last) {
-      const float* part = part_of(s0 + base + lane);
-      m = gmem(part)[ROWS * D + in];
-      l = gmem(part)[ROWS * (D + 1) + in];
-    }
-    request(base);
-    const float now = fmaxf(wave_max(m), top);
-    const float ref = now == -INFINITY ? 0.f : now;
-    const float fo = __builtin_amdgcn_exp2f(top - ref), f = __builtin_amdgcn_exp2f(m - ref);
-    top = now;
-    sum = sum * fo + wave_sum(l * f);
-    o *= fo;
-    const int count = min(kWave, last - base + 1);
-    for (int i = 0; i < count; i += BATCH * SIDE) {
-      if (i) request(base + i);
+  const int quads = (a.heads + kAttnWaves - 1) / kAttnWaves, units = a.b.tokens * quads;
+#pragma unroll 1
+  for (int u = (int)blockIdx.x; u < units; u += (int)gridDim.x) {
+    const int token = (int)((uint32_t)u / (uint32_t)quads);
+    const int r = __builtin_amdgcn_readfirstlane(request_of(d, a.b.requests, token));
+    const int n = d.count(r), tok = token - d.start(r);
+    const int qh = (u - token * quads) * kAttnWaves + wave_id();
+    if (tok < 0 || tok >= n || qh >= a.heads) continue;
+    const int rows = n * a.group, blocks = (rows + ROWS - 1) / ROWS;
+    const int tiles = tiles_of<TILE>(a, d.length[r], n);
+    if (tiles <= a.uncut) continue;
+    const int head = token_of(a, qh), row = tok * a.group + qh - head * a.group;
+    const int first = d.before[r] + (head * blocks + row / ROWS) * (tiles + kGroupCost) + kGroupCost;
+    const int s0 = first / per, s1 = (first + tiles - 1) / per;
+    if (s0 == s1) continue;
+    const int in = row % ROWS;
+    const auto part_of = [&](int s) { return a.parts + ((int64_t)s * 2 + (s == s0)) * (ROWS * (D + 2)); };
+    const int side = lane / LP, piece = lane % LP;
+    const bool has = piece * 4 < D;
+    float top = -INFINITY, sum = 0.f;
+    f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int last = s1 - s0;
+    f32x4 x[BATCH];
+    const auto request = [&](int from) {
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
-        const int s = i + b * SIDE + side;
-        const float fb = __shfl(f, min(s, kWave - 1));
-        if (s < count) o += x[b] * fb;
+        const float* part = part_of(s0 + min(from + b * SIDE + side, last)) + in * D + piece * 4;
+        x[b] = has ? *gmem(reinterpret_cast<const f32x4*>(part)) : f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+    };
+    for (int base = 0; base <= last; base += kWave) {
+      float m = -INFINITY, l = 0.f;
+      if (base + lane <= last) {
+        const float* part = part_of(s0 + base + lane);
+        m = gmem(part)[ROWS * D + in];
+        l = gmem(part)[ROWS * (D + 1) + in];
+      }
+      request(base);
+      const float now = fmaxf(wave_max(m), top);
+      const float ref = now == -INFINITY ? 0.f : now;
+      const float fo = __builtin_amdgcn_exp2f(top - ref), f = __builtin_amdgcn_exp2f(m - ref);
+      top = now;
+      sum = sum * fo + wave_sum(l * f);
+      o *= fo;
+      const int count = min(kWave, last - base + 1);
+      for (int i = 0; i < count; i += BATCH * SIDE) {
+        if (i) request(base + i);
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+          const int s = i + b * SIDE + side;
+          const float fb = __shfl(f, min(s, kWave - 1));
+          if (s < count) o += x[b] * fb;
+        }
       }
     }
-  }
 #pragma unroll
-  for (int s = LP; s < kWave; s <<= 1)
+    for (int s = LP; s < kWave; s <<= 1)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], s);
-  const float f = sum == 0.f ? 0.f : 1.f / sum;
-  if (side == 0 && has) {
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    uint32_t w[2];
+      for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], s);
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    if (side == 0 && has) {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      uint32_t w[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      w[e] = sum == 0.f ? 0u : (uint32_t)f32_to_bf16(o[2 * e] * f) | (uint32_t)f32_to_bf16(o[2 * e + 1] * f) << 16;
-    *gmem(reinterpret_cast<u32x2*>(a.y + (int64_t)token * a.y_stride + qh * D + piece * 4)) = u32x2{w[0], w[1]};
+      for (int e = 0; e < 2; ++e)
+        w[e] = sum == 0.f ? 0u : (uint32_t)f32_to_bf16(o[2 * e] * f) | (uint32_t)f32_to_bf16(o[2 * e + 1] * f) << 16;
+      *gmem(reinterpret_cast<u32x2*>(a.y + (int64_t)token * a.y_stride + qh * D + piece * 4)) = u32x2{w[0], w[1]};
+    }
   }
 }
 
@@ -121,9 +120,16 @@ static int attn_rows(int variant, int head_dim) {
   return variant == kRows16 ? 16 : variant == kRows64 ? 64 : head_dim == 96 ? 128 : 256;
 }
 
-// Positions of a share at least, and of a group that is not cut.
-constexpr int kLeastPositions = 256;
+// Positions of a group that is not cut.  Where all are shorter no joining launch is
+// needed.  Measured, 256 / 512 / 1024 positions, heads of 128: one token over 500
+// positions, 32 key heads, 11.7 / 12.1 / 12.1 us; 16 requests of 500, 8 key heads,
+// 17.6 / 15.2 / 15.2; 5 tokens over 700, 8 key heads, 13.5 / 13.5 / 25.6; 64 such
+// requests 55.2 / 55.2 / 48.9.
 constexpr int kUncutPositions = 512;
+// Workgroups of the joining launch, each of which computes the deal once.  Measured,
+// 512 / 1024 / one per four rows: 32 x 32 tokens over 500 positions 39.1 / 37.8 / 46.4
+// us, 8 x 5 over 700 19.8 / 19.1 / 19.1.
+constexpr int kJoinGroups = 1024;
 
 static bool attn_dims_ok(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_tokens) {
   return heads >= 1 && heads <= kMaxHeads && kv_heads >= 1 && heads % kv_heads == 0 && heads / kv_heads <= 64 &&
@@ -168,7 +174,6 @@ static int attn_launch(const char* name, AttnArgs a, int grid, hipStream_t s) {
   static_assert(ring + deal_bytes(most) + 512 <= 160 * 1024, "ring and deal do not fit LDS");
   const size_t deal = deal_bytes(a.b.requests);
   const size_t lds = ring + deal;
-  a.least = kLeastPositions / TILE;
   a.uncut = kUncutPositions / TILE;
   // lane offsets within 8 rows are 32-bit byte offsets
   const bool page8 = a.c.page_size % 8 == 0 && a.c.token_stride < (1u << 28);
@@ -179,10 +184,10 @@ static int attn_launch(const char* name, AttnArgs a, int grid, hipStream_t s) {
   if (D == 96 || !page8)
     hipLaunchKernelGGL((attention_stream_kernel<D, R, WK, W, false>), dim3(grid), dim3(W * kWave), lds, s, a);
   // a table that covers no more than an uncut group leaves nothing to join
+  const int64_t units = (int64_t)a.b.tokens * ((a.heads + kAttnWaves - 1) / kAttnWaves);
   if ((int64_t)a.c.limit > kUncutPositions)
     hipLaunchKernelGGL((attention_join_kernel<D, ROWS, TILE>),
-                       dim3((unsigned)a.b.tokens, (unsigned)((a.heads + kAttnWaves - 1) / kAttnWaves)),
-                       dim3(kAttnThreads), deal, s, a, grid);
+                       dim3((unsigned)(units < kJoinGroups ? units : kJoinGroups)), dim3(kAttnThreads), deal, s, a, grid);
   return launch_status(name);
 }
 
