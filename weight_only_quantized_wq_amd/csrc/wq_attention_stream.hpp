@@ -25,6 +25,17 @@
 //   * WK = 4, up to 16 rows: all waves have the same rows and take 32 positions
 //     of a tile of 128 each, so that a short context is a few steps long; they
 //     meet in LDS at the end of a piece.
+// Measured (MI355X, heads of 128), with the joining launch: 5 tokens over 32763
+// positions, 64 / 8 heads, 39.4 us (134 MB, 3.4 TB/s; about 5 us until the ring runs
+// and 6.5 to join); 32 trees of 8 over up to 16384, 32 / 8 heads, 59.3 us (231 MB, 3.9
+// TB/s; what pieces cost between their tiles, and the join); one token over 500, 32 /
+// 32 heads, 12.5 us (32 workgroups at the 33 bytes a clock that the direct loads
+// reach on a CU, and a launch); 2 x 64 tokens over 16000, 64 / 8 heads, 101 us (663
+// TFLOP/s: vector ALU 51 % and matrix pipe 32 % of the cycles, LDS 26 %, and too
+// little of each beside the other).  For such trees 4 waves of 32 rows, two
+// workgroups per CU, take 136 us.
+// Page numbers of 8 rows against every row's: 32 trees of 8 65 / 87 us, 2 x 64 tokens
+// 105 / 110, one token 12.9 / 14.2.
 // K rows are stored with their 16-byte pieces exchanged by row (piece p of A
 // row m at p ^ m), so that the 16 lanes reading one piece of 16 rows hit
 // different banks; V rows are read along the row.

@@ -100,11 +100,17 @@ int same_device(const char* name, int32_t device) {
 // One workgroup takes one token (with few tokens, a share of its heads).  The
 // token's first heads are requested, its request is looked up and its rot_dim /
 // 2 angles are reduced in fp64 and turned into (cos, sin) once, in LDS; then
-// every P = pow2(head_dim / 8) lanes take a head, 8
-// elements a lane, so that a head is read and written in 16-byte pieces, its
-// square sum is a butterfly over P lanes and the partner of a rotated element
-// is in the lane itself (interleaved), in a lane a fixed distance away (halves
-// of a multiple of 8) or fetched through LDS (other halves).
+// every P = pow2(head_dim / 8) lanes take a head, 8 elements a lane, so that a
+// head is read and written in 16-byte pieces, its square sum is a butterfly over
+// P lanes and the partner of a rotated element is in the lane itself
+// (interleaved), in a lane a fixed distance away (halves of a multiple of 8) or
+// fetched through LDS (other halves).
+//
+// Measured (MI355X): 4095 rows of 32 / 8 heads of 128 with norms, 24.0 us (101 MB, 4.2
+// TB/s), where the vector ALU is busy most of the time and waves in plenty hide the
+// rest: one head at a time and 64 registers, since four requested at once (80
+// registers) took 27.0 us, two 26.4.  32 x 5 rows of 64 / 8 heads, fp32: 4.9 us, 9.8
+// MB, hardly more than a launch (one row: 3.4).
 
 struct RopeArgs {
   KvCache c;
@@ -127,7 +133,6 @@ struct RopeArgs {
 
 enum { kPairs = 0, kHalves = 1, kOddHalves = 2 };
 constexpr int kRopeThreads = 256;
-constexpr int kRopeHeads = 4;         // heads a lane group requests at once
 
 // Eight elements of a head as loaded.
 template <bool F32>
@@ -189,11 +194,9 @@ __global__ __launch_bounds__(kRopeThreads) void qkv_rope_kernel(RopeArgs a) {
   const int step = (int)gridDim.y * (kRopeThreads / a.lanes);
   const bool in = sub * 8 < dim;
   const int h0 = (int)(blockIdx.y * (kRopeThreads / a.lanes) + threadIdx.x / a.lanes);
-  Head8<F32> raw[kRopeHeads];
+  Head8<F32> raw;
   const auto request = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < kRopeHeads; ++i)
-      if (in && h + i * step < all) raw[i].load(a.qkv, (int64_t)t * a.qkv_stride + (int64_t)(h + i * step) * dim + sub * 8);
+    if (in && h < all) raw.load(a.qkv, (int64_t)t * a.qkv_stride + (int64_t)h * dim + sub * 8);
   };
   request(h0);
   // the token's request: how many of starts[1 ..] lie at or before it
@@ -231,83 +234,85 @@ __global__ __launch_bounds__(kRopeThreads) void qkv_rope_kernel(RopeArgs a) {
     sn[e] = first ? -f.y : f.y;
   }
 
-  for (int hb = h0; hb - h0 < all; hb += kRopeHeads * step) {
-    if (hb != h0) request(hb);
-#pragma unroll
-    for (int u = 0; u < kRopeHeads; ++u) {
-      const int h = hb + u * step;
-      if (h - h0 + (int)(blockIdx.y * (kRopeThreads / a.lanes)) >= all) break;      // the same for the whole workgroup
-      const bool on = in && h < all;
-      float x[8];
-      if (on) {
-        raw[u].values(x);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-      }
-      const bool key = h >= heads, value = h >= heads + kv;
-      if (a.q_norm || a.k_norm) {
-        float sq = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
-        sq = group_sum(sq, a.lanes);
-        if (!value && (key ? a.k_norm : a.q_norm)) {
-          const float f = __builtin_amdgcn_rsqf(fmaf(sq, a.per_dim, a.eps));
-          Head8<false> ws;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ws.w[0][i] = key ? weight[1].w[0][i] : weight[0].w[0][i];
-          float w[8];
-          ws.values(w);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * f * w[e];
-        }
-      }
-      float other[8];
-      if (LAYOUT == kPairs) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) other[e] = x[e ^ 1];
-      } else if (LAYOUT == kHalves) {
-        partners(x, other, lane, sub, half / 8);
-      } else {
-        // a wave reads only what it wrote itself
-        float* row = exch + ((int)threadIdx.x - sub) * 8;
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) row[sub * 8 + e] = x[e];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int i = sub * 8 + e;
-          other[e] = row[i < half ? i + half : i < 2 * half ? i - half : i];
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-      }
-      if (!on) continue;
-      u32x4 w;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float o[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int k = 2 * e + i;
-          // elements past rot_dim, and values, stay as they are (whatever the partner is)
-          const bool turns = !value && sub * 8 + k < 2 * half;
-          o[i] = turns ? fmaf(other[k], sn[k], x[k] * cs[k]) : x[k];
-        }
-        const bf16x2 two = {(__bf16)o[0], (__bf16)o[1]};
-        w[e] = __builtin_bit_cast(uint32_t, two);
-      }
-      uint16_t* to;
-      if (!key) {
-        to = a.q + (int64_t)t * a.q_stride + (int64_t)h * dim;
-      } else {
-        if (cache_row < 0) continue;
-        to = (value ? a.c.v : a.c.k) + cache_row + (int64_t)(h - heads - (value ? kv : 0)) * a.c.head_stride;
-      }
-      *gmem(reinterpret_cast<u32x4*>(to + sub * 8)) = w;
+  const int first = h0 - (int)threadIdx.x / a.lanes;        // the workgroup's first head
+  for (int from = first, h = h0; from < all; from += step, h += step) {       // the same trips for the whole workgroup
+    const bool on = in && h < all;
+    if (h != h0) request(h);
+    if (!F32 && __builtin_amdgcn_readfirstlane(h) >= heads + kv) {
+      // a wave of nothing but values only copies
+      if (on && cache_row >= 0)
+        *gmem(reinterpret_cast<u32x4*>(a.c.v + cache_row + (int64_t)(h - heads - kv) * a.c.head_stride + sub * 8)) = raw.w[0];
+      continue;
     }
+    float x[8];
+    if (on) {
+      raw.values(x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    }
+    const bool key = h >= heads, value = h >= heads + kv;
+    if (a.q_norm || a.k_norm) {
+      float sq = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
+      sq = group_sum(sq, a.lanes);
+      if (!value && (key ? a.k_norm : a.q_norm)) {
+        const float f = __builtin_amdgcn_rsqf(fmaf(sq, a.per_dim, a.eps));
+        Head8<false> ws;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ws.w[0][i] = key ? weight[1].w[0][i] : weight[0].w[0][i];
+        float w[8];
+        ws.values(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * f * w[e];
+      }
+    }
+    float other[8];
+    if (LAYOUT == kPairs) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[e] = x[e ^ 1];
+    } else if (LAYOUT == kHalves) {
+      partners(x, other, lane, sub, half / 8);
+    } else {
+      // a wave reads only what it wrote itself
+      float* row = exch + ((int)threadIdx.x - sub) * 8;
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) row[sub * 8 + e] = x[e];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = sub * 8 + e;
+        other[e] = row[i < half ? i + half : i < 2 * half ? i - half : i];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (!on) continue;
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float o[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = 2 * e + i;
+        // elements past rot_dim, and values, stay as they are (whatever the partner is)
+        const bool turns = !value && sub * 8 + k < 2 * half;
+        o[i] = turns ? fmaf(other[k], sn[k], x[k] * cs[k]) : x[k];
+      }
+      const bf16x2 two = {(__bf16)o[0], (__bf16)o[1]};
+      w[e] = __builtin_bit_cast(uint32_t, two);
+    }
+    uint16_t* to;
+    if (!key) {
+      to = a.q + (int64_t)t * a.q_stride + (int64_t)h * dim;
+    } else {
+      if (cache_row < 0) continue;
+      to = (value ? a.c.v : a.c.k) + cache_row + (int64_t)(h - heads - (value ? kv : 0)) * a.c.head_stride;
+    }
+    *gmem(reinterpret_cast<u32x4*>(to + sub * 8)) = w;
   }
 }
 
@@ -515,7 +520,8 @@ extern "C" int wq_qkv_rope_run(const wq_qkv_rope_plan* plan, void* stream) {
   r.heads = a.heads;
   r.lanes = 1;
   while (r.lanes * 8 < a.cache.head_dim) r.lanes *= 2;
-  // few tokens: their heads are shared out to fill the chip
+  // few tokens: their heads are shared out to fill the chip.  Measured, one / about
+  // 512 workgroups: one row of 32 heads 4.9 / 3.4 us, 160 rows of 64 / 8 heads 6.9 / 4.9.
   const int64_t per_block = kRopeThreads / r.lanes;
   const int64_t most = (a.heads + 2 * a.cache.kv_heads + per_block - 1) / per_block;
   int64_t split = 512 / a.batch.tokens;
