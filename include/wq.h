@@ -481,7 +481,8 @@ int wq_rope_frequencies(int32_t kind, int32_t rot_dim, double base, double facto
  * [rot_dim / 2] on the device; angles are reduced in fp64, all else is fp32,
  * each result rounded to nearest-even once.  rot_dim even, 0 .. head_dim (0:
  * freq may be NULL).  heads a multiple of kv_heads, up to 1024; q and qkv
- * 16-byte aligned, q_stride a multiple of 8; strides at least a row.
+ * 16-byte aligned, not overlapping, q_stride a multiple of 8; strides at least
+ * a row.
  */
 typedef struct {
   wq_kv_cache cache;
@@ -576,7 +577,8 @@ int wq_tree_attention_run(const wq_tree_attention_plan* plan, void* stream);
  * at 0 or later: a request whose path does not is left alone, as is a row
  * whose source or target holds nothing.  Lengths are the caller's to advance.
  * cache describes layer 0; layer l lies l * layer_stride elements on (a
- * multiple of 8), 1 <= layers <= 4096.
+ * multiple of 8, positive where there are several; layers must not share
+ * memory), 1 <= layers <= 4096.
  */
 typedef struct {
   wq_kv_cache cache;

@@ -196,3 +196,9 @@ def test_the_deal_of_the_largest_batches_stays_in_32_bits(width, rc):
     # 4096 requests x 1024 key heads x (tiles + 4) < 2^31, so fewer than 508 tiles of 32 positions; y is misaligned
     assert status("attention", batch=batch(requests=4096), heads=1024, q_stride=65536, y_stride=65536, max_tokens=1,
                   cache=cache(kv_heads=1024, head_stride=64, page_size=1, table_width=width, table_stride=width)) == rc
+
+
+@pytest.mark.parametrize("layers,rc", [(1, 3), (2, 2)])
+def test_layers_must_not_lie_on_each_other(layers, rc):
+    # a row that one layer's copy overwrites could be another's source; the k of a lone layer is only misaligned
+    assert status("accept", layers=layers, layer_stride=0) == rc

@@ -428,8 +428,9 @@ static int accept_check(const char* name, const wq_kv_accept& a) {
   if (!a.lengths || !a.path || !a.accepted)
     return fail(WQ_ERR_NULL, "%s: lengths, path and accepted must be non-null", name);
   if ((rc = check_cache_sizes(name, a.cache))) return rc;
-  if (a.layers < 1 || a.layers > 4096 || a.layer_stride < 0 || a.layer_stride > (int64_t)1 << 40 || a.layer_stride % 8)
-    return fail(WQ_ERR_SHAPE, "%s: layers = %lld (1..4096), layer_stride = %lld (a multiple of 8)", name,
+  if (a.layers < 1 || a.layers > 4096 || a.layer_stride < 0 || a.layer_stride > (int64_t)1 << 40 ||
+      a.layer_stride % 8 || (a.layers > 1 && a.layer_stride == 0))
+    return fail(WQ_ERR_SHAPE, "%s: layers = %lld (1..4096), layer_stride = %lld (a positive multiple of 8)", name,
                 (long long)a.layers, (long long)a.layer_stride);
   if (a.requests < 0 || a.requests > kMaxRequests)
     return fail(WQ_ERR_SHAPE, "%s: requests = %lld must be in [0, %lld]", name, (long long)a.requests,
