@@ -992,3 +992,17 @@ def test_lora_sums_that_are_infinite_or_nearly(wq, rank, out):
     reach = h * np.abs(b64[0]).sum(1)
     tol = (3 * rank + 8) * 2.0 ** -24 * reach + (BF16 * np.abs(want[2]) + 2.0 ** -16 * reach if out == "bf16" else 0)
     assert np.all(np.abs(got[2] - want[2]) <= tol)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("n,heads", [(1, 4), (5, 8), (40, 32)])
+def test_attention_of_one_visible_position_is_its_value(wq, dim, n, heads):
+    # the sum has the weight as the product has it, rounded
+    rng = np.random.default_rng(dim + n)
+    p = Attn(rng, [0, 0, 0], [n, n, n], heads, 4, dim, 16, tree=[1 << i for i in range(n)])
+    run(wq, p)
+    for r in range(3):
+        for i in range(n):
+            row = int(p.table[r][i // 16]), i % 16
+            want = np.repeat(p.v64[row], heads // 4, axis=0)
+            assert np.array_equal(f64(p.y[int(p.starts[r]) + i]), want)

@@ -262,16 +262,23 @@ __device__ __forceinline__ uint32_t sees_of(int past, uint64_t seen) {
   return context | draft;
 }
 
+__device__ __forceinline__ bf16x8 ones() {
+  const __bf16 one = (__bf16)1.f;
+  return bf16x8{one, one, one, one, one, one, one, one};
+}
+
 // One step of the running softmax over 32 positions: raw scores s in, weights w
 // (bf16, relative to 2^top) out; sums and outputs are rescaled where the
 // running maximum is raised.  That happens only when some score exceeds it by
 // more than 2^kLazy (its exact value cancels in the quotient), so the usual
 // step needs no exchange between lanes.  `sees` is used unless `whole`.
-// The weights are rounded to bf16 for the matrix product (2^-8 of each at most;
-// the sum keeps them unrounded), all else is fp32.
+// The weights are rounded to bf16 for the matrix product (2^-8 of each at most).
+// They are summed by one more product, with a column of ones: so the sum has the
+// weights that the output has (a row that sees one position gets its value
+// exactly), in the layout of the output's rows.  All else is fp32.
 template <int R, int CW>
 __device__ __forceinline__ void softmax_step(const f32x4 (&s)[R][2], float scale2, bool whole,
-                                             const uint32_t (&sees)[R], int g, float (&top)[R], float (&sum)[R],
+                                             const uint32_t (&sees)[R], int g, float (&top)[R], f32x4 (&sum)[R],
                                              f32x4 (&o)[R][CW], bf16x8 (&w)[R]) {
   float x[R][8], most[R];
 #pragma unroll
@@ -299,10 +306,10 @@ __device__ __forceinline__ void softmax_step(const f32x4 (&s)[R][2], float scale
       const float now = fmaxf(top[t], m);
       const float f = now == -INFINITY || now == top[t] ? 1.f : __builtin_amdgcn_exp2f(top[t] - now);
       top[t] = now;
-      sum[t] *= f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float fr = __shfl(f, 4 * g + i);
+        sum[t][i] *= fr;
 #pragma unroll
         for (int j = 0; j < CW; ++j) o[t][j][i] *= fr;
       }
@@ -313,10 +320,9 @@ __device__ __forceinline__ void softmax_step(const f32x4 (&s)[R][2], float scale
     const float ref = top[t] == -INFINITY ? 0.f : top[t];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(x[t][e], scale2, -ref));
-      sum[t] += p;
-      w[t][e] = (__bf16)p;
+      w[t][e] = (__bf16)__builtin_amdgcn_exp2f(fmaf(x[t][e], scale2, -ref));
     }
+    sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[t], ones(), sum[t], 0, 0, 0);
   }
 }
 

@@ -276,11 +276,12 @@ __global__ __launch_bounds__(W * kWave, (Shape<D, WK, W>::GROUPS)) void attentio
   while (p.t0 < p.t1) {
     const bool busy = p.block * ROWS + in0 < p.rows;     // else the wave only moves data
     f32x4 o[R][CW];
-    float top[R], sum[R];
+    float top[R];
+    f32x4 sum[R];
 #pragma unroll
     for (int t = 0; t < R; ++t) {
       top[t] = -INFINITY;
-      sum[t] = 0.f;
+      sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < CW; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -382,11 +383,6 @@ __global__ __launch_bounds__(W * kWave, (Shape<D, WK, W>::GROUPS)) void attentio
 #pragma unroll
       for (int t = 0; t < R; ++t) load_query<D>(a, p, p.block * ROWS + in0 + 16 * t + c, g, q[t], seen[t]);
     }
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      sum[t] += __shfl_xor(sum[t], 16);
-      sum[t] += __shfl_xor(sum[t], 32);
-    }
     if constexpr (WK == 1) {
 #pragma unroll
       for (int t = 0; t < R; ++t) {
@@ -394,7 +390,7 @@ __global__ __launch_bounds__(W * kWave, (Shape<D, WK, W>::GROUPS)) void attentio
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           most[i] = __shfl(top[t], 4 * g + i);
-          all[i] = __shfl(sum[t], 4 * g + i);
+          all[i] = sum[t][i];
         }
         if (busy) {
           write_rows<D, ROWS>(a, now, share, in0 + 16 * t, g, c, o[t], most, all);
@@ -403,10 +399,8 @@ __global__ __launch_bounds__(W * kWave, (Shape<D, WK, W>::GROUPS)) void attentio
       }
     } else {
       // the four waves meet: a common maximum, then (2, 3) -> (0, 1) -> 0
-      if (g == 0) {
-        mt.m[wave][c] = top[0];
-        mt.l[wave][c] = sum[0];
-      }
+      if (g == 0) mt.m[wave][c] = top[0];
+      if (c < 4) mt.l[wave][4 * g + c] = c == 0 ? sum[0][0] : c == 1 ? sum[0][1] : c == 2 ? sum[0][2] : sum[0][3];
       if (lane == 0) mt.special[wave] = special;
       __syncthreads();
       const bool any_special = (mt.special[0] | mt.special[1] | mt.special[2] | mt.special[3]) != 0;
