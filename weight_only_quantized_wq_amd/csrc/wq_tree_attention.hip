@@ -95,24 +95,25 @@ __global__ __launch_bounds__(kAttnThreads) void attention_join_kernel(AttnArgs a
 
 constexpr int64_t kAttnMade = 0x77715f6174746e31;
 
-// Which kernel, by the rows per key head that max_tokens can make: up to 16, up
-// to 64, more.  With more than 512 (2048) requests the deal does not fit LDS
-// beside the first (last) one's ring; blocks of 64 rows take any number of both.
-// (head_dim 256: these for all, as its buffers and accumulators fill LDS and the
-// registers.)
-// Measured, heads of 128: up to 16 rows, first / second kernel: one token over 500
-// positions, 32 key heads, 12.9 / 18.4 us; 16 requests of 500, 64 / 8 heads, 15.2 /
-// 19.9 (64 requests of 2 tokens over 400, 32 / 8 heads, 32.0 / 26.6); above 64 rows,
-// third / second: 2 x 64 tokens over 16000, 64 / 8 heads, 105 / 157; 4 x 64 over
-// 1000, 32 / 8 heads, 35.6 / 32.7.
+// Which kernel, by the rows per key head that max_tokens can make: up to 16 in at
+// most 256 (request, key head) groups, one for each of its workgroups; up to 64 (or
+// more groups); more.  With more than 2048 requests the deal does not fit LDS
+// beside the last one's ring; blocks of 64 rows take any number.  (head_dim 256:
+// these for all, as its buffers and accumulators fill LDS and the registers.)
+// Measured, heads of 128, first / second kernel: one token over 500 positions, 32
+// key heads, 12.9 / 18.4 us; 16 requests of 500, 64 / 8 heads, 15.2 / 19.9; 8 of up
+// to 4088, 32 key heads, 57 / 53, all of 4088 104 / 114; but with 8 key heads 48
+// requests of 120 positions 16.4 / 11.7, 128 of 1016 117 / 108.  Above 64 rows, third /
+// second: 2 x 64 tokens over 16000, 64 / 8 heads, 105 / 157; 4 x 64 over 1000, 32 / 8
+// heads, 35.6 / 32.7.
 enum { kRows16 = 0, kRows64 = 1, kRowsMany = 2 };
-constexpr int64_t kRequests16 = 512;
+constexpr int64_t kGroups16 = 256;
 constexpr int64_t kRequestsMany = 2048;
 
-static int attn_variant(int64_t requests, int group, int head_dim, int max_tokens) {
-  const int rows = group * max_tokens;
+static int attn_variant(int64_t requests, int heads, int kv_heads, int head_dim, int max_tokens) {
+  const int rows = heads / kv_heads * max_tokens;
   if (head_dim == 256) return kRows64;
-  if (rows <= 16 && requests <= kRequests16) return kRows16;
+  if (rows <= 16 && requests * kv_heads <= kGroups16) return kRows16;
   return rows <= 64 || requests > kRequestsMany ? kRows64 : kRowsMany;
 }
 
@@ -175,7 +176,7 @@ static int attn_launch(const char* name, AttnArgs a, int grid, hipStream_t s) {
   constexpr int ROWS = 16 * R * (W / WK);
   constexpr int TILE = Shape<D, WK, W>::TILE;
   constexpr size_t ring = sizeof(StreamLds<D, WK, W>) + (WK > 1 ? sizeof(MeetLds<D>) : 0);
-  constexpr int64_t most = WK > 1 ? kRequests16 : R > 1 ? kRequestsMany : kMaxRequests;
+  constexpr int64_t most = WK > 1 ? kGroups16 : R > 1 ? kRequestsMany : kMaxRequests;
   static_assert(ring + deal_bytes(most) + 512 <= 160 * 1024, "ring and deal do not fit LDS");
   const size_t deal = deal_bytes(a.b.requests);
   const size_t lds = ring + deal;
@@ -214,7 +215,7 @@ using namespace wq;
 extern "C" int64_t wq_tree_attention_workspace_bytes(int64_t requests, int32_t heads, int32_t kv_heads,
                                                      int32_t head_dim, int32_t max_tokens) {
   if (requests < 0 || requests > kMaxRequests || !attn_dims_ok(heads, kv_heads, head_dim, max_tokens)) return 0;
-  const int variant = attn_variant(requests, heads / kv_heads, head_dim, max_tokens);
+  const int variant = attn_variant(requests, heads, kv_heads, head_dim, max_tokens);
   return (int64_t)attn_grid(variant, head_dim) * 2 * attn_rows(variant, head_dim) * (head_dim + 2) * 4;
 }
 
@@ -233,7 +234,7 @@ extern "C" int wq_tree_attention_prepare(const wq_tree_attention* a, void* works
   wq_tree_attention_plan p{};
   if ((rc = plan_device(name, &p.device))) return rc;
   p.made = kAttnMade;
-  p.variant = attn_variant(a->batch.requests, a->heads / a->cache.kv_heads, a->cache.head_dim, a->max_tokens);
+  p.variant = attn_variant(a->batch.requests, a->heads, a->cache.kv_heads, a->cache.head_dim, a->max_tokens);
   p.workspace = workspace;
   p.a = *a;
   *plan = p;
