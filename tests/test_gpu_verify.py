@@ -1006,3 +1006,14 @@ def test_attention_of_one_visible_position_is_its_value(wq, dim, n, heads):
             row = int(p.table[r][i // 16]), i % 16
             want = np.repeat(p.v64[row], heads // 4, axis=0)
             assert np.array_equal(f64(p.y[int(p.starts[r]) + i]), want)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("lengths", [(300, 0, 90), (2200, 1900, 2300)])
+def test_attention_wide_trees_over_short_and_long_tables(wq, dim, lengths):
+    # the rows times the positions of the table choose the kernel; one workspace size serves both
+    rng = np.random.default_rng(dim + lengths[0])
+    p = Attn(rng, lengths, [64, 33, 64], 64, 4, dim, 16, tree=lambda n: random_tree(rng, n))
+    assert wq.wq_tree_attention_workspace_bytes(3, 64, 4, dim, 64) > wq.wq_tree_attention_workspace_bytes(3, 4, 4, dim, 64)
+    run(wq, p, max_tokens=64)
+    p.check()

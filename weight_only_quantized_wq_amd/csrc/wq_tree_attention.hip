@@ -97,24 +97,28 @@ constexpr int64_t kAttnMade = 0x77715f6174746e31;
 
 // Which kernel, by the rows per key head that max_tokens can make: up to 16 in at
 // most 256 (request, key head) groups, one for each of its workgroups; up to 64 (or
-// more groups); more.  With more than 2048 requests the deal does not fit LDS
-// beside the last one's ring; blocks of 64 rows take any number.  (head_dim 256:
-// these for all, as its buffers and accumulators fill LDS and the registers.)
+// more groups, or less work than fills the third); more.  With more than 2048
+// requests the deal does not fit LDS beside the last one's ring; blocks of 64 rows
+// take any number.  (head_dim 256: these for all, as its buffers and accumulators
+// fill LDS and the registers.)
 // Measured, heads of 128, first / second kernel: one token over 500 positions, 32
 // key heads, 12.9 / 18.4 us; 16 requests of 500, 64 / 8 heads, 15.2 / 19.9; 8 of up
 // to 4088, 32 key heads, 57 / 53, all of 4088 104 / 114; but with 8 key heads 48
 // requests of 120 positions 16.4 / 11.7, 128 of 1016 117 / 108.  Above 64 rows, third /
-// second: 2 x 64 tokens over 16000, 64 / 8 heads, 105 / 157; 4 x 64 over 1000, 32 / 8
-// heads, 35.6 / 32.7.
+// second, 32 / 8 heads: 64 tokens over 1984 positions 26.3 / 21.4, over 8128 34.8 /
+// 35.0; 4 x 64 over 448 32.2 / 26.9, over 1984 36.7 / 37.3, over 8128 68 / 88; 16 x 64
+// over 448 33 / 28, over 1984 83 / 88, over 8128 208 / 291.
 enum { kRows16 = 0, kRows64 = 1, kRowsMany = 2 };
 constexpr int64_t kGroups16 = 256;
 constexpr int64_t kRequestsMany = 2048;
+constexpr int64_t kLeastMany = 1 << 24;      // rows * positions
 
-static int attn_variant(int64_t requests, int heads, int kv_heads, int head_dim, int max_tokens) {
+static int attn_variant(int64_t requests, int heads, int kv_heads, int head_dim, int max_tokens, int64_t positions) {
   const int rows = heads / kv_heads * max_tokens;
   if (head_dim == 256) return kRows64;
   if (rows <= 16 && requests * kv_heads <= kGroups16) return kRows16;
-  return rows <= 64 || requests > kRequestsMany ? kRows64 : kRowsMany;
+  const bool small = requests * heads * max_tokens * positions <= kLeastMany;
+  return rows <= 64 || small || requests > kRequestsMany ? kRows64 : kRowsMany;
 }
 
 // Workgroups of a launch: as many as are resident.
@@ -215,7 +219,8 @@ using namespace wq;
 extern "C" int64_t wq_tree_attention_workspace_bytes(int64_t requests, int32_t heads, int32_t kv_heads,
                                                      int32_t head_dim, int32_t max_tokens) {
   if (requests < 0 || requests > kMaxRequests || !attn_dims_ok(heads, kv_heads, head_dim, max_tokens)) return 0;
-  const int variant = attn_variant(requests, heads, kv_heads, head_dim, max_tokens);
+  // the most that a table can cover: blocks of more rows need more
+  const int variant = attn_variant(requests, heads, kv_heads, head_dim, max_tokens, kMaxPositions);
   return (int64_t)attn_grid(variant, head_dim) * 2 * attn_rows(variant, head_dim) * (head_dim + 2) * 4;
 }
 
@@ -234,7 +239,8 @@ extern "C" int wq_tree_attention_prepare(const wq_tree_attention* a, void* works
   wq_tree_attention_plan p{};
   if ((rc = plan_device(name, &p.device))) return rc;
   p.made = kAttnMade;
-  p.variant = attn_variant(a->batch.requests, a->heads, a->cache.kv_heads, a->cache.head_dim, a->max_tokens);
+  p.variant = attn_variant(a->batch.requests, a->heads, a->cache.kv_heads, a->cache.head_dim, a->max_tokens,
+                           a->cache.table_width * a->cache.page_size);
   p.workspace = workspace;
   p.a = *a;
   *plan = p;
