@@ -1017,3 +1017,58 @@ def test_attention_wide_trees_over_short_and_long_tables(wq, dim, lengths):
     assert wq.wq_tree_attention_workspace_bytes(3, 64, 4, dim, 64) > wq.wq_tree_attention_workspace_bytes(3, 4, 4, dim, 64)
     run(wq, p, max_tokens=64)
     p.check()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dim,page", [(64, 16), (64, 9), (96, 16), (128, 16), (128, 9), (128, 24)])
+def test_attention_unseen_specials_of_wide_trees_over_long_tables(wq, bad, dim, page):
+    """The same where blocks of the most rows are taken: draft 2 of the third request of four."""
+    import torch
+    rng = np.random.default_rng(dim + page)
+    p = Attn(rng, [1300, 20, 1200, 1500], [6] * 4, 64, 2, dim, page, tree=[1, 3, 5, 9, 27, 33])
+    run(wq, p, max_tokens=64)
+    p.check()
+    clean = p.y.clone()
+    at = int(p.table[2, 1202 // page]), 1202 % page
+    p.k[at], p.v[at] = bad, bad
+    p.y.fill_(7.0)
+    run(wq, p, max_tokens=64)
+    same = [i for i in range(24) if i != 14]
+    assert torch.equal(p.y[same], clean[same])
+    assert not torch.isfinite(p.y[14]).any()
+
+
+def test_attention_wide_trees_captured(wq):
+    import torch
+    rng = np.random.default_rng(55)
+    p = Attn(rng, [1800, 700, 1500], [64, 40, 64], 64, 4, 128, 16, tree=lambda n: random_tree(rng, n))
+    plan = p.plan(wq, max_tokens=64)
+    wq.wq_tree_attention_run(plan)
+    torch.cuda.synchronize()
+    p.check()
+    eager = p.y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        wq.wq_tree_attention_run(plan)
+    for _ in range(3):
+        p.y.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(p.y, eager)
+        p.y.fill_(7.0)
+        wq.wq_tree_attention_run(plan)
+        torch.cuda.synchronize()
+        assert torch.equal(p.y, eager)
+
+
+@pytest.mark.parametrize("requests,heads,kv,dim,max_tokens", [(2048, 4, 2, 64, 64), (2048, 4, 2, 96, 64), (2048, 4, 2, 128, 64),
+                                                             (256, 2, 1, 128, 3), (256, 2, 1, 96, 3), (257, 2, 1, 128, 3)])
+def test_attention_where_a_kernel_takes_its_most_requests(wq, requests, heads, kv, dim, max_tokens):
+    rng = np.random.default_rng(requests + dim)
+    lengths = [int(rng.integers(0, 9)) for _ in range(requests)]
+    lengths[77] = 900
+    counts = [int(rng.integers(0, 3)) for _ in range(requests)]
+    counts[77], counts[requests - 1] = 1, max_tokens
+    p = Attn(rng, lengths, counts, heads, kv, dim, 8)
+    run(wq, p, max_tokens=max_tokens)
+    p.check()

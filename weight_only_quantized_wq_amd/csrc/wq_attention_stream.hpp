@@ -27,7 +27,7 @@
 //     meet in LDS at the end of a piece.
 // Measured (MI355X, heads of 128), with the joining launch: 5 tokens over 32763
 // positions, 64 / 8 heads, 39.4 us (134 MB, 3.4 TB/s; about 5 us until the ring runs
-// and 6.5 to join); 32 trees of 8 over up to 16384, 32 / 8 heads, 59.3 us (231 MB, 3.9
+// and 6.5 to join); 32 trees of 8 over up to 16384, 32 / 8 heads, 60 us (231 MB, 3.9
 // TB/s; what pieces cost between their tiles, and the join); one token over 500, 32 /
 // 32 heads, 12.5 us (32 workgroups at the 33 bytes a clock that the direct loads
 // reach on a CU, and a launch); 2 x 64 tokens over 16000, 64 / 8 heads, 101 us (663
