@@ -1072,3 +1072,44 @@ def test_attention_where_a_kernel_takes_its_most_requests(wq, requests, heads, k
     p = Attn(rng, lengths, counts, heads, kv, dim, 8)
     run(wq, p, max_tokens=max_tokens)
     p.check()
+
+
+@pytest.mark.parametrize("power", [20, 26, 34, 60, 90])
+@pytest.mark.parametrize("lengths,counts,heads,kv,dim,page", [
+    ([500], [1], 4, 4, 128, 16), ([1300, 40], [5, 3], 16, 2, 64, 11), ([900, 0, 2100], [16, 4, 9], 8, 1, 96, 16),
+    ([700, 90], [33, 64], 8, 2, 128, 13), ([4100, 1900], [64, 64], 64, 2, 128, 16), ([1200], [7], 8, 2, 256, 16)])
+def test_attention_scores_of_any_size(wq, power, lengths, counts, heads, kv, dim, page):
+    """Every second token's scores are 2^power times as large.  Queries and keys are small integers, so that scores are
+    exact and their weight is all on the largest, shared where several are equal, whatever the rounding of the product
+    of score and scale (half a step of it is 2^power / 2^24)."""
+    rng = np.random.default_rng(power + heads + dim)
+    p = Attn(rng, lengths, counts, heads, kv, dim, page, tree=lambda n: random_tree(rng, n))
+    p.k64, p.k = bf16(np.rint(1.5 * p.k64))
+    q = np.rint(1.5 * p.q64)
+    q[::2] *= 2.0 ** power
+    p.q64, p.q = bf16(q)
+    run(wq, p, max_tokens=64 if max(counts) > 16 else None)
+    p.check()
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("heads,kv,dim,n,page", [(4, 4, 128, 1, 16), (16, 2, 64, 5, 16), (16, 2, 128, 64, 16), (8, 2, 96, 3, 9),
+                                                 (8, 2, 256, 3, 16)])
+def test_attention_large_equal_scores_weigh_the_same(wq, sign, heads, kv, dim, n, page):
+    """One key at every position: however large (or low) its score, the result is the mean of the values seen."""
+    rng = np.random.default_rng(dim + n)
+    p = Attn(rng, [1100, 30], [n, n], heads, kv, dim, page)
+    p.k64, p.k = bf16(np.broadcast_to(p.k64[0, 0], p.k64.shape).copy())
+    q = sign * np.sign(p.k64[0, 0]).repeat(heads // kv, axis=0) * np.abs(p.q64) * 2.0 ** 36
+    p.q64, p.q = bf16(q)
+    run(wq, p)
+    want = np.zeros_like(p.q64)
+    reach = np.zeros_like(p.q64)
+    for r, length in enumerate(p.lengths):
+        for j in range(n):
+            at = np.arange(length + j + 1)
+            v = p.v64[p.table[r, at // page], at % page].repeat(heads // kv, axis=1)
+            want[p.starts[r] + j], reach[p.starts[r] + j] = v.mean(0), np.abs(v).mean(0)
+    got = f64(p.y)
+    # equal weights round alike and cancel; sums of 1164 values in fp32
+    assert np.all(np.abs(got - want) <= BF16 * np.abs(want) + 2.0 ** -12 * reach)

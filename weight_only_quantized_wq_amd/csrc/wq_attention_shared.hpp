@@ -39,6 +39,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = 4;
 constexpr float kLazy = 8.f;          // powers of two the running maximum may lag behind
+constexpr float kFar = 4194304.f;     // 2^22: from here on a maximum's own rounding moves weights (softmax_step)
 
 struct AttnArgs {
   KvCache c;
@@ -267,6 +268,12 @@ __device__ __forceinline__ bf16x8 ones() {
   return bf16x8{one, one, one, one, one, one, one, one};
 }
 
+// x * scale rounded as the running maximum is: not fused with what follows.
+__device__ __forceinline__ float scaled(float x, float scale) {
+#pragma clang fp contract(off)
+  return x * scale;
+}
+
 // One step of the running softmax over 32 positions: raw scores s in, weights w
 // (bf16, relative to 2^top) out; sums and outputs are rescaled where the
 // running maximum is raised.  That happens only when some score exceeds it by
@@ -276,10 +283,16 @@ __device__ __forceinline__ bf16x8 ones() {
 // They are summed by one more product, with a column of ones: so the sum has the
 // weights that the output has (a row that sees one position gets its value
 // exactly), in the layout of the output's rows.  All else is fp32.
+// The maximum is a rounded product.  One fma for score * scale - maximum keeps
+// that rounding, up to half a step of the maximum, as a common factor of all the
+// row's weights; below 2^22 that is less than 2^0.5 and cancels in the quotient, but
+// from 2^31 on it leaves the range of fp32 (all weights 0, or infinite).  Where a row
+// of the wave has such a maximum (`far`, kept from step to step: it changes only
+// where a maximum does) the product is rounded first.
 template <int R, int CW>
 __device__ __forceinline__ void softmax_step(const f32x4 (&s)[R][2], float scale2, bool whole,
-                                             const uint32_t (&sees)[R], int g, float (&top)[R], f32x4 (&sum)[R],
-                                             f32x4 (&o)[R][CW], bf16x8 (&w)[R]) {
+                                             const uint32_t (&sees)[R], int g, float (&top)[R], bool& far,
+                                             f32x4 (&sum)[R], f32x4 (&o)[R][CW], bf16x8 (&w)[R]) {
   float x[R][8], most[R];
 #pragma unroll
   for (int t = 0; t < R; ++t)
@@ -299,6 +312,7 @@ __device__ __forceinline__ void softmax_step(const f32x4 (&s)[R][2], float scale
     raise |= most[t] > top[t] + kLazy;
   }
   if (__any(raise)) {
+    bool past = false;
 #pragma unroll
     for (int t = 0; t < R; ++t) {
       float m = fmaxf(most[t], __shfl_xor(most[t], 16));
@@ -306,6 +320,7 @@ __device__ __forceinline__ void softmax_step(const f32x4 (&s)[R][2], float scale
       const float now = fmaxf(top[t], m);
       const float f = now == -INFINITY || now == top[t] ? 1.f : __builtin_amdgcn_exp2f(top[t] - now);
       top[t] = now;
+      past |= fabsf(now) >= kFar && now != -INFINITY;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float fr = __shfl(f, 4 * g + i);
@@ -314,13 +329,23 @@ __device__ __forceinline__ void softmax_step(const f32x4 (&s)[R][2], float scale
         for (int j = 0; j < CW; ++j) o[t][j][i] *= fr;
       }
     }
+    far = __any(past);
   }
+  if (__builtin_expect(far, 0)) {
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      const float ref = top[t] == -INFINITY ? 0.f : top[t];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[t][e] = scaled(x[t][e], scale2) - ref;
+    }
+  }
+  const float factor = far ? 1.f : scale2;
 #pragma unroll
   for (int t = 0; t < R; ++t) {
-    const float ref = top[t] == -INFINITY ? 0.f : top[t];
+    const float ref = far || top[t] == -INFINITY ? 0.f : top[t];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      w[t][e] = (__bf16)__builtin_amdgcn_exp2f(fmaf(x[t][e], scale2, -ref));
+      w[t][e] = (__bf16)__builtin_amdgcn_exp2f(fmaf(x[t][e], factor, -ref));
     }
     sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[t], ones(), sum[t], 0, 0, 0);
   }

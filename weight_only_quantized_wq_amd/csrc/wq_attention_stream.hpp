@@ -285,7 +285,7 @@ __global__ __launch_bounds__(W * kWave, (Shape<D, WK, W>::GROUPS)) void attentio
 #pragma unroll
       for (int j = 0; j < CW; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    bool special = false;
+    bool special = false, far = false;
 #pragma unroll 1
     for (int tile = p.t0; tile < p.t1; ++tile) {
 #pragma unroll
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(W * kWave, (Shape<D, WK, W>::GROUPS)) void attentio
             if (__any(found)) special = true;
           }
           bf16x8 w[R];
-          softmax_step<R, CW>(s, a.scale2, whole, sees, g, top, sum, o, w);
+          softmax_step<R, CW>(s, a.scale2, whole, sees, g, top, far, sum, o, w);
 #pragma unroll
           for (int j = 0; j < CW; ++j) {
             const bf16x8 b = v_column<VW>(vw, j);
