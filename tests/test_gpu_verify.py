@@ -1113,3 +1113,48 @@ def test_attention_large_equal_scores_weigh_the_same(wq, sign, heads, kv, dim, n
     got = f64(p.y)
     # equal weights round alike and cancel; sums of 1164 values in fp32
     assert np.all(np.abs(got - want) <= BF16 * np.abs(want) + 2.0 ** -12 * reach)
+
+
+@pytest.mark.parametrize("rank,k,tokens", [(16, 64, 3), (32, 512, 20), (8, 4104, 5), (64, 256, 40), (128, 96, 33)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_lora_infinite_weights_of_b(wq, rank, k, tokens, out):
+    """B's infinities and NaN act on A x as a whole, not on each of the parts that carry it."""
+    import torch
+    rng = np.random.default_rng(rank + k)
+    x = rng.normal(size=(tokens, k))
+    a = rng.normal(size=(2, rank, k)) / np.sqrt(k)
+    x[1], a[0, 0] = 0, 0
+    x[1, 0], a[0, 0, 0] = 1.0, 2.0                     # row 1: A x is exactly 2 at rank 0, whose further parts are 0
+    b = rng.normal(size=(2, 70, rank))
+    x64, xt = bf16(x)
+    a64, at = bf16(a)
+    b64, _ = bf16(b)
+    b64[0, 7, 0], b64[0, 65, 3], b64[0, 30, 5], b64[0, 31, 2] = np.inf, -np.inf, np.nan, np.inf
+    b64[0, 40, 1], b64[0, 40, 4] = np.inf, -np.inf
+    b64[1, 7, 6] = -np.inf
+    adapter = np.array([0 if t % 5 != 4 else 1 for t in range(tokens)])
+    adapter[2] = 1 if tokens < 4 else -1
+    y = torch.zeros(tokens, 70, device="cuda", dtype=torch.float32 if out == "f32" else torch.bfloat16)
+    base = rng.normal(size=(tokens, 70)).astype(np.float32)
+    wq.wq_lora_run(wq.wq_lora_prepare(xt, at, torch.from_numpy(b64).to(torch.bfloat16).cuda(), i32(adapter), y,
+                                      base=torch.from_numpy(base).cuda()))
+    torch.cuda.synchronize()
+    got = f64(y)
+    for t, c in enumerate(adapter):
+        want, tol = base[t].astype(np.float64), np.zeros(70)
+        if c >= 0:
+            h = a64[c] @ x64[t]
+            assert np.abs(h).min() > 1e-5
+            with np.errstate(invalid="ignore"):
+                want = want + b64[c] @ h
+            fine = np.where(np.isfinite(b64[c]), b64[c], 0)
+            tol = 2 * ((k + 8) * 2.0 ** -24 * (np.abs(fine) @ (np.abs(a64[c]) @ np.abs(x64[t]))) +
+                       (3 * rank + 8) * 2.0 ** -24 * (np.abs(fine) @ np.abs(h)))
+            if out == "bf16":
+                tol = tol + 2.0 ** -16 * (np.abs(fine) @ np.abs(h))
+        assert np.array_equal(np.isnan(got[t]), np.isnan(want)), t
+        inf = np.isinf(want)
+        assert np.array_equal(got[t][inf], want[inf]), t
+        ok = np.isfinite(want)
+        tol = tol + 2.0 ** -22 * np.abs(want) + (BF16 * np.abs(want) if out == "bf16" else 0)
+        assert np.all(np.abs(got[t][ok] - want[ok]) <= tol[ok]), t
