@@ -1158,3 +1158,28 @@ def test_lora_infinite_weights_of_b(wq, rank, k, tokens, out):
         ok = np.isfinite(want)
         tol = tol + 2.0 ** -22 * np.abs(want) + (BF16 * np.abs(want) if out == "bf16" else 0)
         assert np.all(np.abs(got[t][ok] - want[ok]) <= tol[ok]), t
+
+
+@pytest.mark.parametrize("power", [-62, -64, -66, 40])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (128, True), (20, False)])
+def test_rope_norm_of_tiny_heads_without_eps(wq, power, f32, rot, interleaved):
+    """mean(x^2) below 2^-126: its fp32 squares are good to 2^-18 of the sum (128 of them, each off by 2^-150 at most)."""
+    import torch
+    rng = np.random.default_rng(60)
+    raw = rng.normal(size=(3, 4 * 128)) * 2.0 ** power
+    qkv64, qkv = bf16(raw)
+    if f32:
+        qkv = qkv.float()
+    _, k = bf16(np.zeros((1, 16, 1, 128)))
+    v, q = k.clone(), torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda")
+    w64, w = bf16(1 + 0.2 * rng.normal(size=128))
+    freq = wq.wq_rope_frequencies(rot, 10000.0)[0]
+    wq.wq_qkv_rope_run(wq.wq_qkv_rope_prepare(qkv, q, k, v, i32([[0]]), i32([0, 3]), i32([2]), freq.cuda(), q_norm=w, k_norm=w,
+                                              eps=0.0, interleaved=interleaved))
+    torch.cuda.synchronize()
+    wq_, wk, _ = verify.qkv_rope(qkv64, np.zeros((1, 16, 1, 128)), np.zeros((1, 16, 1, 128)), np.array([[0]]), [0, 3], [2], 2,
+                                 freq.double().numpy(), q_norm=w64, k_norm=w64, eps=0.0, interleaved=interleaved)
+    for got, want in ((f64(q), wq_), (f64(k)[:, 2:5], wk[:, 2:5])):
+        pair = np.abs(want).max(axis=-1, keepdims=True)
+        assert np.all(np.abs(got - want) <= BF16 * np.abs(want) + 2.0 ** -16 * 1.5 * pair)

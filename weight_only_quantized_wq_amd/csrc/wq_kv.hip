@@ -183,7 +183,17 @@ __device__ __forceinline__ void partners(const float (&x)[8], float (&other)[8],
   }
 }
 
-template <bool F32, int LAYOUT>
+// 1 / sqrt(m).  The instruction takes a subnormal m for 0.  An eps of 2^-126 or more
+// rules that out; below (TINY) such an m is scaled by 2^48, and the result by 2^24.
+// (An instantiation of its own: 4095 rows take 20.3 us with it, 19.6 without.)
+template <bool TINY>
+__device__ __forceinline__ float inverse_root(float m) {
+  if (!TINY) return __builtin_amdgcn_rsqf(m);
+  const bool tiny = m < 0x1p-126f;
+  return __builtin_amdgcn_rsqf(tiny ? m * 0x1p48f : m) * (tiny ? 0x1p24f : 1.f);
+}
+
+template <bool F32, int LAYOUT, bool TINY>
 __global__ __launch_bounds__(kRopeThreads) void qkv_rope_kernel(RopeArgs a) {
   __shared__ float2 turn[128];
   __shared__ float exch[LAYOUT == kOddHalves ? kRopeThreads * 8 : 1];
@@ -258,7 +268,7 @@ __global__ __launch_bounds__(kRopeThreads) void qkv_rope_kernel(RopeArgs a) {
       for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
       sq = group_sum(sq, a.lanes);
       if (!value && (key ? a.k_norm : a.q_norm)) {
-        const float f = __builtin_amdgcn_rsqf(fmaf(sq, a.per_dim, a.eps));
+        const float f = inverse_root<TINY>(fmaf(sq, a.per_dim, a.eps));
         Head8<false> ws;
 #pragma unroll
         for (int i = 0; i < 4; ++i) ws.w[0][i] = key ? weight[1].w[0][i] : weight[0].w[0][i];
@@ -345,14 +355,14 @@ static int rope_check(const char* name, const wq_qkv_rope& a) {
   return WQ_OK;
 }
 
-template <bool F32>
+template <bool F32, bool TINY>
 static void rope_launch(const RopeArgs& r, int layout, dim3 grid, hipStream_t s) {
   if (layout == kPairs)
-    hipLaunchKernelGGL((qkv_rope_kernel<F32, kPairs>), grid, dim3(kRopeThreads), 0, s, r);
+    hipLaunchKernelGGL((qkv_rope_kernel<F32, kPairs, TINY>), grid, dim3(kRopeThreads), 0, s, r);
   else if (layout == kHalves)
-    hipLaunchKernelGGL((qkv_rope_kernel<F32, kHalves>), grid, dim3(kRopeThreads), 0, s, r);
+    hipLaunchKernelGGL((qkv_rope_kernel<F32, kHalves, TINY>), grid, dim3(kRopeThreads), 0, s, r);
   else
-    hipLaunchKernelGGL((qkv_rope_kernel<F32, kOddHalves>), grid, dim3(kRopeThreads), 0, s, r);
+    hipLaunchKernelGGL((qkv_rope_kernel<F32, kOddHalves, TINY>), grid, dim3(kRopeThreads), 0, s, r);
 }
 
 // ---------------------------------------------------------------------------
@@ -531,10 +541,10 @@ extern "C" int wq_qkv_rope_run(const wq_qkv_rope_plan* plan, void* stream) {
   split = split < 1 ? 1 : split > most ? most : split;
   const dim3 grid((unsigned)a.batch.tokens, (unsigned)split);
   const int layout = a.interleaved ? kPairs : a.rot_dim % 16 == 0 ? kHalves : kOddHalves;
-  if (a.qkv_f32)
-    rope_launch<true>(r, layout, grid, (hipStream_t)stream);
-  else
-    rope_launch<false>(r, layout, grid, (hipStream_t)stream);
+  const bool tiny = a.eps < 0x1p-126f && (a.q_norm || a.k_norm);
+  const auto launch = a.qkv_f32 ? (tiny ? rope_launch<true, true> : rope_launch<true, false>)
+                                : (tiny ? rope_launch<false, true> : rope_launch<false, false>);
+  launch(r, layout, grid, (hipStream_t)stream);
   return launch_status(name);
 }
 
