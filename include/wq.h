@@ -481,8 +481,8 @@ int wq_rope_frequencies(int32_t kind, int32_t rot_dim, double base, double facto
  * [rot_dim / 2] on the device; angles are reduced in fp64, all else is fp32,
  * each result rounded to nearest-even once.  rot_dim even, 0 .. head_dim (0:
  * freq may be NULL).  heads a multiple of kv_heads, up to 1024; q and qkv
- * 16-byte aligned, not overlapping, q_stride a multiple of 8; strides at least
- * a row.
+ * 16-byte aligned, their rows not overlapping (WQ_ERR_SHAPE), q_stride a
+ * multiple of 8; strides at least a row.
  */
 typedef struct {
   wq_kv_cache cache;
@@ -525,7 +525,8 @@ int wq_qkv_rope_run(const wq_qkv_rope_plan* plan, void* stream);
  * nothing gets zeros; what a row does not see (NaN and infinities too) does
  * not change it.
  *   q, y  bf16 [tokens][q_stride / y_stride], rows of heads * head_dim,
- *         16-byte aligned, strides multiples of 8; y must not overlap q
+ *         16-byte aligned, strides multiples of 8; rows of y must not overlap
+ *         rows of q (WQ_ERR_SHAPE)
  * A request brings at most max_tokens rows, 1 <= max_tokens <= 64; one that
  * brings more is left alone.  heads / kv_heads <= 64.  scale finite.  requests
  * * kv_heads * row blocks (of 64 rows per key head) * (positions / 32 + 4)
@@ -619,7 +620,8 @@ int wq_kv_accept_run(const wq_kv_accept_plan* plan, void* stream);
  *         not used, whatever it holds)
  *   scale fp32 [adapters] or NULL: 1
  *   y_f32 / y_bf16 [tokens][y_stride], either may be NULL but not both; base
- *         may be y_f32 itself (then with the same stride)
+ *         may be y_f32 itself (then with the same stride), otherwise results
+ *         overlap neither each other nor an input (WQ_ERR_SHAPE)
  * Rows of one adapter share its weights, wherever they stand in the batch.
  * Sums are fp32, and A x is carried to the second product in bf16 parts: three
  * (24 bits), or two (16 bits) where only y_bf16 is asked for.  k % 8 == 0, 8 <= k <= 65536; rank % 8 == 0,

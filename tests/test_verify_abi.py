@@ -202,3 +202,58 @@ def test_the_deal_of_the_largest_batches_stays_in_32_bits(width, rc):
 def test_layers_must_not_lie_on_each_other(layers, rc):
     # a row that one layer's copy overwrites could be another's source; the k of a lone layer is only misaligned
     assert status("accept", layers=layers, layer_stride=0) == rc
+
+
+# rows of 4 heads of 64 (512 bytes) beside rows of 8 (q | k | v, 1024 bytes), five of them
+MEET = [
+    ("rope", dict(q=OK, qkv_bf16=OK)),                                                     # in place
+    ("rope", dict(q=OK + 4096, qkv_bf16=OK)),                                              # the last row
+    ("rope", dict(q=OK, qkv_bf16=OK + 4 * 512)),                                           # the first
+    ("rope", dict(q=OK, qkv_bf16=None, qkv_f32=OK + 4 * 512, qkv_stride=512)),
+    ("rope", dict(q=OK + 1008, qkv_bf16=OK, q_stride=768, qkv_stride=768)),                # columns of one buffer, 8 of them shared
+    ("rope", dict(q=OK + 5 * 1536 - 16, qkv_bf16=OK + 1008, q_stride=256, qkv_stride=768)),
+    ("rope", dict(q=OK + 1024, qkv_bf16=OK, q_stride=776, qkv_stride=768)),                # strides that drift apart, row 33
+    ("attention", dict(q=OK, y=OK + 4 * 512)),
+    ("attention", dict(q=OK + 16, y=OK)),
+    ("attention", dict(q=OK + 496, y=OK, q_stride=512, y_stride=512)),
+    ("lora", dict(x=OK, y_f32=OK + 256)),                                                  # x: 3 rows of 128 bytes
+    ("lora", dict(x=OK, y_f32=None, base=None, y_bf16=OK, y_stride=64)),                   # y in place of x
+    ("lora", dict(x=OK, y_f32=OK + 0x1000 - 16, a=OK + 0x1000)),
+    ("lora", dict(x=OK, y_f32=OK + 0x2000, b=OK + 0x2000)),
+    ("lora", dict(x=OK, y_f32=OK + 0x3000, adapter=OK + 0x3000 + 380)),
+    ("lora", dict(x=OK, y_f32=OK + 0x3000, ranks=OK + 0x3000)),
+    ("lora", dict(x=OK, y_f32=OK + 0x3000, scale=OK + 0x3000)),
+    ("lora", dict(x=OK, y_f32=OK + 0x3000, y_bf16=OK + 0x3000 + 376)),
+    ("lora", dict(x=OK, y_f32=OK + 0x3000, base=OK + 0x3000 + 128)),                       # base a row on
+    ("lora", dict(x=OK, y_f32=None, y_bf16=OK + 0x3000, base=OK + 0x3000)),
+]
+APART = [
+    ("rope", dict(q=OK + 5 * 1024, qkv_bf16=OK)), ("rope", dict(q=OK, qkv_bf16=OK + 5 * 512)),
+    ("rope", dict(q=OK + 1024, qkv_bf16=OK, q_stride=768, qkv_stride=768)),                # columns of one buffer
+    ("rope", dict(q=OK, qkv_bf16=OK + 512, q_stride=768, qkv_stride=768)),
+    ("rope", dict(q=OK + 1024, qkv_bf16=OK, q_stride=768, qkv_stride=768, batch=batch(tokens=1 << 20))),
+    ("attention", dict(q=OK, y=OK + 5 * 512)), ("attention", dict(q=OK + 512, y=OK, q_stride=512, y_stride=512)),
+    ("attention", dict(q=OK, y=OK, batch=batch(tokens=0))),
+    ("lora", dict(x=OK, base=0x13000, y_f32=0x13000, a=0x20000, b=0x30000)),               # base in place
+    ("lora", dict(x=OK, base=0x13080, y_f32=0x13000, a=0x20000, b=0x30000, y_stride=64, base_stride=64)),
+    ("lora", dict(x=OK, base=0x13000, y_f32=0x13000, y_bf16=0x13180, a=0x20000, b=0x30000)),
+]
+
+
+def room(call, kw):
+    """Inputs of their own for adapters, unless the case says otherwise."""
+    return dict(dict(base=0x40000, a=0x20000, b=0x30000, adapter=0x50000, ranks=0x51000, scale=0x52000), **kw) if call == "lora" else kw
+
+
+@pytest.mark.parametrize("call,kw", MEET, ids=str)
+def test_results_must_not_lie_on_what_is_read(call, kw):
+    if kw.get("q_stride") == 776:
+        kw = dict(kw, batch=batch(tokens=34))
+    assert status(call, **room(call, kw)) == 2
+    assert "overlap" in wq.last_error() or "y must not be q" in wq.last_error()
+
+
+@pytest.mark.parametrize("call,kw", APART, ids=str)
+def test_results_beside_what_is_read(call, kw):
+    # accepted, or refused only for want of a device
+    assert status(call, **room(call, kw)) in (0, 4), wq.last_error()

@@ -73,6 +73,23 @@ KvCache device_cache(const wq_kv_cache& c) {
   return d;
 }
 
+bool rows_meet(const ByteRows& a, const ByteRows& b) {
+  if (!a.at || !b.at || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+  // in order of address; rows of one buffer do not overlap (stride >= width, below 2^43)
+  uint64_t x = (uint64_t)(uintptr_t)a.at, y = (uint64_t)(uintptr_t)b.at;
+  const uint64_t xe = x + (uint64_t)(a.rows - 1) * a.stride, ye = y + (uint64_t)(b.rows - 1) * b.stride;
+  if (xe + a.width <= y || ye + b.width <= x) return false;
+  while (x <= xe && y <= ye) {
+    if (x + a.width <= y)
+      x += a.stride;
+    else if (y + b.width <= x)
+      y += b.stride;
+    else
+      return true;
+  }
+  return false;
+}
+
 int plan_device(const char* name, int32_t* device) {
   int rc = check_device();
   if (rc) return rc;
@@ -499,6 +516,13 @@ extern "C" int wq_qkv_rope_prepare(const wq_qkv_rope* a, wq_qkv_rope_plan* plan)
   if (!a || !plan) return fail(WQ_ERR_NULL, "%s: a and plan must be non-null", name);
   int rc = rope_check(name, *a);
   if (rc) return rc;
+  // the workgroups of a row read and write its heads in no order
+  const int64_t dim = a->cache.head_dim, heads = a->heads, all = heads + 2 * a->cache.kv_heads;
+  const int64_t unit = a->qkv_f32 ? 4 : 2;
+  const void* qkv = a->qkv_f32 ? (const void*)a->qkv_f32 : (const void*)a->qkv_bf16;
+  if (rows_meet({a->q, a->batch.tokens, 2 * a->q_stride, 2 * heads * dim},
+                {qkv, a->batch.tokens, unit * a->qkv_stride, unit * all * dim}))
+    return fail(WQ_ERR_SHAPE, "%s: q must not overlap qkv", name);
   wq_qkv_rope_plan p{};
   if ((rc = plan_device(name, &p.device))) return rc;
   p.made = kRopeMade;

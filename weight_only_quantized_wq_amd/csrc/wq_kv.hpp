@@ -67,6 +67,14 @@ inline Batch device_batch(const wq_batch& b) {
   return Batch{b.starts, b.lengths, (int32_t)b.tokens, (int32_t)b.requests};
 }
 
+// Rows of a buffer, in bytes; whether two such buffers share any (columns of one
+// wider buffer side by side do not).
+struct ByteRows {
+  const void* at;
+  int64_t rows, stride, width;
+};
+bool rows_meet(const ByteRows& a, const ByteRows& b);
+
 // The device a plan is bound to: recorded by prepare, compared by run.
 int plan_device(const char* name, int32_t* device);
 int same_device(const char* name, int32_t device);

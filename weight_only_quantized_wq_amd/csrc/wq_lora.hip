@@ -619,6 +619,26 @@ static int lora_check(const char* name, const wq_lora& a) {
   return WQ_OK;
 }
 
+// Results that lie on each other or on what other workgroups may still read (x and
+// the weights, throughout; base, but for the very elements that it is added to).
+static int lora_overlap(const char* name, const wq_lora& a) {
+  const ByteRows y32{a.y_f32, a.tokens, 4 * a.y_stride, 4 * a.n}, y16{a.y_bf16, a.tokens, 2 * a.y_stride, 2 * a.n};
+  const ByteRows base{a.base, a.tokens, 4 * a.base_stride, 4 * a.n};
+  const ByteRows in[] = {{a.x, a.tokens, 2 * a.x_stride, 2 * a.k},
+                         {a.a, 1, 0, 2 * a.adapters * a.rank * a.k},
+                         {a.b, 1, 0, 2 * a.adapters * a.n * a.rank},
+                         {a.adapter, 1, 0, 4 * a.tokens},
+                         {a.ranks, 1, 0, 4 * a.adapters},
+                         {a.scale, 1, 0, 4 * a.adapters}};
+  for (const ByteRows& i : in)
+    if (rows_meet(y32, i) || rows_meet(y16, i))
+      return fail(WQ_ERR_SHAPE, "%s: y must not overlap x, a, b, adapter, ranks or scale", name);
+  if (rows_meet(y32, y16)) return fail(WQ_ERR_SHAPE, "%s: y_f32 must not overlap y_bf16", name);
+  if ((a.base != a.y_f32 && rows_meet(y32, base)) || rows_meet(y16, base))
+    return fail(WQ_ERR_SHAPE, "%s: base must be y_f32 or overlap no result", name);
+  return WQ_OK;
+}
+
 template <int RT>
 static int lora_launch(const char* name, LoraArgs a, hipStream_t s) {
   if constexpr (RT <= 2) {
@@ -679,6 +699,7 @@ extern "C" int wq_lora_prepare(const wq_lora* a, void* workspace, int64_t worksp
     return fail(WQ_ERR_SHAPE, "%s: workspace_bytes = %lld, %lld are needed", name, (long long)workspace_bytes,
                 (long long)need);
   if (!aligned16(workspace)) return fail(WQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", name);
+  if ((rc = lora_overlap(name, *a))) return rc;
   wq_lora_plan p{};
   if ((rc = plan_device(name, &p.device))) return rc;
   p.made = kLoraMade;

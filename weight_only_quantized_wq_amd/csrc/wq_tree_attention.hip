@@ -236,6 +236,10 @@ extern "C" int wq_tree_attention_prepare(const wq_tree_attention* a, void* works
     return fail(WQ_ERR_SHAPE, "%s: workspace_bytes = %lld, %lld are needed", name, (long long)workspace_bytes,
                 (long long)need);
   if (!aligned16(workspace)) return fail(WQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", name);
+  // a group's queries are read by every workgroup that has a share of it
+  const int64_t row = 2 * (int64_t)a->heads * a->cache.head_dim;
+  if (rows_meet({a->q, a->batch.tokens, 2 * a->q_stride, row}, {a->y, a->batch.tokens, 2 * a->y_stride, row}))
+    return fail(WQ_ERR_SHAPE, "%s: y must not overlap q", name);
   wq_tree_attention_plan p{};
   if ((rc = plan_device(name, &p.device))) return rc;
   p.made = kAttnMade;
