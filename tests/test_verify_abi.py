@@ -8,6 +8,7 @@ import torch
 
 import weight_only_quantized_wq_amd as wq
 
+from oracle import verify
 from weight_only_quantized_wq_amd import _binding
 
 BAD = 0x1001
@@ -257,3 +258,11 @@ def test_results_must_not_lie_on_what_is_read(call, kw):
 def test_results_beside_what_is_read(call, kw):
     # accepted, or refused only for want of a device
     assert status(call, **room(call, kw)) in (0, 4), wq.last_error()
+
+
+@pytest.mark.parametrize("kind,high", [("bands", 4.0), (2, 4.0), ("ramp", 32.0), (3, 32.0)])
+def test_rope_frequency_turns_that_a_kind_is_published_with(kind, high):
+    got, scale = wq.wq_rope_frequencies(128, 10000.0, kind, factor=8.0, original=4096.0)
+    want, want_scale = verify.rope_frequencies({2: "bands", 3: "ramp"}.get(kind, kind), 128, 10000.0, 8.0, 1.0, high, 4096.0)
+    assert torch.all((got.double() - torch.from_numpy(want)).abs() <= 2.0 ** -23 * torch.from_numpy(want))
+    assert abs(scale - want_scale) <= 2.0 ** -24 * want_scale

@@ -537,10 +537,13 @@ def _run(name, fn, plan, stream):
         raise WQError(name, rc, lib.wq_last_error().decode(errors="replace"))
 
 
-def wq_rope_frequencies(rot_dim, base, kind="plain", factor=1.0, low=1.0, high=4.0, original=8192.0):
+def wq_rope_frequencies(rot_dim, base, kind="plain", factor=1.0, low=1.0, high=None, original=8192.0):
     """Rotary frequencies as a CPU tensor fp32 [rot_dim / 2], and the rot_scale that goes with them.  kind:
-    "plain", "linear", "bands" or "ramp" (a WQ_ROPE name or code)."""
+    "plain", "linear", "bands" or "ramp" (a WQ_ROPE name or code).  high None: what the kind is published with, 4
+    turns for bands and 32 for a ramp."""
     import torch
+    if high is None:
+        high = 32.0 if WQ_ROPE.get(kind, kind) == WQ_ROPE["ramp"] else 4.0
     freq = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float32)
     scale = ctypes.c_float()
     rc = lib.wq_rope_frequencies(WQ_ROPE.get(kind, kind), rot_dim, base, factor, low, high, original,
