@@ -87,16 +87,20 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 }
 
 // Lane l's 16 (4) bytes at `from` to LDS at `to` + 16 (4) l.  In assembly so that
-// no wait is placed for it but those below.
+// no wait is placed for it but those below; `to` is an operand in m0, so that the
+// compiler itself writes that register (one wait state before its use).
 __device__ __forceinline__ void request16(const void* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(to), "v"(from) : "memory");
 }
-// The same from lane offsets to a uniform address.
+// The same from lane offsets to a uniform address, which scalar additions make: a
+// vector write of `base` would need five wait states before the load (a test reads the
+// listing for that; with them in place one token takes 12.4 us instead of 12.3, wide
+// trees 103 instead of 102).
 __device__ __forceinline__ void request16(const void* base, uint32_t off, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(off), "s"(base) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void request4(const void* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(to), "v"(from) : "memory");
 }
 // All but the N newest requests of this wave are done, its LDS accesses too.
 template <int N>
