@@ -1183,3 +1183,22 @@ def test_rope_norm_of_tiny_heads_without_eps(wq, power, f32, rot, interleaved):
     for got, want in ((f64(q), wq_), (f64(k)[:, 2:5], wk[:, 2:5])):
         pair = np.abs(want).max(axis=-1, keepdims=True)
         assert np.all(np.abs(got - want) <= BF16 * np.abs(want) + 2.0 ** -16 * 1.5 * pair)
+
+
+@pytest.mark.parametrize("rank", [16, 32, 64, 128])
+@pytest.mark.parametrize("rows", [17, 32, 33, 100])
+@pytest.mark.parametrize("out", [("bf16",), ("f32",)])
+def test_lora_tiles_with_a_filled_second_half(wq, rank, rows, out):
+    # more than 16 rows of one adapter, several shares of k, outputs that end inside a wave's 64
+    rng = np.random.default_rng(rank * rows)
+    adapter = rng.permutation([1] * rows + [0, 0, 2, -1, 3])
+    lora_case(wq, rng, adapter, 3, rank, 2056, 133, out=out)
+    lora_case(wq, rng, adapter, 3, rank, 1040, 333, out=out, ranks=[rank, rank - 3, 5], pad=3)
+
+
+@pytest.mark.parametrize("rank,k", [(8, 512), (16, 1024), (32, 1024)])
+@pytest.mark.parametrize("out", [("bf16",), ("f32",)])
+def test_lora_tiles_with_a_filled_second_half_in_one_launch(wq, rank, k, out):
+    rng = np.random.default_rng(rank * k)
+    for rows in (17, 31, 32):
+        lora_case(wq, rng, rng.permutation([1] * rows + [0] * (32 - rows)), 2, rank, k, 650, out=out, ranks=[rank, rank - 1])
