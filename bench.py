@@ -59,10 +59,17 @@ def parse(argv=None):
     return p.parse_args(argv)
 
 
-def source_sha():
+# Sources of the calls between the linears (rotation, attention, acceptance, adapters); no workload here runs them.
+OPERATOR_SOURCES = ("wq_kv.", "wq_tree_attention.", "wq_attention_", "wq_lora.")
+
+
+def source_sha(base=os.path.join(ROOT, "weight_only_quantized_wq_amd", "csrc"), operators=False):
+    """Hash of the kernel sources that the workloads run, or of those of the calls between the linears.  (What both
+    include, wq_device.hpp and wq_host.hpp, counts for the workloads.)"""
     h = hashlib.sha256()
-    base = os.path.join(ROOT, "weight_only_quantized_wq_amd", "csrc")
     for name in sorted(os.listdir(base)):
+        if name.startswith(OPERATOR_SOURCES) != operators:
+            continue
         with open(os.path.join(base, name), "rb") as fh:
             h.update(name.encode() + fh.read())
     return h.hexdigest()[:16]

@@ -196,3 +196,32 @@ def test_tensor_parallel_shards_split_rows_or_inputs():
     s8 = {(m.n, m.k) for m in WORKLOADS["llama3.1-70b-int4-m5-tp8"].matrices()}
     assert s8 == {(1280, 8192), (8192, 1024), (7168, 8192), (8192, 3584), (128256, 8192)}
     assert WORKLOADS["llama3.1-70b-int4-m5-tp8"].m == 5
+
+
+def test_the_hash_of_a_workloads_sources_is_not_moved_by_other_calls(tmp_path):
+    """Counted traffic is reported while the sources of the kernels that were counted hash alike: all of what they
+    include, and nothing of what no workload runs."""
+    import re
+    import shutil
+    import bench
+    csrc = os.path.join(bench.ROOT, "weight_only_quantized_wq_amd", "csrc")
+    names = sorted(os.listdir(csrc))
+    other = [n for n in names if n.startswith(bench.OPERATOR_SOURCES)]
+    assert {"wq_kv.hip", "wq_tree_attention.hip", "wq_lora.hip"} <= set(other)
+    for n in set(names) - set(other):
+        with open(os.path.join(csrc, n)) as fh:
+            assert not set(re.findall(r'#include "([^"]+)"', fh.read())) & set(other), n
+    copy = str(tmp_path / "csrc")
+    shutil.copytree(csrc, copy)
+    linears, operators = bench.source_sha(), bench.source_sha(operators=True)
+    assert bench.source_sha(copy) == linears != operators == bench.source_sha(copy, operators=True)
+    for n in names:
+        path = os.path.join(copy, n)
+        with open(path) as fh:
+            text = fh.read()
+        with open(path, "w") as fh:
+            fh.write(text + "\n")
+        assert (bench.source_sha(copy) == linears) == (n in other), n
+        assert (bench.source_sha(copy, operators=True) == operators) == (n not in other), n
+        with open(path, "w") as fh:
+            fh.write(text)

@@ -4,8 +4,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 namespace wq {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -121,33 +119,6 @@ __device__ __forceinline__ float wave_sum(float v) {
   v += dpp_f<0x140>(v);         // row_mirror
   v += dpp_f<0x142, 0xA>(v);    // row_bcast15 into rows 1 and 3
   v += dpp_f<0x143, 0xC>(v);    // row_bcast31 into rows 2 and 3
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-
-// Sum over the lanes up to and with this one (DPP, lanes a step does not reach add 0).
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast15 into rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast31 into rows 2 and 3
-  return v;
-}
-
-// Wave-wide maximum (lanes a step does not reach see -inf).
-__device__ __forceinline__ float wave_max(float v) {
-  const auto step = [](float x, auto ctrl, auto rows) {
-    return fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp((int)0xFF800000, __float_as_int(x), decltype(ctrl)::value,
-                                                               decltype(rows)::value, 0xF, false)));
-  };
-  using std::integral_constant;
-  v = step(v, integral_constant<int, 0xB1>{}, integral_constant<int, 0xF>{});
-  v = step(v, integral_constant<int, 0x4E>{}, integral_constant<int, 0xF>{});
-  v = step(v, integral_constant<int, 0x141>{}, integral_constant<int, 0xF>{});
-  v = step(v, integral_constant<int, 0x140>{}, integral_constant<int, 0xF>{});
-  v = step(v, integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});
-  v = step(v, integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
