@@ -532,7 +532,9 @@ int wq_qkv_rope_run(const wq_qkv_rope_plan* plan, void* stream);
  * * kv_heads * row blocks (of 64 rows per key head) * (positions / 32 + 4)
  * stays below 2^31, with the positions that the table covers.
  * Scores and sums are fp32 (any finite score, before and after scaling); the
- * weights enter the second product as bf16.
+ * weights enter the second product as bf16.  The weighted values are summed
+ * before the division, with weights of at most 2^8: a row's positions times its
+ * largest value must stay below 2^119.
  *
  * The positions of all requests are cut into equal shares for the launch's
  * workgroups and partial results joined in a fixed order: results are

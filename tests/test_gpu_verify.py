@@ -1202,3 +1202,15 @@ def test_lora_tiles_with_a_filled_second_half_in_one_launch(wq, rank, k, out):
     rng = np.random.default_rng(rank * k)
     for rows in (17, 31, 32):
         lora_case(wq, rng, rng.permutation([1] * rows + [0] * (32 - rows)), 2, rank, k, 650, out=out, ranks=[rank, rank - 1])
+
+
+@pytest.mark.parametrize("scale,power", [(0.0, 118), (2.0 ** -125, 118), (-(2.0 ** -125), 118), (2.0 ** -140, 118), (2.0 ** -110, 104)])
+@pytest.mark.parametrize("heads,n", [(4, 2), (16, 30), (64, 64)])
+def test_attention_scales_next_to_nothing(wq, scale, power, heads, n):
+    # queries and keys are small integers times 2^power: scores up to 2^125 are exact, scaled ones about 1 or none
+    rng = np.random.default_rng(n)
+    p = Attn(rng, [900, 3], [n, n], heads, 2, 64, 16, scale=scale, tree=lambda m: random_tree(rng, m))
+    p.k64, p.k = bf16(np.rint(p.k64))
+    p.q64, p.q = bf16(np.rint(p.q64) * 2.0 ** power)
+    run(wq, p)
+    p.check()

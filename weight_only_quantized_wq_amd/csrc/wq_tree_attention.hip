@@ -1,5 +1,7 @@
 // Attention of drafted tokens over a paged cache and their tree: the joining
 // launch and the host side.  The kernel is in wq_attention_stream.hpp.
+#include <float.h>
+
 #include "wq_attention_stream.hpp"
 
 namespace wq {
@@ -269,8 +271,9 @@ extern "C" int wq_tree_attention_run(const wq_tree_attention_plan* plan, void* s
   a.y_stride = t.y_stride;
   a.tree = t.tree;
   a.parts = static_cast<float*>(plan->workspace);
-  // a negative scale turns the queries over; a zero one leaves equal weights
-  a.scale2 = fmaxf(fabsf(t.scale) * 1.44269504088896340736f, 1e-37f);
+  // a negative scale turns the queries over; a zero one leaves equal weights (2^-149
+  // keeps a hidden score at minus infinity and is far below a step of any weight)
+  a.scale2 = fmaxf(fabsf(t.scale) * 1.44269504088896340736f, FLT_TRUE_MIN);
   a.q_flip = t.scale < 0.f ? 0x80008000u : 0u;
   a.heads = t.heads;
   a.group = t.heads / t.cache.kv_heads;
