@@ -1214,3 +1214,50 @@ def test_attention_scales_next_to_nothing(wq, scale, power, heads, n):
     p.q64, p.q = bf16(np.rint(p.q64) * 2.0 ** power)
     run(wq, p)
     p.check()
+
+
+def test_attention_plans_of_one_stream_share_a_workspace(wq):
+    """As the layers of a model do: runs that follow each other, eager and in one captured graph."""
+    import torch
+    rng = np.random.default_rng(106)
+    ps = [Attn(rng, [3000, 20], [5, 8], 8, 2, 128, 16), Attn(rng, [40, 2500], [8, 3], 8, 2, 128, 16)]
+    ws = torch.empty(wq.wq_tree_attention_workspace_bytes(2, 8, 2, 128, 8), dtype=torch.uint8, device="cuda")
+    plans = [p.plan(wq, max_tokens=8, workspace=ws) for p in ps]
+    for plan in plans:
+        wq.wq_tree_attention_run(plan)
+    torch.cuda.synchronize()
+    for p in ps:
+        p.check()
+    first = [p.y.clone() for p in ps]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for plan in plans:
+            wq.wq_tree_attention_run(plan)
+    for _ in range(3):
+        for p in ps:
+            p.y.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p.y, y) for p, y in zip(ps, first))
+        torch.randn(1000, device="cuda").sum().item()
+
+
+def test_accept_captured_follows_its_buffers(wq):
+    import torch
+    rng = np.random.default_rng(107)
+    k0 = torch.from_numpy(rng.integers(-30000, 30000, (3, 20, 8, 2, 64)).astype(np.int16)).cuda()
+    k, v = k0.clone(), torch.flip(k0, [1]).contiguous()
+    v0 = v.clone()
+    table = rng.permutation(20).astype(np.int32).reshape(2, 10)
+    lengths, path, accepted = i32([3, 17]), i32([[0, 2, 5], [1, 3, 4]]), i32([3, 3])
+    plan = wq.wq_kv_accept_prepare(k, v, i32(table), lengths, path, accepted)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        wq.wq_kv_accept_run(plan)
+    for l, p, n in (([3, 17], [[0, 2, 5], [1, 3, 4]], [3, 3]), ([0, 40], [[1, 2, 3], [0, 1, 7]], [2, 3]), ([9, 1], [[0, 4, 3], [2, 9, 30]], [3, 1])):
+        lengths.copy_(i32(l)), path.copy_(i32(p)), accepted.copy_(i32(n))
+        k.copy_(k0), v.copy_(v0)
+        graph.replay()
+        torch.cuda.synchronize()
+        wk, wv = verify.kv_accept(k0.cpu().numpy(), v0.cpu().numpy(), table, l, np.array(p), n)
+        assert np.array_equal(k.cpu().numpy(), wk) and np.array_equal(v.cpu().numpy(), wv)
