@@ -476,8 +476,9 @@ int wq_rope_frequencies(int32_t kind, int32_t rot_dim, double base, double facto
  *         (i, i + rot_dim / 2); the others as they are
  *   q     bf16 [tokens][q_stride] out; keys and values (bf16) go to the
  *         cache rows of the tokens
- * positions int32 [tokens], or NULL: cache positions (drafts of a tree turn
- * by their depth, which is not their place in the cache).  freq fp32
+ * positions int32 [tokens], or NULL: cache positions, lengths[r] + j (right for
+ * one token and for a chain; a draft of a tree stands at lengths[r] + its depth
+ * in the tree, which is not its place in the cache).  freq fp32
  * [rot_dim / 2] on the device; angles are reduced in fp64, all else is fp32,
  * each result rounded to nearest-even once.  rot_dim even, 0 .. head_dim (0:
  * freq may be NULL).  heads a multiple of kv_heads, up to 1024; q and qkv

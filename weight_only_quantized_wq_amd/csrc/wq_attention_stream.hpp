@@ -19,19 +19,19 @@
 // head:
 //   * WK = 1, blocks of 16 R W rows: every wave owns 16 R rows from the first
 //     position of a piece to the last and reads the whole tile; nothing is
-//     joined inside the workgroup.  Two workgroups of W = 4 waves share a CU, or
-//     one of 8 waves with R = 2, whose blocks of 256 rows pay half as much for
-//     each tile's way to LDS.
+//     joined inside the workgroup.  Two workgroups of W = 4 waves share a CU (while
+//     the deal leaves room for both, see attn_grid), or one of 8 waves with R = 2,
+//     whose blocks of 256 rows pay half as much for each tile's way to LDS.
 //   * WK = 4, up to 16 rows: all waves have the same rows and take 32 positions
 //     of a tile of 128 each, so that a short context is a few steps long; they
 //     meet in LDS at the end of a piece.
 // Measured (MI355X, heads of 128), with the joining launch: 5 tokens over 32763
-// positions, 64 / 8 heads, 39.4 us (134 MB, 3.4 TB/s; about 5 us until the ring runs
-// and 6.5 to join); 32 trees of 8 over up to 16384, 32 / 8 heads, 60 us (231 MB, 3.9
+// positions, 64 / 8 heads, 39.7 us (134 MB, 3.4 TB/s; about 5 us until the ring runs
+// and 6.5 to join); 32 trees of 8 over up to 16384, 32 / 8 heads, 61 us (231 MB, 3.8
 // TB/s; what pieces cost between their tiles, and the join); one token over 500, 32 /
-// 32 heads, 12.5 us (32 workgroups at the 33 bytes a clock that the direct loads
-// reach on a CU, and a launch); 2 x 64 tokens over 16000, 64 / 8 heads, 101 us (663
-// TFLOP/s: vector ALU 51 % and matrix pipe 32 % of the cycles, LDS 26 %, and too
+// 32 heads, 12.3 us (32 workgroups at the 33 bytes a clock that the direct loads
+// reach on a CU, and a launch); 2 x 64 tokens over 16000, 64 / 8 heads, 103 us (656
+// TFLOP/s: vector ALU 48 % and matrix pipe 33 % of the cycles, LDS 25 %, and too
 // little of each beside the other).  For such trees 4 waves of 32 rows, two
 // workgroups per CU, take 136 us.
 // Page numbers of 8 rows against every row's: 32 trees of 8 65 / 87 us, 2 x 64 tokens

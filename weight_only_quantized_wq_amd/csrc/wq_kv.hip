@@ -123,7 +123,7 @@ int same_device(const char* name, int32_t device) {
 // (interleaved), in a lane a fixed distance away (halves of a multiple of 8) or
 // fetched through LDS (other halves).
 //
-// Measured (MI355X): 4095 rows of 32 / 8 heads of 128 with norms, 22-24 us (101 MB, 4.4
+// Measured (MI355X): 4095 rows of 32 / 8 heads of 128 with norms, 22 us (101 MB, 4.6
 // TB/s), where the vector ALU is busy most of the time and waves in plenty hide the
 // rest: one head at a time and 64 registers, since four requested at once (80
 // registers) took 27.0 us, two 26.4.  32 x 5 rows of 64 / 8 heads, fp32: 4.9 us, 9.8

@@ -19,7 +19,7 @@
 // Weights are read once per tile.  Measured (MI355X): 32 x 5 rows of 28 adapters,
 // rank 32, k = 8192, n = 10240: 18.1 us, 43 MB, of which the two launches' own
 // cost and the search are about 8; 8 x 128 rows of 4 adapters, rank 64, k = 4096, n =
-// 22016: 48.5 us, 157 MB (of it the second launch 39 us, 135 MB, 3.5 TB/s under the
+// 22016: 48.9 us, 157 MB (of it the second launch 39 us, 135 MB, 3.5 TB/s under the
 // registers' two waves per SIMD); one row: launches.
 #include <math.h>
 

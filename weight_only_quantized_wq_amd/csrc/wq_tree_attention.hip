@@ -110,6 +110,12 @@ constexpr int64_t kAttnMade = 0x77715f6174746e31;
 // second, 32 / 8 heads: 64 tokens over 1984 positions 26.3 / 21.4, over 8128 34.8 /
 // 35.0; 4 x 64 over 448 32.2 / 26.9, over 1984 36.7 / 37.3, over 8128 68 / 88; 16 x 64
 // over 448 33 / 28, over 1984 83 / 88, over 8128 208 / 291.
+// The positions are those that the table covers, since the lengths are known on the
+// device only: short contexts in a wide table take the third kernel where the second
+// is faster (4 x 64 over 448, 32 / 8 heads: 27.0 us with a table of 512 positions,
+// 30.2 with 1024 to 2048, where the second kernel has a joining launch, 35.2 from 4096
+// on; 16 x 64 over 448 28.4 and 38.7 from 1024 on; 64 over 1984 23.2 and 27.7 with
+// 32768).
 enum { kRows16 = 0, kRows64 = 1, kRowsMany = 2 };
 constexpr int64_t kGroups16 = 256;
 constexpr int64_t kRequestsMany = 2048;
@@ -123,7 +129,10 @@ static int attn_variant(int64_t requests, int heads, int kv_heads, int head_dim,
   return rows <= 64 || small || requests > kRequestsMany ? kRows64 : kRowsMany;
 }
 
-// Workgroups of a launch: as many as are resident.
+// Workgroups of a launch: as many as are resident while two (with WK = 1 and 4
+// waves) fit a CU's 160 KB of LDS.  Each holds the deal, 12 bytes per request, behind
+// its ring: up to about 480 requests with heads of 96, 1250 with 128, 3980 with 64.
+// With more the 512 run in two rounds.
 static int attn_grid(int variant, int head_dim) {
   return variant == kRows16 || (variant == kRowsMany && head_dim != 96) || head_dim == 256 ? 256 : 512;
 }
@@ -136,7 +145,10 @@ static int attn_rows(int variant, int head_dim) {
 // needed.  Measured, 256 / 512 / 1024 positions, heads of 128: one token over 500
 // positions, 32 key heads, 11.7 / 12.1 / 12.1 us; 16 requests of 500, 8 key heads,
 // 17.6 / 15.2 / 15.2; 5 tokens over 700, 8 key heads, 13.5 / 13.5 / 25.6; 64 such
-// requests 55.2 / 55.2 / 48.9.
+// requests 55.2 / 55.2 / 48.9.  The joining launch is left out by the table's width,
+// not by the lengths: with a table of more than 512 positions a run over short contexts
+// pays 2.4 us for a launch that joins nothing (one token over 500 12.2 / 14.6, 8 x 5
+// over 500, 8 key heads, 18.6 / 21.1).
 constexpr int kUncutPositions = 512;
 // Workgroups of the joining launch, each of which computes the deal once.  Measured,
 // 512 / 1024 / one per four rows: 32 x 32 tokens over 500 positions 39.1 / 37.8 / 46.4
