@@ -266,3 +266,15 @@ def test_rope_frequency_turns_that_a_kind_is_published_with(kind, high):
     want, want_scale = verify.rope_frequencies({2: "bands", 3: "ramp"}.get(kind, kind), 128, 10000.0, 8.0, 1.0, high, 4096.0)
     assert torch.all((got.double() - torch.from_numpy(want)).abs() <= 2.0 ** -23 * torch.from_numpy(want))
     assert abs(scale - want_scale) <= 2.0 ** -24 * want_scale
+
+
+@pytest.mark.parametrize("name", ["adapter", "ranks", "scale", "a", "b"])
+@pytest.mark.timeout(20, method="thread")
+def test_inputs_between_the_rows_of_a_padded_result(name):
+    # results of 128 bytes every 512 (b: every 2048): an input of one piece in the gap behind the first or second row
+    wide = 512 if name in ("a", "b") else 128
+    for row in (0, 1):
+        kw = dict(x=OK, y_f32=0x13000, y_stride=wide, k=8, x_stride=8, **{name: 0x13000 + row * 4 * wide + 144})
+        assert status("lora", **room("lora", kw)) in (0, 4), wq.last_error()
+        kw[name] = 0x13000 + row * 4 * wide + 112
+        assert status("lora", **room("lora", kw)) == (3 if name in ("a", "b") and kw[name] % 16 else 2)

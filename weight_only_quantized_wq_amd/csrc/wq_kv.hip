@@ -75,15 +75,17 @@ KvCache device_cache(const wq_kv_cache& c) {
 
 bool rows_meet(const ByteRows& a, const ByteRows& b) {
   if (!a.at || !b.at || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
-  // in order of address; rows of one buffer do not overlap (stride >= width, below 2^43)
+  // in order of address; rows of one buffer do not overlap (stride >= width, below
+  // 2^43; of a single row it may be anything)
   uint64_t x = (uint64_t)(uintptr_t)a.at, y = (uint64_t)(uintptr_t)b.at;
-  const uint64_t xe = x + (uint64_t)(a.rows - 1) * a.stride, ye = y + (uint64_t)(b.rows - 1) * b.stride;
+  const uint64_t xs = a.rows > 1 ? a.stride : a.width, ys = b.rows > 1 ? b.stride : b.width;
+  const uint64_t xe = x + (a.rows - 1) * xs, ye = y + (b.rows - 1) * ys;
   if (xe + a.width <= y || ye + b.width <= x) return false;
   while (x <= xe && y <= ye) {
     if (x + a.width <= y)
-      x += a.stride;
+      x += xs;
     else if (y + b.width <= x)
-      y += b.stride;
+      y += ys;
     else
       return true;
   }
