@@ -667,6 +667,76 @@ int64_t wq_lora_workspace_bytes(int64_t tokens, int64_t k, int64_t adapters, int
 int wq_lora_prepare(const wq_lora* a, void* workspace, int64_t workspace_bytes, wq_lora_plan* plan);
 int wq_lora_run(const wq_lora_plan* plan, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* MXFP4 weights and activations, and a block around them -- [TAGS] "Grouped */
+/* Quantization" (grouped quantization parameters; here 4-bit floats under a */
+/* power of two per group of 32).                                            */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * MXFP4: groups of 32 consecutive inputs of one row.  A code is a 4-bit float
+ * (sign, 2 exponent bits, 1 mantissa bit): 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives; a value is code * 2^(scale - 127), scale one byte per group, 255
+ * making the whole group NaN.
+ *   in : w_f32 fp32 or w_bf16 bf16 [n][k] (exactly one), k % 32 == 0
+ *   out: q     u8 [n][k/2]    byte j = code(2j) | code(2j+1) << 4
+ *        scale u8 [n][k/32]   max(floor(log2 max |w|) - 2, -127) + 127, the
+ *                             smallest byte for a group of zeros
+ * code = the nearest to w / 2^(scale - 127), ties to the even code, magnitudes
+ * past 6 to 6.  A group that holds an infinity or a NaN gets scale 255 and
+ * codes 0.  17/32 byte per weight.  w, q 16-byte aligned; n * k <= 2^40;
+ * nothing overlaps (WQ_ERR_SHAPE).  Bit-identical to the CPU oracle.
+ */
+int wq_quantize_mxfp4(const float* w_f32, const uint16_t* w_bf16, int64_t n, int64_t k, uint8_t* q, uint8_t* scale,
+                      void* stream);
+
+/*
+ * The values that codes stand for, as fp32 or bf16 [n][k] (exactly one; both
+ * hold them exactly, but values past the largest finite one, which scale bytes
+ * of 253 and 254 reach, are infinite).  q, y 16-byte aligned.
+ */
+int wq_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int64_t n, int64_t k, float* y_f32, uint16_t* y_bf16,
+                        void* stream);
+
+/*
+ * y = x W^T for any number of rows, W in MXFP4 (q, scale as above, [n][k]):
+ *   x     bf16 [m][x_stride], or in MXFP4 xq [m][k/2] with x_scale [m][k/32]
+ *         (exactly one of x and xq)
+ *   y     fp32 and / or bf16 [m][y_stride], either may be NULL but not both
+ * Sums are fp32.  A weight is its value as wq_dequantize_mxfp4 gives it.
+ * 0 <= m <= 2^20, 0 <= n <= 2^24, k a multiple of 32, 32 .. 2^18; x, xq, q
+ * 16-byte aligned, x_stride a multiple of 8; scale and x_scale 4-byte aligned
+ * (their last 4-byte word is read whole); y overlaps nothing (WQ_ERR_SHAPE).
+ * A prepare and a run, as for the calls of a verify pass; `workspace` as there.
+ */
+typedef struct {
+  const uint16_t* x;
+  int64_t x_stride;
+  const uint8_t* xq;
+  const uint8_t* x_scale;
+  const uint8_t* q;
+  const uint8_t* scale;
+  float* y_f32;
+  uint16_t* y_bf16;
+  int64_t y_stride;
+  int64_t m;
+  int64_t n;
+  int64_t k;
+} wq_gemm_mxfp4;
+
+typedef struct {
+  int64_t made;        /* set by prepare */
+  int32_t device;
+  int32_t reserved;
+  void* workspace;
+  wq_gemm_mxfp4 a;
+} wq_gemm_mxfp4_plan;
+
+/* Workspace of a plan with these sizes (0 if they are not supported). */
+int64_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int wq_gemm_mxfp4_prepare(const wq_gemm_mxfp4* a, void* workspace, int64_t workspace_bytes, wq_gemm_mxfp4_plan* plan);
+int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream);
+
 /* Static text for a wq_status value ("unknown status" otherwise). */
 const char* wq_status_string(int status);
 

@@ -11,6 +11,8 @@ _EXPORTS = (
     "LIB_PATH", "WQError", "WQ_STATUS", "lib", "status_string", "last_error",
     "wq_quantize_int8", "wq_quantize_int4g32", "wq_quantize_int4",
     "wq_gemv_bf16", "wq_gemv_int8", "wq_gemv_int4g32", "wq_gemv_int4", "wq_gemm_smallM", "wq_gemm_smallM_int4", "wq_gemm_smallM_int8",
+    "wq_quantize_mxfp4", "wq_dequantize_mxfp4",
+    "wq_gemm_mxfp4", "wq_gemm_mxfp4_plan", "wq_gemm_mxfp4_workspace_bytes", "wq_gemm_mxfp4_prepare", "wq_gemm_mxfp4_run",
     "moe_top2_gemv", "moe_top2_gemv_noalloc",
     "WQ_FORMAT", "wq_matrix", "wq_step_plan",
     "wq_decode_step_workspace_bytes", "wq_decode_step_prepare", "wq_decode_step_run",

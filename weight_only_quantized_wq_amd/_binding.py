@@ -32,6 +32,8 @@ _SIGNATURES = {
     "wq_gemm_smallM": [_P, _I64, _P, _P, _I64, _I64, _P, _P, _P],
     "wq_gemm_smallM_int8": [_P, _I64, _P, _P, _I64, _I64, _P, _P, _P],
     "wq_gemm_smallM_int4": [_P, _I64, _P, _P, _I64, _I64, _I32, _P, _P, _P],
+    "wq_quantize_mxfp4": [_P, _P, _I64, _I64, _P, _P, _P],
+    "wq_dequantize_mxfp4": [_P, _P, _I64, _I64, _P, _P, _P],
     "moe_top2_gemv": [_P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P],
     "moe_top2_gemv_noalloc": [_P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P],
 }
@@ -94,6 +96,11 @@ class wq_lora(ctypes.Structure):
                 ("tokens", _I64), ("k", _I64), ("n", _I64), ("adapters", _I64), ("rank", _I32)]
 
 
+class wq_gemm_mxfp4(ctypes.Structure):
+    _fields_ = [("x", _P), ("x_stride", _I64), ("xq", _P), ("x_scale", _P), ("q", _P), ("scale", _P), ("y_f32", _P),
+                ("y_bf16", _P), ("y_stride", _I64), ("m", _I64), ("n", _I64), ("k", _I64)]
+
+
 # Plans: ctypes instances take further attributes, and `keep` holds the tensors
 # a plan's addresses point into for as long as the plan lives.
 class wq_qkv_rope_plan(ctypes.Structure):
@@ -111,6 +118,10 @@ class wq_kv_accept_plan(ctypes.Structure):
 class wq_lora_plan(ctypes.Structure):
     _fields_ = [("made", _I64), ("device", _I32), ("tiles", _I32), ("splits", _I32), ("reserved", _I32),
                 ("workspace", _P), ("a", wq_lora)]
+
+
+class wq_gemm_mxfp4_plan(ctypes.Structure):
+    _fields_ = [("made", _I64), ("device", _I32), ("reserved", _I32), ("workspace", _P), ("a", wq_gemm_mxfp4)]
 
 
 WQ_ROPE = {"plain": 0, "linear": 1, "bands": 2, "ramp": 3}
@@ -156,6 +167,8 @@ def _load():
     lib.wq_tree_attention_workspace_bytes.restype = _I64
     lib.wq_lora_workspace_bytes.argtypes = [_I64, _I64, _I64, _I32]
     lib.wq_lora_workspace_bytes.restype = _I64
+    lib.wq_gemm_mxfp4_workspace_bytes.argtypes = [_I64] * 3
+    lib.wq_gemm_mxfp4_workspace_bytes.restype = _I64
     # prepare and run are called with ctypes.byref of the structures above
     lib.wq_qkv_rope_prepare.argtypes = [_P, _P]
     lib.wq_qkv_rope_run.argtypes = [_P, _P]
@@ -165,6 +178,8 @@ def _load():
     lib.wq_kv_accept_run.argtypes = [_P, _P]
     lib.wq_lora_prepare.argtypes = [_P, _P, _I64, _P]
     lib.wq_lora_run.argtypes = [_P, _P]
+    lib.wq_gemm_mxfp4_prepare.argtypes = [_P, _P, _I64, _P]
+    lib.wq_gemm_mxfp4_run.argtypes = [_P, _P]
     lib.wq_status_string.argtypes = [ctypes.c_int]
     lib.wq_status_string.restype = ctypes.c_char_p
     lib.wq_last_error.argtypes = []
@@ -311,6 +326,18 @@ def wq_gemm_smallM_int8(x, m, q, scale, n, k, y_f32=None, y_bf16=None, stream=No
     _call("wq_gemm_smallM_int8", _ptr(x, ok and 2 * m * k, "x"), m, _ptr(q, ok and n * k, "q"),
           _ptr(scale, ok and 2 * n, "scale"), n, k, _ptr(y_f32, ok and 4 * m * n, "y_f32"),
           _ptr(y_bf16, ok and 2 * m * n, "y_bf16"), _stream(stream))
+
+
+def wq_quantize_mxfp4(w_f32, w_bf16, n, k, q, scale, stream=None):
+    ok = _nonneg(n, k)
+    _call("wq_quantize_mxfp4", _ptr(w_f32, ok and 4 * n * k, "w_f32"), _ptr(w_bf16, ok and 2 * n * k, "w_bf16"), n, k,
+          _ptr(q, ok and n * k // 2, "q"), _ptr(scale, ok and n * k // 32, "scale"), _stream(stream))
+
+
+def wq_dequantize_mxfp4(q, scale, n, k, y_f32=None, y_bf16=None, stream=None):
+    ok = _nonneg(n, k)
+    _call("wq_dequantize_mxfp4", _ptr(q, ok and n * k // 2, "q"), _ptr(scale, ok and n * k // 32, "scale"), n, k,
+          _ptr(y_f32, ok and 4 * n * k, "y_f32"), _ptr(y_bf16, ok and 2 * n * k, "y_bf16"), _stream(stream))
 
 
 def _moe_bytes(e, dim, f):
@@ -691,3 +718,68 @@ def wq_lora_prepare(x, a, b, adapter, y, y2=None, base=None, ranks=None, scale=N
 
 def wq_lora_run(plan, stream=None):
     _run("wq_lora_run", lib.wq_lora_run, plan, stream)
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 products and the block around them: plans, as above.
+
+
+def _outputs(y, y2, shape, device):
+    """Addresses of an fp32 and a bf16 result (either may be missing) and their row stride."""
+    out = {"f32": None, "bf16": None}
+    for t, what in ((y, "y"), (y2, "y2")):
+        if t is None:
+            continue
+        _view(t, what, 2, ("float32",) + _BF16, device)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"libwq: {what} must be {shape}, not {tuple(t.shape)}")
+        kind = "f32" if str(t.dtype) == "torch.float32" else "bf16"
+        if out[kind] is not None:
+            raise ValueError("libwq: y and y2 must be one fp32 and one bf16")
+        out[kind] = t
+    strides = {_row_stride(t, shape[1]) for t in out.values() if t is not None}
+    if len(strides) > 1:
+        raise ValueError("libwq: y and y2 must have the same row stride")
+    return [None if t is None else _at(t) for t in out.values()], max(strides, default=0)
+
+
+def _mx_view(q, scale, what, dims, device):
+    """MXFP4 codes [..., n, k / 2] and scales [..., n, k / 32], contiguous; k."""
+    _view(q, what, dims, ("uint8",), device)
+    _view(scale, f"the scales of {what}", dims, ("uint8",), q.device)
+    if not q.is_contiguous() or not scale.is_contiguous():
+        raise ValueError(f"libwq: {what} and its scales must be contiguous")
+    if q.shape[:-1] != scale.shape[:-1] or q.shape[-1] != 16 * scale.shape[-1]:
+        raise ValueError(f"libwq: {what} {tuple(q.shape)} and its scales {tuple(scale.shape)} do not go together")
+    return 2 * q.shape[-1]
+
+
+def wq_gemm_mxfp4_workspace_bytes(m, n, k):
+    return int(lib.wq_gemm_mxfp4_workspace_bytes(m, n, k))
+
+
+def wq_gemm_mxfp4_prepare(x, q, scale, y, y2=None, x_scale=None, workspace=None):
+    """x bf16 [m, k], or uint8 codes [m, k / 2] with x_scale uint8 [m, k / 32]; q uint8 [n, k / 2], scale uint8
+    [n, k / 32]; y fp32 or bf16 [m, n], y2 the other of the two (same row stride) or None."""
+    device = getattr(x, "device", None)
+    k = _mx_view(q, scale, "q", 2, device)
+    n = q.shape[0]
+    if x_scale is None:
+        _view(x, "x", 2, _BF16, device)
+        if x.shape[1] != k:
+            raise ValueError(f"libwq: x {tuple(x.shape)} does not go with q {tuple(q.shape)}")
+        ins = (_at(x), _row_stride(x, k), None, None)
+    else:
+        if _mx_view(x, x_scale, "x", 2, device) != k:
+            raise ValueError(f"libwq: x {tuple(x.shape)} does not go with q {tuple(q.shape)}")
+        ins = (None, 0, _at(x), _at(x_scale))
+    m = x.shape[0]
+    outs, y_stride = _outputs(y, y2, (m, n), device)
+    a = wq_gemm_mxfp4(*ins, _at(q), _at(scale), *outs, y_stride, m, n, k)
+    workspace, nbytes = _workspace(workspace, wq_gemm_mxfp4_workspace_bytes(m, n, k), device)
+    return _prepare("wq_gemm_mxfp4_prepare", wq_gemm_mxfp4_plan(), device, (x, q, scale, y, y2, x_scale, workspace),
+                    ctypes.byref(a), _at(workspace), nbytes)
+
+
+def wq_gemm_mxfp4_run(plan, stream=None):
+    _run("wq_gemm_mxfp4_run", lib.wq_gemm_mxfp4_run, plan, stream)

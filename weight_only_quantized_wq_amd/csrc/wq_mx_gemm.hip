@@ -1,0 +1,202 @@
+// y = x W^T with W in MXFP4 and x in bf16 or MXFP4.
+//
+// Few rows (mx_rows_kernel) are bound by W's bytes: a workgroup takes a block of 16-row
+// tiles, its waves split the row's spans (and, for short rows, the tiles), and their
+// sums meet in LDS in a fixed order.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "wq_host.hpp"
+#include "wq_kv.hpp"
+#include "wq_row_stream.hpp"
+
+namespace wq {
+
+struct MxRowsArgs {
+  StreamWeights w;
+  const char* x;          // bf16 rows, or codes
+  const uint8_t* xscale;
+  int64_t x_stride;       // bytes
+  uint32_t x_bytes;       // of a row
+  float* y32;
+  uint16_t* y16;
+  int64_t y_stride;
+  int64_t m;
+  int32_t tiles;          // of 16 rows of W
+  int32_t per;            // tiles of a workgroup
+  int32_t ways;           // waves that share a tile's spans
+  int32_t spans;
+};
+
+constexpr int row_tiles(bool xq) { return xq ? 8 : 16; }      // at most, of a wave
+
+template <bool XQ, bool ODD, int COLS, int WAVES, int P>
+__global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxRowsArgs a) {
+  using S = RowStream<true, XQ, ODD, COLS, P>;
+  constexpr int kRowTiles = row_tiles(XQ);
+  constexpr int kRed = WAVES * kRowTiles * 1024, kAll = WAVES * S::kBytes;
+  __shared__ __align__(1024) char lds[kAll > kRed ? kAll : kRed];
+  const int wave = wave_id(), ways = a.ways, kw = wave % ways, tw = wave / ways, teams = WAVES / ways;
+  const S s(lds + wave * S::kBytes);
+  const int first = (int)blockIdx.x * a.per, mine = min(a.per, a.tiles - first);
+  const int64_t m0 = (int64_t)blockIdx.y * COLS;
+  const int cols = (int)min((int64_t)COLS, a.m - m0);
+  f32x4 acc[kRowTiles];
+#pragma unroll
+  for (int t = 0; t < kRowTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int tiles = (mine - tw + teams - 1) / teams;
+  const char* x = a.x + m0 * a.x_stride;
+  s.template run<kRowTiles>(
+      a.w, tiles, kw, ways, a.spans, (int)a.w.srow,
+      [&](int t, int64_t& row0, int& left) {
+        row0 = (int64_t)(first + tw + t * teams) * 16;
+        left = (int)min((int64_t)16, a.w.rows - row0);
+      },
+      [&](int col) { return x + min(col, cols - 1) * a.x_stride; }, a.x_bytes, a.xscale, a.m, m0, cols, acc);
+  // the waves' sums of a tile, lane by lane
+  __syncthreads();
+  for_tiles<kRowTiles>(tiles, [&](auto at) __attribute__((always_inline)) {
+    *reinterpret_cast<f32x4*>(lds + (wave * kRowTiles + at.value) * 1024 + s.lane * 16) = acc[at.value];
+  });
+  __syncthreads();
+  for (int o = (int)threadIdx.x; o < mine * 16 * cols; o += WAVES * 64) {
+    const int row = o & 15, col = (o >> 4) % cols, tile = (o >> 4) / cols;
+    const char* from = lds + ((tile % teams) * ways * kRowTiles + tile / teams) * 1024 + ((row >> 2) * 16 + col) * 16 + (row & 3) * 4;
+    float v = 0.f;
+    for (int w = 0; w < ways; ++w) v += *reinterpret_cast<const float*>(from + w * kRowTiles * 1024);
+    const int64_t r = (int64_t)(first + tile) * 16 + row;
+    if (r >= a.w.rows) continue;
+    const int64_t at = (m0 + col) * a.y_stride + r;
+    if (a.y32) gmem(a.y32)[at] = v;
+    if (a.y16) gmem(a.y16)[at] = f32_to_bf16(v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+
+constexpr int64_t kGemmMade = 0x77715f6d78676d31;
+constexpr int64_t kGemmMaxM = 1 << 20, kGemmMaxN = 1 << 24, kGemmMaxK = 1 << 18;
+
+// Tiles per workgroup and waves per tile: the fewest units in the longest chain, with
+// two units' worth for what a workgroup costs besides.
+static void rows_plan(MxRowsArgs& a, int waves, int most, int64_t chunks) {
+  double best = 1e300;
+  for (int ways = 1; ways <= waves; ways *= 2) {
+    const int teams = waves / ways;
+    for (int t = 1; t <= most; ++t) {
+      const int per = t * teams;
+      const int64_t groups = (int64_t)((a.tiles + per - 1) / per) * chunks;
+      const int64_t rounds = (groups + 255) / 256;
+      const double cost = (double)rounds * ((double)t * ((a.spans + ways - 1) / ways) + 2.0);
+      if (cost < best) {
+        best = cost;
+        a.per = per;
+        a.ways = ways;
+      }
+    }
+  }
+}
+
+template <bool XQ, int COLS, int WAVES, int P>
+static int rows_launch(const char* name, MxRowsArgs a, hipStream_t s) {
+  const int64_t chunks = (a.m + COLS - 1) / COLS;
+  rows_plan(a, WAVES, row_tiles(XQ), chunks);
+  const dim3 grid((unsigned)((a.tiles + a.per - 1) / a.per), (unsigned)chunks);
+  if (a.w.srow % 4)
+    hipLaunchKernelGGL((mx_rows_kernel<XQ, true, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
+  else
+    hipLaunchKernelGGL((mx_rows_kernel<XQ, false, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
+  return launch_status(name);
+}
+
+static int gemm_check(const char* name, const wq_gemm_mxfp4& a) {
+  if (!a.x == !a.xq) return fail(WQ_ERR_NULL, "%s: exactly one of x and xq must be given", name);
+  if (a.xq && !a.x_scale) return fail(WQ_ERR_NULL, "%s: xq needs x_scale", name);
+  if (!a.q || !a.scale) return fail(WQ_ERR_NULL, "%s: q and scale must be non-null", name);
+  if (!a.y_f32 && !a.y_bf16) return fail(WQ_ERR_NULL, "%s: at least one of y_f32 / y_bf16 must be non-null", name);
+  if (a.m < 0 || a.m > kGemmMaxM || a.n < 0 || a.n > kGemmMaxN || a.k < kMxGroup || a.k > kGemmMaxK || a.k % kMxGroup)
+    return fail(WQ_ERR_SHAPE, "%s: m = %lld (0..2^20), n = %lld (0..2^24), k = %lld (a multiple of 32 up to 2^18)", name,
+                (long long)a.m, (long long)a.n, (long long)a.k);
+  const int64_t most = (int64_t)1 << 40;
+  if (a.x && (a.x_stride < a.k || a.x_stride > most || a.x_stride % 8))
+    return fail(WQ_ERR_SHAPE, "%s: x_stride = %lld must be a multiple of 8 and hold a row", name, (long long)a.x_stride);
+  if (a.y_stride < a.n || a.y_stride > most)
+    return fail(WQ_ERR_SHAPE, "%s: y_stride = %lld must hold a row", name, (long long)a.y_stride);
+  if (!aligned16(a.x) || !aligned16(a.xq) || !aligned16(a.q))
+    return fail(WQ_ERR_ALIGN, "%s: x, xq and q must be 16-byte aligned", name);
+  if (((uintptr_t)a.x_scale & 3) || ((uintptr_t)a.scale & 3) || ((uintptr_t)a.y_f32 & 3) || ((uintptr_t)a.y_bf16 & 1))
+    return fail(WQ_ERR_ALIGN, "%s: scales must be 4-byte aligned and y to its elements", name);
+  return WQ_OK;
+}
+
+static int gemm_overlap(const char* name, const wq_gemm_mxfp4& a) {
+  const ByteRows y32{a.y_f32, a.m, 4 * a.y_stride, 4 * a.n}, y16{a.y_bf16, a.m, 2 * a.y_stride, 2 * a.n};
+  const ByteRows in[] = {{a.x, a.m, 2 * a.x_stride, 2 * a.k},
+                         {a.xq, 1, 0, a.m * a.k / 2},
+                         {a.xq ? a.x_scale : nullptr, 1, 0, a.m * a.k / kMxGroup},
+                         {a.q, 1, 0, a.n * a.k / 2},
+                         {a.scale, 1, 0, a.n * a.k / kMxGroup}};
+  for (const ByteRows& i : in)
+    if (rows_meet(y32, i) || rows_meet(y16, i)) return fail(WQ_ERR_SHAPE, "%s: y must overlap no input", name);
+  if (rows_meet(y32, y16)) return fail(WQ_ERR_SHAPE, "%s: y_f32 must not overlap y_bf16", name);
+  return WQ_OK;
+}
+
+}  // namespace wq
+
+using namespace wq;
+
+extern "C" int64_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || m > kGemmMaxM || n < 0 || n > kGemmMaxN || k < kMxGroup || k > kGemmMaxK || k % kMxGroup) return 0;
+  return 16;
+}
+
+extern "C" int wq_gemm_mxfp4_prepare(const wq_gemm_mxfp4* a, void* workspace, int64_t workspace_bytes,
+                                     wq_gemm_mxfp4_plan* plan) {
+  const char* name = "wq_gemm_mxfp4_prepare";
+  if (!a || !plan || !workspace) return fail(WQ_ERR_NULL, "%s: a, workspace and plan must be non-null", name);
+  int rc = gemm_check(name, *a);
+  if (rc) return rc;
+  const int64_t need = wq_gemm_mxfp4_workspace_bytes(a->m, a->n, a->k);
+  if (workspace_bytes < need)
+    return fail(WQ_ERR_SHAPE, "%s: workspace_bytes = %lld, %lld are needed", name, (long long)workspace_bytes,
+                (long long)need);
+  if (!aligned16(workspace)) return fail(WQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", name);
+  if ((rc = gemm_overlap(name, *a))) return rc;
+  wq_gemm_mxfp4_plan p{};
+  if ((rc = plan_device(name, &p.device))) return rc;
+  p.made = kGemmMade;
+  p.workspace = workspace;
+  p.a = *a;
+  *plan = p;
+  return WQ_OK;
+}
+
+extern "C" int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream) {
+  const char* name = "wq_gemm_mxfp4_run";
+  if (!plan) return fail(WQ_ERR_NULL, "%s: plan must be non-null", name);
+  if (plan->made != kGemmMade) return fail(WQ_ERR_SHAPE, "%s: the plan was not made by wq_gemm_mxfp4_prepare", name);
+  int rc = same_device(name, plan->device);
+  if (rc) return rc;
+  const wq_gemm_mxfp4& g = plan->a;
+  if (g.m == 0 || g.n == 0) return WQ_OK;
+  MxRowsArgs a{};
+  a.w = {g.q, g.scale, g.n, (uint32_t)(g.k / 2), (uint32_t)(g.k / kMxGroup)};
+  a.x = g.x ? reinterpret_cast<const char*>(g.x) : reinterpret_cast<const char*>(g.xq);
+  a.xscale = g.x_scale;
+  a.x_stride = g.x ? 2 * g.x_stride : g.k / 2;
+  a.x_bytes = (uint32_t)(g.x ? 2 * g.k : g.k / 2);
+  a.y32 = g.y_f32;
+  a.y16 = g.y_bf16;
+  a.y_stride = g.y_stride;
+  a.m = g.m;
+  a.tiles = (int32_t)((g.n + 15) / 16);
+  a.spans = (int32_t)((g.k + 511) / 512);
+  hipStream_t s = (hipStream_t)stream;
+  if (g.xq) return rows_launch<true, 16, 8, 3>(name, a, s);
+  if (g.m <= 4) return rows_launch<false, 4, 8, 3>(name, a, s);
+  if (g.m <= 8) return rows_launch<false, 8, 8, 2>(name, a, s);
+  return rows_launch<false, 16, 4, 4>(name, a, s);
+}
