@@ -59,8 +59,10 @@ def parse(argv=None):
     return p.parse_args(argv)
 
 
-# Sources of the calls between the linears (rotation, attention, acceptance, adapters); no workload here runs them.
-OPERATOR_SOURCES = ("wq_kv.", "wq_tree_attention.", "wq_attention_", "wq_lora.")
+# Sources of the calls between the linears (rotation, attention, acceptance, adapters) and of the MXFP4 block (products,
+# expert layer, norms); no workload here runs them.
+OPERATOR_SOURCES = ("wq_kv.", "wq_tree_attention.", "wq_attention_", "wq_lora.", "wq_direct.", "wq_mx", "wq_row_stream.",
+                    "wq_moe_ffn.", "wq_block_norm.")
 
 
 def source_sha(base=os.path.join(ROOT, "weight_only_quantized_wq_amd", "csrc"), operators=False):
