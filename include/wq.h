@@ -256,7 +256,9 @@ enum {
   WQ_FORMAT_INT4G256 = 6,
   /* int4 with one group per row (wq_quantize_int4 with group == k): each
      matrix's sz is [n][1][2]; k % 32 == 0 */
-  WQ_FORMAT_INT4PC = 7
+  WQ_FORMAT_INT4PC = 7,
+  /* MXFP4 (wq_quantize_mxfp4); wq_moe_ffn only */
+  WQ_FORMAT_MXFP4 = 8
 };
 
 /* One linear layer of a step, in the layout of the single-matrix calls:
@@ -736,6 +738,127 @@ typedef struct {
 int64_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);
 int wq_gemm_mxfp4_prepare(const wq_gemm_mxfp4* a, void* workspace, int64_t workspace_bytes, wq_gemm_mxfp4_plan* plan);
 int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens -- [README] "Mixtral 8x7B"
+ * (sparse MoE), with any number of experts and selections:
+ *   s[t][e] = x[t] . router[e], or logits[t][e]
+ *   sel[t]  = the `top` largest s[t] (equal ones: lower index first; NaN after
+ *             all others)
+ *   gate    = exp(s) over the sum of exp(s), of the selected experts
+ *             (renormalize) or of all
+ *   y[t]    = sum_j gate[t][j] W2 (silu(W1 x[t]) * (W3 x[t])), W of expert sel[t][j]
+ *   x       bf16 [tokens][x_stride]
+ *   router  bf16 [e][dim], or logits fp32 [tokens][e] (exactly one)
+ *   format  WQ_FORMAT_INT8 (w13 int8 [e][2f][dim], s13 bf16 [e][2f], w2 int8
+ *           [e][dim][f], s2 bf16 [e][dim]) or WQ_FORMAT_MXFP4 (w13 [e][2f][dim/2]
+ *           with s13 u8 [e][2f][dim/32], w2 [e][dim][f/2] with s2 [e][dim][f/32]);
+ *           rows 0..f-1 of w13: W1 (gate), rows f..2f-1: W3 (up)
+ *   y       fp32 and / or bf16 [tokens][y_stride], either may be NULL but not both
+ *   sel     int32 [tokens][top], gates fp32 [tokens][top], each may be NULL
+ * Scores are fp64 sums, so that no order of summation decides which experts run;
+ * products are summed in fp32, and silu(W1 x) * (W3 x) is carried to the second
+ * in bf16 parts: three (24 bits), or two (16 bits) where only y_bf16 is asked
+ * for.  Weights past the largest finite bf16 (MXFP4 scale bytes of 253 and 254)
+ * give results that are not finite.  Only the selected experts' weights are
+ * read; routing happens on the device.  tokens 0..64, e 1..256, top 1..16 (at
+ * most e), dim and f multiples of 16 (MXFP4: 32) up to 32768; x, w13, w2, router
+ * 16-byte, s13 and s2 4-byte aligned (MXFP4: their last 4-byte word is read
+ * whole), x_stride a multiple of 8; results overlap nothing (WQ_ERR_SHAPE).
+ */
+typedef struct {
+  const uint16_t* x;
+  int64_t x_stride;
+  const uint16_t* router;
+  const float* logits;
+  const void* w13;
+  const void* s13;
+  const void* w2;
+  const void* s2;
+  float* y_f32;
+  uint16_t* y_bf16;
+  int64_t y_stride;
+  int32_t* sel;
+  float* gates;
+  int64_t tokens;
+  int64_t dim;
+  int64_t f;
+  int64_t e;
+  int32_t top;
+  int32_t format;
+  int32_t renormalize;
+} wq_moe_ffn;
+
+typedef struct {
+  int64_t made;        /* set by prepare */
+  int32_t device;
+  int32_t reserved;
+  void* workspace;
+  wq_moe_ffn a;
+} wq_moe_ffn_plan;
+
+/* Workspace of a plan with these sizes (0 if they are not supported). */
+int64_t wq_moe_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t f, int64_t e, int32_t top);
+int wq_moe_ffn_prepare(const wq_moe_ffn* a, void* workspace, int64_t workspace_bytes, wq_moe_ffn_plan* plan);
+int wq_moe_ffn_run(const wq_moe_ffn_plan* plan, void* stream);
+
+/*
+ * What stands between two blocks of a decoder, in one pass:
+ *   h'    = h + scale * act(gate) * norm(f)
+ *   u     = norm(h')                     norm(v) = v / sqrt(mean(v^2) + eps) * weight
+ *   h     fp32 or bf16 [rows][h_stride] (exactly one)
+ *   f     fp32 or bf16 [rows][f_stride], the block's result, or NULL: h' = h
+ *   f_norm bf16 [dim], or NULL: f as it is
+ *   gate  bf16 [rows][gate_stride] (stride 0: one row for all), or NULL: 1;
+ *         gate_kind: WQ_GATE_PLAIN gate, WQ_GATE_SIGMOID sigmoid(gate),
+ *         WQ_GATE_SILU gate * sigmoid(gate)
+ *   out   h' as fp32 or bf16 [rows][out_stride], or NULL; may be h itself (same
+ *         type and stride)
+ *   norm  bf16 [dim], or NULL: 1
+ *   u     bf16 [rows][u_stride], and / or in MXFP4 q u8 [rows][dim/2] with
+ *         q_scale u8 [rows][dim/32] (as wq_quantize_mxfp4 makes them); each may
+ *         be NULL, but something must be asked for
+ * h' is not rounded on its way into u.  Sums are fp64; elements are fp32, and
+ * fp64 where q is asked for (its codes are those of the formula).  dim a
+ * multiple of 8 (with q: 32) up to 32768, rows 0..2^24, strides multiples of 8;
+ * pointers 16-byte aligned, q 4-byte; results overlap nothing else
+ * (WQ_ERR_SHAPE).
+ */
+enum { WQ_GATE_PLAIN = 0, WQ_GATE_SIGMOID = 1, WQ_GATE_SILU = 2 };
+typedef struct {
+  const float* h_f32;
+  const uint16_t* h_bf16;
+  int64_t h_stride;
+  float* out_f32;
+  uint16_t* out_bf16;
+  int64_t out_stride;
+  const float* f_f32;
+  const uint16_t* f_bf16;
+  int64_t f_stride;
+  const uint16_t* f_norm;
+  const uint16_t* gate;
+  int64_t gate_stride;
+  const uint16_t* norm;
+  uint16_t* u;
+  int64_t u_stride;
+  uint8_t* q;
+  uint8_t* q_scale;
+  int64_t rows;
+  int64_t dim;
+  float scale;
+  float eps;
+  int32_t gate_kind;
+} wq_block_norm;
+
+typedef struct {
+  int64_t made;        /* set by prepare */
+  int32_t device;
+  int32_t reserved;
+  wq_block_norm a;
+} wq_block_norm_plan;
+
+int wq_block_norm_prepare(const wq_block_norm* a, wq_block_norm_plan* plan);
+int wq_block_norm_run(const wq_block_norm_plan* plan, void* stream);
 
 /* Static text for a wq_status value ("unknown status" otherwise). */
 const char* wq_status_string(int status);

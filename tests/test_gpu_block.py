@@ -8,6 +8,14 @@ Tolerances, fixed before the first run.  A rounding to bf16 is off by at most
   codes and scales), so a result differs by the roundings of its fp32 sum, at
   most (k + 16) 2^-23 of sum |x w| (additions that truncate count double), and
   one rounding to bf16 where that is asked for.
+* expert layer: h1 and h3 as products; |silu'| <= 1.1 carries their errors to
+  a = silu(h1) h3, whose own exp, quotient and products add 2^-19 |a|; a is
+  carried in 24 bits (2^-23 |a|; 2^-16 |a| where only bf16 is asked for); the
+  second product adds its sum's roundings, (3 f + 16) 2^-23 of sum |a w|, and
+  the gate 2^-19; then a rounding to bf16.  Selections are exact.
+* norm: fp32 elements through at most 16 roundings and an exp each (2^-19 of
+  every term, |h| and |scale act(gate) norm(f)|), a factor good to 2^-19, a
+  rounding to bf16; where MXFP4 is asked for the codes of the fp64 formula.
 """
 
 import numpy as np
@@ -190,3 +198,238 @@ SHAPES = [(1, 1, 32), (1, 16, 64), (1, 17, 96), (2, 33, 128), (3, 100, 160), (4,
 def test_product(wq, m, n, k, xkind):
     rng = np.random.default_rng(m * 7 + n * 3 + k)
     _product(wq, rng, m, n, k, xkind, ["f32", "bf16", "both"][(m + n) % 3], pad=(m + n) % 2)
+
+
+# --- expert layer ----------------------------------------------------------
+
+
+def _experts(rng, e, rows, k, weights):
+    """(values [e, rows, k], device tensors)"""
+    if weights == "mxfp4":
+        q, s = mx(rng, e * rows, k, spread=2)
+        v = block.mx_values(q, s).reshape(e, rows, k) * 2.0 ** -5
+        s -= 5
+        return v, (up(q.reshape(e, rows, -1)), up(s.reshape(e, rows, -1)))
+    q = rng.integers(-127, 128, (e, rows, k), dtype=np.int8)
+    s, st = bf16(rng.uniform(0.5, 1.5, (e, rows)) * 2.0 ** -9)
+    return q * s[..., None], (up(q), st)
+
+
+def _moe_allowed(x, w13, w2, sel, gates, want, parts, out):
+    f, k = w2.shape[2], w13.shape[2]
+    allowed = np.zeros(want.shape)
+    for t in range(x.shape[0]):
+        for e, g in zip(sel[t], gates[t]):
+            h = w13[e] @ x[t]
+            dh = (k + 16) * 2.0 ** -23 * (np.abs(w13[e]) @ np.abs(x[t]))
+            a = np.abs(block.silu(h[:f]) * h[f:])
+            da = 1.1 * dh[:f] * (np.abs(h[f:]) + dh[f:]) + np.abs(block.silu(h[:f])) * dh[f:] + a * 2.0 ** -19
+            da += a * (2.0 ** -23 if parts == 3 else 2.0 ** -16)
+            m = np.abs(w2[e])
+            allowed[t] += g * (m @ da + ((3 * f + 16) * 2.0 ** -23 + 2.0 ** -19) * (m @ a))
+    return allowed if out == "f32" else allowed + BF16 * (np.abs(want) + allowed)
+
+
+def _moe(wq, rng, tokens, e, top, dim, f, weights, scores, out, renormalize=True, logits=None, pad=0, router=None):
+    import torch
+    w13, t13 = _experts(rng, e, 2 * f, dim, weights)
+    w2, t2 = _experts(rng, e, dim, f, weights)
+    x, xt = bf16(rng.normal(0, 1, (tokens, dim)))
+    rt = lt = None
+    if scores == "router":
+        r, rt = bf16(rng.normal(0, 1.5 * dim ** -0.5, (e, dim)) if router is None else router)
+        logits = x @ r.T
+    else:
+        logits, lt = f32(rng.normal(0, 1.5, (tokens, e)) if logits is None else logits)
+    if pad:
+        wide = torch.full((tokens, dim + 8 * pad), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, :dim] = xt
+        xt = wide[:, :dim]
+    stride = dim + 3 * pad
+    y32 = torch.full((tokens + 2, stride), 777.0, device="cuda")
+    y16 = torch.full((tokens + 2, stride), 777.0, dtype=torch.bfloat16, device="cuda")
+    a, b = y32[1:tokens + 1, :dim], y16[1:tokens + 1, :dim]
+    sel, gates = empty(tokens, top, dtype="int32", fill=-1), empty(tokens, top, fill=-1)
+    plan = wq.wq_moe_ffn_prepare(xt, *t13, *t2, a if out != "bf16" else b, y2=b if out == "both" else None, router=rt,
+                                 logits=lt, top=top, renormalize=renormalize, sel=sel, gates=gates)
+    wq.wq_moe_ffn_run(plan)
+    want, want_sel, want_gates = block.moe_ffn(x, logits, w13, w2, top, renormalize)
+    assert np.array_equal(sel.cpu().numpy(), want_sel)
+    within(f64(gates), want_gates, 2.0 ** -19 * want_gates + 2.0 ** -126, "gates")
+    parts = 2 if out == "bf16" else 3
+    if out != "bf16":
+        within(f64(a), want, _moe_allowed(x, w13, w2, want_sel, want_gates, want, parts, "f32"), "fp32")
+    if out != "f32":
+        within(f64(b), want, _moe_allowed(x, w13, w2, want_sel, want_gates, want, parts, "bf16"), "bf16")
+    for t, used in ((y32, out != "bf16"), (y16, out != "f32")):
+        written = torch.zeros_like(t, dtype=torch.bool)
+        written[1:tokens + 1, :dim] = used
+        assert (t[~written] == 777.0).all()
+    first = y32.clone(), y16.clone(), sel.clone(), gates.clone()
+    wq.wq_moe_ffn_run(plan)
+    assert all(torch.equal(u, v) for u, v in zip(first, (y32, y16, sel, gates))), "a second run differs"
+
+
+LAYERS = [(1, 8, 2, 256, 512), (1, 4, 1, 32, 32), (2, 8, 2, 544, 96), (3, 16, 4, 96, 160), (4, 8, 2, 1024, 352),
+          (5, 8, 2, 64, 1056), (8, 60, 4, 128, 64), (9, 8, 2, 160, 96), (17, 4, 3, 64, 128), (33, 128, 8, 64, 32),
+          (64, 3, 2, 96, 64), (64, 256, 16, 32, 32), (61, 1, 1, 64, 64)]
+
+
+@pytest.mark.parametrize("weights", ["mxfp4", "int8"])
+@pytest.mark.parametrize("tokens,e,top,dim,f", LAYERS)
+def test_expert_layer(wq, tokens, e, top, dim, f, weights):
+    rng = np.random.default_rng(tokens * 31 + e + dim + f)
+    i = tokens + e + (weights == "int8")
+    _moe(wq, rng, tokens, e, top, dim, f, weights, ["router", "logits"][i % 2], ["f32", "bf16", "both"][i % 3],
+         renormalize=i % 5 != 0, pad=i % 2)
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 20])
+def test_int8_experts_of_odd_sixteens(wq, tokens):
+    _moe(wq, np.random.default_rng(tokens), tokens, 5, 2, 48, 272, "int8", "router", "f32")
+
+
+@pytest.mark.parametrize("tokens", [2, 12])
+def test_ties_infinities_and_nan_among_logits(wq, tokens):
+    rng = np.random.default_rng(3)
+    logits = rng.integers(-1, 2, (tokens, 70)).astype(np.float64)        # ties everywhere
+    logits[0, 5] = -np.inf
+    _moe(wq, rng, tokens, 70, 6, 32, 32, "mxfp4", "logits", "f32", logits=logits)
+
+
+def test_equal_router_rows_tie_to_the_lower_index(wq):
+    rng = np.random.default_rng(4)
+    row = rng.normal(0, 0.1, (1, 64))
+    _moe(wq, rng, 6, 9, 3, 64, 32, "int8", "router", "bf16", router=np.repeat(row, 9, 0))
+
+
+@pytest.mark.parametrize("tokens", [2, 30])
+def test_nan_logits_select_distinct_experts_in_range(wq, tokens):
+    import torch
+    w13, w2 = torch.zeros(4, 64, 32, dtype=torch.int8, device="cuda"), torch.zeros(4, 32, 32, dtype=torch.int8, device="cuda")
+    s13, s2 = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(4, 32, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(tokens, 32, dtype=torch.bfloat16, device="cuda")
+    logits = torch.full((tokens, 4), float("nan"), device="cuda")
+    logits[1] = torch.tensor([float("nan"), 1.0, float("-inf"), float("nan")])
+    sel, y = empty(tokens, 3, dtype="int32", fill=-1), empty(tokens, 32)
+    wq.wq_moe_ffn_run(wq.wq_moe_ffn_prepare(x, w13, s13, w2, s2, y, logits=logits, top=3, sel=sel))
+    got = sel.cpu().tolist()
+    assert got[0] == [0, 1, 2] and got[1] == [1, 2, 0]
+
+
+def test_large_activations_between_the_products_keep_their_values(wq):
+    """silu(h1) h3 next to the largest fp32, which no bf16 rounded to nearest reaches."""
+    import torch
+    w13 = torch.zeros(1, 64, 32, dtype=torch.int8, device="cuda")
+    w13[0, :, 0] = 1
+    s13 = torch.ones(1, 64, dtype=torch.bfloat16, device="cuda")
+    s13[0, 32:] = 1 + 2.0 ** -7
+    w2 = torch.zeros(1, 32, 32, dtype=torch.int8, device="cuda")
+    w2[0, torch.arange(32), torch.arange(32)] = 1
+    s2 = torch.full((1, 32), 0.5, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(1, 32, dtype=torch.bfloat16, device="cuda")
+    # 2^64 (1 - 2^-8): times itself and 1 + 2^-7 it is 2^128 (1 - 2^-14 + ...), past the largest bf16, 2^128 (1 - 2^-8),
+    # and its rounding border, 2^128 (1 - 2^-9)
+    x[0, 0] = 2.0 ** 64 * (1 - 2.0 ** -8)
+    y = empty(1, 32)
+    wq.wq_moe_ffn_run(wq.wq_moe_ffn_prepare(x, w13, s13, w2, s2, y, logits=torch.zeros(1, 1, device="cuda"), top=1))
+    a = float(x[0, 0].double()) ** 2 * (1 + 2.0 ** -7)
+    assert 2.0 ** 128 * (1 - 2.0 ** -9) < a < float(torch.finfo(torch.float32).max)
+    want = a * 0.5
+    within(f64(y), np.full((1, 32), want), 2.0 ** -18 * want, "large")
+
+
+# --- norm ------------------------------------------------------------------
+
+
+def _block(wq, rng, rows, dim, h="f32", f="bf16", post=True, gate="sigmoid", u="bf16", out=True, norm=True, scale=0.75,
+           eps=1e-6, pad=0, wide_gate=True, in_place=False, size=3.0):
+    import torch
+    make = {"f32": f32, "bf16": bf16}
+    hv, ht = make[h](rng.normal(0, size, (rows, dim)))
+    fv, ft = make[f](rng.normal(0, 1, (rows, dim))) if f else (None, None)
+    pv, pt = bf16(rng.normal(1, 0.1, dim)) if f and post else (None, None)
+    gv, gt = bf16(rng.normal(0, 2, (rows, dim) if wide_gate else dim)) if f and gate != "none" else (None, None)
+    nv, nt = bf16(rng.normal(1, 0.1, dim)) if norm else (None, None)
+    kind = "plain" if gate == "none" else gate
+
+    def padded(t):
+        if not pad or t is None or t.dim() < 2:
+            return t
+        w = torch.full((rows, dim + 8 * pad), float("nan"), dtype=t.dtype, device="cuda")
+        w[:, :dim] = t
+        return w[:, :dim]
+    ht, ft, gt = padded(ht), padded(ft), padded(gt)
+    ot = ht if in_place else padded(torch.zeros(rows, dim, dtype=ht.dtype, device="cuda")) if out else None
+    ut = padded(torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")) if "bf16" in u else None
+    q, qs = (empty(rows, dim // 2, dtype="uint8", fill=7), empty(rows, dim // 32, dtype="uint8", fill=7)) if "mxfp4" in u else (None, None)
+    plan = wq.wq_block_norm_prepare(ht, h_out=ot, f=ft, f_norm=pt, gate=gt, gate_kind=kind, scale=scale, norm=nt, u=ut, q=q,
+                                    q_scale=qs, eps=eps)
+    wq.wq_block_norm_run(plan)
+    # scale and eps are fp32 numbers
+    scale, eps = float(np.float32(scale)), float(np.float32(eps))
+    want_h, want_u = block.block_norm(hv, fv, pv, gv, kind, scale, nv, eps)
+    added = want_h - hv
+    dh = 2.0 ** -19 * (np.abs(hv) + np.abs(added)) + 1e-40
+    if ot is not None:
+        within(f64(ot), want_h, dh + (BF16 * (np.abs(want_h) + dh) if h == "bf16" else 0), "h")
+    if ut is not None:
+        r = np.abs(want_u / np.where(want_h == 0, 1, want_h))
+        du = r * dh + 2.0 ** -18 * np.abs(want_u)
+        within(f64(ut), want_u, du + BF16 * (np.abs(want_u) + du), "u")
+    if q is not None:
+        want_q, want_s = block.mx_quantize(want_u)
+        assert np.array_equal(qs.cpu().numpy(), want_s)
+        assert np.array_equal(q.cpu().numpy(), want_q)
+
+
+NORMS = [(1, 8), (1, 4096), (2, 520), (3, 32), (5, 1024), (7, 2048), (13, 4104), (4, 8192), (2, 16384), (3, 20000), (1, 32768),
+         (300, 64)]
+
+
+@pytest.mark.parametrize("rows,dim", NORMS)
+@pytest.mark.parametrize("gate", ["none", "plain", "sigmoid", "silu"])
+def test_block_norm(wq, rows, dim, gate):
+    rng = np.random.default_rng(rows + dim)
+    i = rows + dim // 8
+    u = ["bf16", "mxfp4", "bf16+mxfp4"][i % 3] if dim % 32 == 0 else "bf16"
+    _block(wq, rng, rows, dim, h=["f32", "bf16"][i % 2], f=["bf16", "f32"][i // 2 % 2], post=i % 5 != 0, gate=gate, u=u,
+           pad=i % 2, norm=i % 7 != 0, wide_gate=i % 4 != 1)
+
+
+@pytest.mark.parametrize("h", ["f32", "bf16"])
+def test_block_norm_in_place_without_f_and_without_norm(wq, h):
+    rng = np.random.default_rng(1)
+    _block(wq, rng, 9, 264, h=h, in_place=True)
+    _block(wq, rng, 9, 264, h=h, f=None, out=False)
+    _block(wq, rng, 9, 288, h=h, u="", norm=False)
+    _block(wq, rng, 9, 288, h=h, u="mxfp4", out=False, norm=False, f=None)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e30])
+@pytest.mark.parametrize("u", ["bf16", "mxfp4"])
+def test_block_norm_of_tiny_and_huge_rows(wq, size, u):
+    _block(wq, np.random.default_rng(2), 3, 512, f=None, out=False, u=u, eps=0.0, size=size)
+
+
+def test_zero_rows_and_rows_of_zeros(wq):
+    import torch
+    h, u = torch.zeros(2, 64, device="cuda"), empty(2, 64, dtype="bfloat16", fill=5)
+    q, s = empty(2, 32, dtype="uint8", fill=7), empty(2, 2, dtype="uint8", fill=7)
+    wq.wq_block_norm_run(wq.wq_block_norm_prepare(h, u=u, q=q, q_scale=s))
+    assert not u.any() and not q.any() and not s.any()
+    wq.wq_block_norm_run(wq.wq_block_norm_prepare(h[:0], u=u[:0]))
+
+
+def test_an_infinity_or_nan_stays_in_its_row_and_group(wq):
+    import torch
+    h = torch.randn(3, 128, device="cuda")
+    f = torch.zeros(3, 128, device="cuda")
+    f[1, 40] = float("nan")
+    out, u = torch.empty_like(h), empty(3, 128, dtype="bfloat16")
+    q, s = empty(3, 64, dtype="uint8", fill=7), empty(3, 4, dtype="uint8", fill=7)
+    wq.wq_block_norm_run(wq.wq_block_norm_prepare(h, h_out=out, f=f, u=u, q=q, q_scale=s))
+    bad = torch.isnan(out)
+    assert bad[1, 40] and bad.sum() == 1
+    assert torch.isnan(u[1]).all() and torch.isfinite(u[[0, 2]]).all()
+    assert (s[1] == 255).all() and (q[1] == 0).all() and (s[[0, 2]] != 255).all()

@@ -13,6 +13,8 @@ _EXPORTS = (
     "wq_gemv_bf16", "wq_gemv_int8", "wq_gemv_int4g32", "wq_gemv_int4", "wq_gemm_smallM", "wq_gemm_smallM_int4", "wq_gemm_smallM_int8",
     "wq_quantize_mxfp4", "wq_dequantize_mxfp4",
     "wq_gemm_mxfp4", "wq_gemm_mxfp4_plan", "wq_gemm_mxfp4_workspace_bytes", "wq_gemm_mxfp4_prepare", "wq_gemm_mxfp4_run",
+    "wq_moe_ffn", "wq_moe_ffn_plan", "wq_moe_ffn_workspace_bytes", "wq_moe_ffn_prepare", "wq_moe_ffn_run",
+    "WQ_GATE", "wq_block_norm", "wq_block_norm_plan", "wq_block_norm_prepare", "wq_block_norm_run",
     "moe_top2_gemv", "moe_top2_gemv_noalloc",
     "WQ_FORMAT", "wq_matrix", "wq_step_plan",
     "wq_decode_step_workspace_bytes", "wq_decode_step_prepare", "wq_decode_step_run",

@@ -38,7 +38,8 @@ _SIGNATURES = {
     "moe_top2_gemv_noalloc": [_P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P],
 }
 
-WQ_FORMAT = {"bf16": 1, "int8": 2, "int4g32": 3, "int4g64": 4, "int4g128": 5, "int4g256": 6, "int4pc": 7}
+WQ_FORMAT = {"bf16": 1, "int8": 2, "int4g32": 3, "int4g64": 4, "int4g128": 5, "int4g256": 6, "int4pc": 7,
+             "mxfp4": 8}
 
 
 class wq_matrix(ctypes.Structure):
@@ -101,6 +102,20 @@ class wq_gemm_mxfp4(ctypes.Structure):
                 ("y_bf16", _P), ("y_stride", _I64), ("m", _I64), ("n", _I64), ("k", _I64)]
 
 
+class wq_moe_ffn(ctypes.Structure):
+    _fields_ = [("x", _P), ("x_stride", _I64), ("router", _P), ("logits", _P), ("w13", _P), ("s13", _P), ("w2", _P),
+                ("s2", _P), ("y_f32", _P), ("y_bf16", _P), ("y_stride", _I64), ("sel", _P), ("gates", _P),
+                ("tokens", _I64), ("dim", _I64), ("f", _I64), ("e", _I64), ("top", _I32), ("format", _I32),
+                ("renormalize", _I32)]
+
+
+class wq_block_norm(ctypes.Structure):
+    _fields_ = [("h_f32", _P), ("h_bf16", _P), ("h_stride", _I64), ("out_f32", _P), ("out_bf16", _P),
+                ("out_stride", _I64), ("f_f32", _P), ("f_bf16", _P), ("f_stride", _I64), ("f_norm", _P), ("gate", _P),
+                ("gate_stride", _I64), ("norm", _P), ("u", _P), ("u_stride", _I64), ("q", _P), ("q_scale", _P),
+                ("rows", _I64), ("dim", _I64), ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("gate_kind", _I32)]
+
+
 # Plans: ctypes instances take further attributes, and `keep` holds the tensors
 # a plan's addresses point into for as long as the plan lives.
 class wq_qkv_rope_plan(ctypes.Structure):
@@ -123,6 +138,16 @@ class wq_lora_plan(ctypes.Structure):
 class wq_gemm_mxfp4_plan(ctypes.Structure):
     _fields_ = [("made", _I64), ("device", _I32), ("reserved", _I32), ("workspace", _P), ("a", wq_gemm_mxfp4)]
 
+
+class wq_moe_ffn_plan(ctypes.Structure):
+    _fields_ = [("made", _I64), ("device", _I32), ("reserved", _I32), ("workspace", _P), ("a", wq_moe_ffn)]
+
+
+class wq_block_norm_plan(ctypes.Structure):
+    _fields_ = [("made", _I64), ("device", _I32), ("reserved", _I32), ("a", wq_block_norm)]
+
+
+WQ_GATE = {"plain": 0, "sigmoid": 1, "silu": 2}
 
 WQ_ROPE = {"plain": 0, "linear": 1, "bands": 2, "ramp": 3}
 
@@ -169,6 +194,8 @@ def _load():
     lib.wq_lora_workspace_bytes.restype = _I64
     lib.wq_gemm_mxfp4_workspace_bytes.argtypes = [_I64] * 3
     lib.wq_gemm_mxfp4_workspace_bytes.restype = _I64
+    lib.wq_moe_ffn_workspace_bytes.argtypes = [_I64] * 4 + [_I32]
+    lib.wq_moe_ffn_workspace_bytes.restype = _I64
     # prepare and run are called with ctypes.byref of the structures above
     lib.wq_qkv_rope_prepare.argtypes = [_P, _P]
     lib.wq_qkv_rope_run.argtypes = [_P, _P]
@@ -180,6 +207,10 @@ def _load():
     lib.wq_lora_run.argtypes = [_P, _P]
     lib.wq_gemm_mxfp4_prepare.argtypes = [_P, _P, _I64, _P]
     lib.wq_gemm_mxfp4_run.argtypes = [_P, _P]
+    lib.wq_moe_ffn_prepare.argtypes = [_P, _P, _I64, _P]
+    lib.wq_moe_ffn_run.argtypes = [_P, _P]
+    lib.wq_block_norm_prepare.argtypes = [_P, _P]
+    lib.wq_block_norm_run.argtypes = [_P, _P]
     lib.wq_status_string.argtypes = [ctypes.c_int]
     lib.wq_status_string.restype = ctypes.c_char_p
     lib.wq_last_error.argtypes = []
@@ -783,3 +814,92 @@ def wq_gemm_mxfp4_prepare(x, q, scale, y, y2=None, x_scale=None, workspace=None)
 
 def wq_gemm_mxfp4_run(plan, stream=None):
     _run("wq_gemm_mxfp4_run", lib.wq_gemm_mxfp4_run, plan, stream)
+
+
+def wq_moe_ffn_workspace_bytes(tokens, dim, f, e, top):
+    return int(lib.wq_moe_ffn_workspace_bytes(tokens, dim, f, e, top))
+
+
+def wq_moe_ffn_prepare(x, w13, s13, w2, s2, y, y2=None, router=None, logits=None, top=2, renormalize=True, sel=None,
+                       gates=None, workspace=None):
+    """x bf16 [tokens, dim]; w13 int8 [e, 2f, dim] with s13 bf16 [e, 2f] and w2 int8 [e, dim, f] with s2 bf16 [e, dim],
+    or MXFP4: uint8 [e, 2f, dim / 2] with uint8 [e, 2f, dim / 32] and [e, dim, f / 2] with [e, dim, f / 32]; router bf16
+    [e, dim] or logits fp32 [tokens, e]; y fp32 or bf16 [tokens, dim], y2 the other of the two; sel int32 and gates fp32
+    [tokens, top], out."""
+    _view(x, "x", 2, _BF16, None)
+    device, (tokens, dim) = x.device, x.shape
+    mx = str(getattr(w13, "dtype", "")) == "torch.uint8"
+    if mx:
+        up, f = _mx_view(w13, s13, "w13", 3, device), _mx_view(w2, s2, "w2", 3, device)
+    else:
+        for t, what, dims, kinds in ((w13, "w13", 3, ("int8",)), (s13, "s13", 2, _BF16), (w2, "w2", 3, ("int8",)),
+                                     (s2, "s2", 2, _BF16)):
+            _view(t, what, dims, kinds, device)
+            if not t.is_contiguous():
+                raise ValueError(f"libwq: {what} must be contiguous")
+        up, f = w13.shape[2], w2.shape[2]
+        if s13.shape != w13.shape[:2] or s2.shape != w2.shape[:2]:
+            raise ValueError(f"libwq: scales {tuple(s13.shape)}, {tuple(s2.shape)} do not go with w13 "
+                             f"{tuple(w13.shape)} and w2 {tuple(w2.shape)}")
+    e = w13.shape[0]
+    if up != dim or w13.shape[1] != 2 * f or tuple(w2.shape[:2]) != (e, dim):
+        raise ValueError(f"libwq: w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not go with x {tuple(x.shape)}")
+    for t, what, shape, kinds in ((router, "router", (e, dim), _BF16), (logits, "logits", (tokens, e), ("float32",)),
+                                  (sel, "sel", (tokens, top), ("int32",)), (gates, "gates", (tokens, top), ("float32",))):
+        if t is not None:
+            _view(t, what, 2, kinds, device)
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"libwq: {what} must be {shape} and contiguous, not {tuple(t.shape)}")
+    outs, y_stride = _outputs(y, y2, (tokens, dim), device)
+    a = wq_moe_ffn(_at(x), _row_stride(x, dim), *(None if t is None else _at(t) for t in (router, logits)), _at(w13),
+                   _at(s13), _at(w2), _at(s2), *outs, y_stride, *(None if t is None else _at(t) for t in (sel, gates)),
+                   tokens, dim, f, e, top, WQ_FORMAT["mxfp4" if mx else "int8"], 1 if renormalize else 0)
+    workspace, nbytes = _workspace(workspace, wq_moe_ffn_workspace_bytes(tokens, dim, f, e, top), device)
+    return _prepare("wq_moe_ffn_prepare", wq_moe_ffn_plan(), device,
+                    (x, w13, s13, w2, s2, y, y2, router, logits, sel, gates, workspace), ctypes.byref(a), _at(workspace),
+                    nbytes)
+
+
+def wq_moe_ffn_run(plan, stream=None):
+    _run("wq_moe_ffn_run", lib.wq_moe_ffn_run, plan, stream)
+
+
+def wq_block_norm_prepare(h, h_out=None, f=None, f_norm=None, gate=None, gate_kind="plain", scale=1.0, norm=None, u=None,
+                          q=None, q_scale=None, eps=1e-6):
+    """h, h_out and f fp32 or bf16 [rows, dim] (h_out may be h); f_norm and norm bf16 [dim]; gate bf16 [rows, dim] (a row
+    expanded over all is read once) or [dim], gate_kind a WQ_GATE name or code; u bf16 [rows, dim]; q uint8
+    [rows, dim / 2] with q_scale uint8 [rows, dim / 32]."""
+    kinds = ("float32",) + _BF16
+    _view(h, "h", 2, kinds, None)
+    device, (rows, dim) = h.device, h.shape
+
+    def rows_of(t, what, dtypes):
+        """(fp32 address, bf16 address, row stride)"""
+        if t is None:
+            return None, None, 0
+        _view(t, what, 2, dtypes, device)
+        if tuple(t.shape) != (rows, dim):
+            raise ValueError(f"libwq: {what} must be {(rows, dim)}, not {tuple(t.shape)}")
+        f32 = str(t.dtype) == "torch.float32"
+        return _at(t) if f32 else None, None if f32 else _at(t), _row_stride(t, dim)
+
+    if gate is not None and hasattr(gate, "dim") and gate.dim() == 1:
+        gate = gate.expand(rows, dim) if gate.shape[0] == dim else gate
+    _, gate_at, gate_stride = rows_of(gate, "gate", _BF16)
+    if gate is not None and rows > 1 and gate.stride(0) == 0:
+        gate_stride = 0
+    _, u_at, u_stride = rows_of(u, "u", _BF16)
+    if (q is None) != (q_scale is None):
+        raise ValueError("libwq: q and q_scale go together")
+    if q is not None and _mx_view(q, q_scale, "q", 2, device) != dim or q is not None and q.shape[0] != rows:
+        raise ValueError(f"libwq: q {tuple(q.shape)} does not go with h {tuple(h.shape)}")
+    a = wq_block_norm(*rows_of(h, "h", kinds), *rows_of(h_out, "h_out", kinds), *rows_of(f, "f", kinds),
+                      _vector(f_norm, "f_norm", dim, _BF16, device), gate_at, gate_stride,
+                      _vector(norm, "norm", dim, _BF16, device), u_at, u_stride, None if q is None else _at(q),
+                      None if q is None else _at(q_scale), rows, dim, scale, eps, WQ_GATE.get(gate_kind, gate_kind))
+    return _prepare("wq_block_norm_prepare", wq_block_norm_plan(), device,
+                    (h, h_out, f, f_norm, gate, norm, u, q, q_scale), ctypes.byref(a))
+
+
+def wq_block_norm_run(plan, stream=None):
+    _run("wq_block_norm_run", lib.wq_block_norm_run, plan, stream)

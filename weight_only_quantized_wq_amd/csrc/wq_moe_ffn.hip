@@ -1,0 +1,729 @@
+// A whole mixture-of-experts layer for a few tokens: router, selected experts (SwiGLU)
+// and their weighted sum.  Bound by the bytes of the experts in use, each read once.
+//
+//   scores   x router^T in fp64 (bf16 products are exact there: which experts run does
+//            not depend on an order of summation); where the caller gives logits, none
+//   route    the `top` largest scores of each token and their gates
+//   up       a workgroup takes a block of rows of W1 and W3 of one expert over the
+//            tokens that chose it: h1, h3 meet in LDS, silu(h1) h3 goes to the workspace
+//   down     a workgroup takes 16 rows of W2 of every expert in use, so that the sum
+//            over experts stays inside it; its waves split (expert, span of f)
+//
+// A token's experts are distinct and there are at most 64 tokens, so the tokens of an
+// expert are a 64-bit mask, which every workgroup builds itself from the selections.
+// The second product takes silu(h1) h3 in bf16 parts: three (24 bits), or two (16 bits)
+// where only bf16 results are asked for, as further columns of the matrix instruction.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "wq_host.hpp"
+#include "wq_kv.hpp"
+#include "wq_row_stream.hpp"
+
+namespace wq {
+
+constexpr int kMoeTokens = 64, kMoeExperts = 256, kMoeTop = 16;
+
+struct MoeArgs {
+  const uint16_t* x;
+  int64_t x_stride;
+  const uint16_t* router;
+  const float* logits;
+  double* scores;          // [tokens][e], or null where logits are given
+  int32_t* sel;            // [tokens][top]
+  float* gates;
+  int32_t* user_sel;       // the caller's copies, or null
+  float* user_gates;
+  uint16_t* act;           // [tokens * top][parts][f], in the order of experts
+  StreamWeights w13, w2;
+  const uint16_t* s13;     // int8: row scales
+  const uint16_t* s2;
+  float* y32;
+  uint16_t* y16;
+  int64_t y_stride;
+  int32_t tokens, dim, f, e, top, renormalize;
+  int32_t here;            // the selection is made by the up launch itself
+  int32_t parts;
+  int32_t pairs, per, ways, blocks, spans;   // up: row tiles of W1 (and W3), of a workgroup; waves per tile
+  int32_t spans2;
+};
+
+// ---------------------------------------------------------------------------
+// Scores and selection
+
+constexpr int kScoreWaves = 16, kScoreBatch = 4;
+
+template <int N>
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int d = N / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Experts first .. last - 1 of token t, by the waves of a workgroup; put(e, score) is
+// called in one lane.
+template <class Put>
+__device__ __forceinline__ void score_experts(const MoeArgs& a, int t, int first, int last, Put put) {
+  const int lane = lane_id();
+  const uint16_t* x = a.x + t * a.x_stride;
+  for (int e = first + wave_id() * kScoreBatch; e < last; e += kScoreWaves * kScoreBatch) {
+    double sum[kScoreBatch] = {0., 0., 0., 0.};
+    for (int i = lane * 8; i < a.dim; i += 512) {
+      const u32x4 xv = load16(x + i);
+      u32x4 wv[kScoreBatch];
+#pragma unroll
+      for (int b = 0; b < kScoreBatch; ++b) wv[b] = load16(a.router + (int64_t)min(e + b, last - 1) * a.dim + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const double lo = bf16lo_to_f32(xv[j]), hi = bf16hi_to_f32(xv[j]);
+#pragma unroll
+        for (int b = 0; b < kScoreBatch; ++b) {
+          sum[b] = fma(lo, (double)bf16lo_to_f32(wv[b][j]), sum[b]);
+          sum[b] = fma(hi, (double)bf16hi_to_f32(wv[b][j]), sum[b]);
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kScoreBatch; ++b) {
+      const double v = wave_sum64<64>(sum[b]);
+      if (lane == 0 && e + b < last) put(e + b, v);
+    }
+  }
+}
+
+template <int CTRL, int MASK = 0xF>
+__device__ __forceinline__ int32_t dpp_max(int32_t v) {
+  const int32_t o = __builtin_amdgcn_update_dpp((int)0x80000000, v, CTRL, MASK, 0xF, false);
+  return v > o ? v : o;
+}
+__device__ __forceinline__ int32_t wave_max_i32(int32_t v) {
+  v = dpp_max<0xB1>(v);
+  v = dpp_max<0x4E>(v);
+  v = dpp_max<0x141>(v);
+  v = dpp_max<0x140>(v);
+  v = dpp_max<0x142, 0xA>(v);
+  v = dpp_max<0x143, 0xC>(v);
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// The selection of one token by one wave: score(e) of e < a.e, the largest `top` in
+// order, equal ones by index, NaN after all others.  out(j, expert, gate) is called in
+// one lane.
+template <class Score, class Out>
+__device__ __forceinline__ void select_experts(const MoeArgs& a, Score score, Out out) {
+  const int lane = lane_id();
+  constexpr int N = kMoeExperts / kWave;
+  int64_t key[N];
+  double s[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = lane + 64 * i;
+    s[i] = e < a.e ? score(e) + 0.0 : 0.0;      // -0 counts as 0
+    const int64_t b = __double_as_longlong(s[i]);
+    key[i] = b ^ ((b >> 63) & 0x7FFFFFFFFFFFFFFFll);   // ordered as the values are
+    if (s[i] != s[i]) key[i] = INT64_MIN + 1;
+    if (e >= a.e) key[i] = INT64_MIN;
+  }
+  int mine = -1;                                // lane j: the j-th expert and its score
+  double value = 0.;
+  for (int j = 0; j < a.top; ++j) {
+    int64_t k = key[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) k = k > key[i] ? k : key[i];
+    const int32_t hi = wave_max_i32((int32_t)(k >> 32));
+    // the low half as it compares unsigned, among the lanes with this high half
+    const int32_t lo = wave_max_i32((int32_t)(k >> 32) == hi ? (int32_t)((uint32_t)k ^ 0x80000000u) : INT32_MIN);
+    const int64_t best = (int64_t)(((uint64_t)(uint32_t)hi << 32) | ((uint32_t)lo ^ 0x80000000u));
+    int found = 0;
+    bool done = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint64_t at = __ballot(key[i] == best);
+      if (!done && at) {
+        done = true;
+        const int l = __ffsll((unsigned long long)at) - 1;
+        found = l + 64 * i;
+        const double v = __shfl(s[i], l);
+        if (lane == j) {
+          mine = found;
+          value = v;
+        }
+        if (lane == l) key[i] = INT64_MIN;
+      }
+    }
+  }
+  const double top = __shfl(value, 0);
+  float w = lane < a.top ? expf((float)(value - top)) : 0.f;
+  float total;
+  if (a.renormalize) {
+    total = wave_sum(w);
+  } else {
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + 64 * i < a.e) all += expf((float)(s[i] - top));
+    total = wave_sum(all);
+  }
+  if (lane < a.top) out(lane, mine, w / total);
+}
+
+__device__ __forceinline__ void put_selection(const MoeArgs& a, int t, int j, int e, float gate) {
+  const int at = t * a.top + j;
+  a.sel[at] = e;
+  a.gates[at] = gate;
+  if (a.user_sel) a.user_sel[at] = e;
+  if (a.user_gates) a.user_gates[at] = gate;
+}
+
+// Scores of a token's experts by one workgroup, which selects at once; or of a share of
+// them (gridDim.y > 1), for route_kernel.
+__global__ __launch_bounds__(kScoreWaves * 64) void moe_score_kernel(MoeArgs a) {
+  __shared__ double score[kMoeExperts];
+  const int t = (int)blockIdx.x, share = (a.e + (int)gridDim.y - 1) / (int)gridDim.y;
+  const int first = (int)blockIdx.y * share, last = min(first + share, a.e);
+  score_experts(a, t, first, last, [&](int e, double v) {
+    if (gridDim.y == 1)
+      score[e] = v;
+    else
+      a.scores[t * a.e + e] = v;
+  });
+  if (gridDim.y > 1) return;
+  __syncthreads();
+  if (wave_id() == 0)
+    select_experts(a, [&](int e) { return score[e]; }, [&](int j, int e, float g) { put_selection(a, t, j, e, g); });
+}
+
+__global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a) {
+  const int t = (int)blockIdx.x;
+  select_experts(
+      a, [&](int e) { return a.logits ? (double)a.logits[t * a.e + e] : a.scores[t * a.e + e]; },
+      [&](int j, int e, float g) { put_selection(a, t, j, e, g); });
+}
+
+// ---------------------------------------------------------------------------
+// The experts' tokens
+
+struct MoeTokens {
+  uint64_t mask[kMoeExperts];
+  int32_t sel[kMoeTokens * kMoeTop];
+  float gate[kMoeTokens * kMoeTop];
+};
+
+// Fills `all` from the selections (a barrier at the end).
+template <int WAVES>
+__device__ __forceinline__ void find_tokens(const MoeArgs& a, MoeTokens& all) {
+  const int tid = (int)threadIdx.x, n = a.tokens * a.top;
+  for (int e = tid; e < kMoeExperts; e += WAVES * 64) all.mask[e] = 0;
+  if (!a.here) {
+    for (int i = tid; i < n; i += WAVES * 64) {
+      all.sel[i] = a.sel[i];
+      all.gate[i] = a.gates[i];
+    }
+  } else {
+    for (int t = wave_id(); t < a.tokens; t += WAVES)
+      select_experts(
+          a, [&](int e) { return (double)a.logits[t * a.e + e]; },
+          [&](int j, int e, float g) {
+            all.sel[t * a.top + j] = e;
+            if (blockIdx.x == 0) put_selection(a, t, j, e, g);
+          });
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += WAVES * 64) atomicOr((unsigned long long*)&all.mask[all.sel[i]], 1ull << (i / a.top));
+  __syncthreads();
+}
+
+// Sum over the lower lanes (and the lane's own) of v.
+__device__ __forceinline__ int wave_prefix(int v) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// Item `item` of the experts in use, `chunk` tokens an item: its expert, the first of
+// its tokens among the expert's, and the expert's first row of `act`; false past the
+// last item.
+__device__ __forceinline__ bool find_item(const MoeTokens& all, int item, int chunk, int& expert, int& begin, int& slot) {
+  const int lane = lane_id();
+  constexpr int N = kMoeExperts / kWave;
+  int items = 0, rows = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = __popcll(all.mask[lane * N + i]);
+    items += (c + chunk - 1) / chunk;
+    rows += c;
+  }
+  const int before = wave_prefix(items) - items, row0 = wave_prefix(rows) - rows;
+  const uint64_t at = __ballot(item >= before && item < before + items);
+  if (!at) return false;
+  const int l = __ffsll((unsigned long long)at) - 1;
+  int left = item - __shfl(before, l), row = __shfl(row0, l);
+  expert = l * N;
+  for (int i = 0; i < N; ++i) {
+    const int c = __popcll(all.mask[l * N + i]), n = (c + chunk - 1) / chunk;
+    expert = l * N + i;
+    if (left < n) break;
+    left -= n;
+    row += c;
+  }
+  expert = __builtin_amdgcn_readfirstlane(expert);
+  begin = __builtin_amdgcn_readfirstlane(left * chunk);
+  slot = __builtin_amdgcn_readfirstlane(row);
+  return true;
+}
+
+// bf16 parts of v whose sum is v (three), or v to 16 bits (two).  Truncated, so that
+// none overflows; infinities and NaN are the first part alone.
+__device__ __forceinline__ void bf16_parts(float v, int parts, uint16_t (&p)[3]) {
+  p[1] = p[2] = 0;
+  if (!(fabsf(v) < INFINITY)) {
+    p[0] = f32_to_bf16(v);
+    return;
+  }
+  const uint32_t b = __float_as_uint(v);
+  p[0] = (uint16_t)(b >> 16);
+  const float rest = v - __uint_as_float(b & 0xFFFF0000u);
+  if (parts == 2) {
+    p[1] = f32_to_bf16(rest);
+  } else {
+    const uint32_t m = __float_as_uint(rest);
+    p[1] = (uint16_t)(m >> 16);
+    p[2] = f32_to_bf16(rest - __uint_as_float(m & 0xFFFF0000u));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// First products and the gate
+
+constexpr int kUpTiles = 16;
+
+template <bool MX, bool ODD, int COLS, int WAVES, int P>
+__global__ __launch_bounds__(WAVES * 64) void moe_up_kernel(MoeArgs a) {
+  using S = RowStream<MX, false, ODD, COLS, P>;
+  constexpr int kRed = WAVES * kUpTiles * 1024, kAll = WAVES * S::kBytes;
+  __shared__ __align__(1024) char lds[kAll > kRed ? kAll : kRed];
+  __shared__ int list[COLS];
+  MoeTokens& all = *reinterpret_cast<MoeTokens*>(lds);
+  static_assert(sizeof(MoeTokens) <= sizeof(lds));
+  find_tokens<WAVES>(a, all);
+  int expert, begin, slot;
+  if (!find_item(all, (int)blockIdx.x / a.blocks, COLS, expert, begin, slot)) return;
+  const uint64_t mask = all.mask[expert];
+  const int cols = min(COLS, __popcll(mask) - begin);
+  if (wave_id() == 0) {
+    const int lane = lane_id(), rank = __popcll(mask & ((1ull << lane) - 1)) - begin;
+    if ((mask >> lane & 1) && rank >= 0 && rank < COLS) list[rank] = lane;
+  }
+  __syncthreads();
+  const int wave = wave_id(), ways = a.ways, kw = wave % ways, tw = wave / ways, teams = WAVES / ways;
+  const S s(lds + wave * S::kBytes);
+  const int first = (int)blockIdx.x % a.blocks * a.per, mine = min(a.per, a.pairs - first);
+  const int pairs = (mine - tw + teams - 1) / teams;
+  f32x4 acc[kUpTiles];
+#pragma unroll
+  for (int t = 0; t < kUpTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t rows0 = (int64_t)expert * 2 * a.f;
+  // a tile of W1, then the same rows of W3
+  s.template run<kUpTiles>(
+      a.w13, 2 * pairs, kw, ways, a.spans, (int)(a.w13.row_bytes / 16),
+      [&](int t, int64_t& row0, int& left) {
+        row0 = rows0 + (t & 1) * a.f + (int64_t)(first + tw + (t >> 1) * teams) * 16;
+        left = 16;
+      },
+      [&](int col) { return reinterpret_cast<const char*>(a.x + list[min(col, cols - 1)] * a.x_stride); }, 2u * a.dim, nullptr, 0,
+      0, 1, acc);
+  __syncthreads();
+  for_tiles<kUpTiles>(2 * pairs, [&](auto at) __attribute__((always_inline)) {
+    *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * 1024 + s.lane * 16) = acc[at.value];
+  });
+  __syncthreads();
+  for (int o = (int)threadIdx.x; o < mine * 16 * cols; o += WAVES * 64) {
+    const int row = o & 15, col = (o >> 4) % cols, pair = (o >> 4) / cols;
+    const char* from = lds + ((pair % teams) * ways * kUpTiles + 2 * (pair / teams)) * 1024 + ((row >> 2) * 16 + col) * 16 + (row & 3) * 4;
+    float h1 = 0.f, h3 = 0.f;
+    for (int w = 0; w < ways; ++w) {
+      h1 += *reinterpret_cast<const float*>(from + w * kUpTiles * 1024);
+      h3 += *reinterpret_cast<const float*>(from + w * kUpTiles * 1024 + 1024);
+    }
+    const int r = (first + pair) * 16 + row;
+    if constexpr (!MX) {
+      h1 *= __uint_as_float((uint32_t)gmem(a.s13)[rows0 + r] << 16);
+      h3 *= __uint_as_float((uint32_t)gmem(a.s13)[rows0 + a.f + r] << 16);
+    }
+    const float v = h1 / (1.f + expf(-h1)) * h3;
+    uint16_t p[3];
+    bf16_parts(v, a.parts, p);
+    uint16_t* to = a.act + (int64_t)(slot + begin + col) * a.parts * a.f + r;
+    for (int q = 0; q < a.parts; ++q) gmem(to)[q * a.f] = p[q];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Second product and the sum over experts
+
+// The experts in use, in order.
+struct MoeDown {
+  int32_t expert[kMoeExperts];
+  int32_t slot[kMoeExperts];
+  int32_t used;
+};
+
+template <bool MX, bool ODD, int COLS, int WAVES, int P, int TM>
+__global__ __launch_bounds__(WAVES * 64) void moe_down_kernel(MoeArgs a) {
+  using S = RowStream<MX, false, ODD, COLS, P>;
+  // a unit is a span of W2's rows and of the activations that meet it; both have P slots
+  constexpr int kWave0 = S::kXBytes * (P - 1) + S::kBytes;
+  __shared__ __align__(1024) char lds[WAVES * kWave0];
+  __shared__ __align__(16) float sums[WAVES][TM * 16];
+  __shared__ MoeTokens all;
+  __shared__ MoeDown down;
+  find_tokens<WAVES>(a, all);
+  const int wave = wave_id(), lane = lane_id();
+  if (wave == 0) {
+    constexpr int N = kMoeExperts / kWave;
+    int used = 0, rows = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = __popcll(all.mask[lane * N + i]);
+      used += c > 0;
+      rows += c;
+    }
+    int at = wave_prefix(used) - used, row = wave_prefix(rows) - rows;
+    for (int i = 0; i < N; ++i) {
+      const int c = __popcll(all.mask[lane * N + i]);
+      if (c) {
+        down.expert[at] = lane * N + i;
+        down.slot[at++] = row;
+      }
+      row += c;
+    }
+    if (lane == 63) down.used = at;
+  }
+  for (int i = lane; i < TM * 16; i += 64) sums[wave][i] = 0.f;
+  __syncthreads();
+  const int used = down.used, chunk = COLS / a.parts;
+  const int64_t tile = (int64_t)blockIdx.x * 16;
+  char* const base = lds + wave * kWave0;
+  const int g = lane >> 4, c = lane & 15;
+
+  // this wave's units: (expert in use, span) pairs wave, wave + WAVES, ..., each over
+  // the chunks of the expert's tokens
+  struct Cursor {
+    int pair, chunk;
+  };
+  const int pairs = used * a.spans2;
+  auto tokens_of = [&](int pair) { return __builtin_amdgcn_readfirstlane(__popcll(all.mask[down.expert[pair / a.spans2]])); };
+  auto next = [&](Cursor& q) {
+    if ((q.chunk + 1) * chunk < tokens_of(q.pair)) {
+      ++q.chunk;
+    } else {
+      q.chunk = 0;
+      q.pair += WAVES;
+    }
+  };
+  // slots of weights lie behind those of activations
+  auto request = [&](const Cursor& q, int slot) {
+    const int u = q.pair / a.spans2, span = q.pair % a.spans2;
+    const int expert = __builtin_amdgcn_readfirstlane(down.expert[u]), row = __builtin_amdgcn_readfirstlane(down.slot[u]);
+    const int have = min(chunk, tokens_of(q.pair) - q.chunk * chunk);
+    const uint16_t* act = a.act + (int64_t)(row + q.chunk * chunk) * a.parts * a.f;
+    // columns: part after part, `chunk` tokens each
+    const S x(base + slot * S::kXBytes);
+    x.request_x(
+        [&](int col) {
+          const int part = min(col / chunk, a.parts - 1), tok = min(col % chunk, have - 1);
+          return reinterpret_cast<const char*>(act + (int64_t)(tok * a.parts + part) * a.f);
+        },
+        2u * a.f, span);
+    const S w(base + (P - 1) * S::kXBytes);
+    w.request_unit(a.w2, (int64_t)expert * a.dim + tile, 16, span, slot);
+  };
+  Cursor ask{wave, 0}, now{wave, 0};
+  int made = 0, done = 0;
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    if (ask.pair < pairs) {
+      request(ask, made++ % P);
+      next(ask);
+    }
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int kOps = S::kOps + S::kXOps;
+  const int pieces = (int)(a.w2.row_bytes / 16);
+  while (now.pair < pairs) {
+    const int u = now.pair / a.spans2, span = now.pair % a.spans2;
+    const int expert = __builtin_amdgcn_readfirstlane(down.expert[u]);
+    const int slot = done % P;
+    if (made - done == P)
+      wait_requests<(P - 1) * kOps>();
+    else
+      wait_requests<0>();
+    u32x4 x[S::kFrags];
+    S(base + slot * S::kXBytes).read_x(x, span, pieces);
+    const auto unit = S(base + (P - 1) * S::kXBytes).read_unit(a.w2, (int64_t)expert * a.dim + tile, 16, span, pieces, slot);
+    wait_lds();
+    if (ask.pair < pairs) {
+      request(ask, slot);
+      ++made;
+      next(ask);
+    }
+    acc = S::multiply(unit, x, 0u, acc);
+    ++done;
+    Cursor after = now;
+    next(after);
+    if (after.pair >= pairs || after.chunk != now.chunk || after.pair / a.spans2 != u) {
+      // columns of a token's parts meet, then go to its row of this wave's sums
+      f32x4 v = acc;
+      for (int q = 1; q < a.parts; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __shfl(acc[i], lane + q * chunk);
+      const uint64_t mask = all.mask[expert];
+      const int begin = now.chunk * chunk, have = min(chunk, __popcll(mask) - begin);
+      if (c < have) {
+        // the (begin + c)-th token of the mask
+        uint64_t m = mask;
+        for (int i = 0; i < begin + c; ++i) m &= m - 1;
+        const int t = __ffsll((unsigned long long)m) - 1;
+        float gate = 0.f;
+        for (int j = 0; j < a.top; ++j)
+          if (all.sel[t * a.top + j] == expert) gate = all.gate[t * a.top + j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float o = v[i];
+          if constexpr (!MX) o *= __uint_as_float((uint32_t)gmem(a.s2)[(int64_t)expert * a.dim + tile + 4 * g + i] << 16);
+          sums[wave][t * 16 + 4 * g + i] += gate * o;
+        }
+      }
+      acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    now = after;
+  }
+  __syncthreads();
+  for (int o = (int)threadIdx.x; o < a.tokens * 16; o += WAVES * 64) {
+    float v = 0.f;
+    for (int w = 0; w < WAVES; ++w) v += sums[w][o];
+    const int64_t at = (o >> 4) * a.y_stride + tile + (o & 15);
+    if (a.y32) gmem(a.y32)[at] = v;
+    if (a.y16) gmem(a.y16)[at] = f32_to_bf16(v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+
+constexpr int64_t kMoeMade = 0x77715f6d6f656631;
+
+static bool moe_sizes_ok(int64_t tokens, int64_t dim, int64_t f, int64_t e, int32_t top) {
+  return tokens >= 0 && tokens <= kMoeTokens && dim >= 16 && dim <= 32768 && dim % 16 == 0 && f >= 16 && f <= 32768 && f % 16 == 0 &&
+         e >= 1 && e <= kMoeExperts && top >= 1 && top <= kMoeTop && top <= e;
+}
+
+// Workspace: selections, gates, scores, activations.
+struct MoeSpace {
+  int64_t sel, gates, scores, act, all;
+};
+static MoeSpace moe_space(int64_t tokens, int64_t f, int64_t e, int32_t top) {
+  auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
+  MoeSpace s;
+  s.sel = 0;
+  s.gates = s.sel + up(4 * tokens * top);
+  s.scores = s.gates + up(4 * tokens * top);
+  s.act = s.scores + up(8 * tokens * e);
+  s.all = s.act + up(tokens * top * 3 * f * 2);
+  return s;
+}
+
+static int moe_check(const char* name, const wq_moe_ffn& a) {
+  if (!a.x || !a.w13 || !a.s13 || !a.w2 || !a.s2) return fail(WQ_ERR_NULL, "%s: x, w13, s13, w2 and s2 must be non-null", name);
+  if (!a.router == !a.logits) return fail(WQ_ERR_NULL, "%s: exactly one of router and logits must be given", name);
+  if (!a.y_f32 && !a.y_bf16) return fail(WQ_ERR_NULL, "%s: at least one of y_f32 / y_bf16 must be non-null", name);
+  if (a.format != WQ_FORMAT_INT8 && a.format != WQ_FORMAT_MXFP4)
+    return fail(WQ_ERR_SHAPE, "%s: format = %d (need WQ_FORMAT_INT8 or WQ_FORMAT_MXFP4)", name, a.format);
+  if (!moe_sizes_ok(a.tokens, a.dim, a.f, a.e, a.top))
+    return fail(WQ_ERR_SHAPE,
+                "%s: tokens = %lld (0..64), dim = %lld, f = %lld (multiples of 16 up to 32768), e = %lld (1..256), top = %d "
+                "(1..16, at most e)",
+                name, (long long)a.tokens, (long long)a.dim, (long long)a.f, (long long)a.e, a.top);
+  if (a.format == WQ_FORMAT_MXFP4 && (a.dim % kMxGroup || a.f % kMxGroup))
+    return fail(WQ_ERR_SHAPE, "%s: dim = %lld, f = %lld must be multiples of 32 for MXFP4", name, (long long)a.dim, (long long)a.f);
+  if (a.router && a.dim % 8) return fail(WQ_ERR_SHAPE, "%s: dim must be a multiple of 8", name);
+  const int64_t most = (int64_t)1 << 40;
+  if (a.x_stride < a.dim || a.x_stride > most || a.x_stride % 8)
+    return fail(WQ_ERR_SHAPE, "%s: x_stride = %lld must be a multiple of 8 and hold a row", name, (long long)a.x_stride);
+  if (a.y_stride < a.dim || a.y_stride > most)
+    return fail(WQ_ERR_SHAPE, "%s: y_stride = %lld must hold a row", name, (long long)a.y_stride);
+  if (!aligned16(a.x) || !aligned16(a.w13) || !aligned16(a.w2) || !aligned16(a.router))
+    return fail(WQ_ERR_ALIGN, "%s: x, w13, w2 and router must be 16-byte aligned", name);
+  if (((uintptr_t)a.s13 & 3) || ((uintptr_t)a.s2 & 3) || ((uintptr_t)a.logits & 3) || ((uintptr_t)a.y_f32 & 3) ||
+      ((uintptr_t)a.y_bf16 & 1) || ((uintptr_t)a.sel & 3) || ((uintptr_t)a.gates & 3))
+    return fail(WQ_ERR_ALIGN, "%s: s13 and s2 must be 4-byte aligned, logits, y, sel and gates to their elements", name);
+  return WQ_OK;
+}
+
+static int moe_overlap(const char* name, const wq_moe_ffn& a) {
+  const bool mx = a.format == WQ_FORMAT_MXFP4;
+  const int64_t up = a.e * 2 * a.f, down = a.e * a.dim;
+  const ByteRows out[] = {{a.y_f32, a.tokens, 4 * a.y_stride, 4 * a.dim},
+                          {a.y_bf16, a.tokens, 2 * a.y_stride, 2 * a.dim},
+                          {a.sel, 1, 0, 4 * a.tokens * a.top},
+                          {a.gates, 1, 0, 4 * a.tokens * a.top}};
+  const ByteRows in[] = {{a.x, a.tokens, 2 * a.x_stride, 2 * a.dim},
+                         {a.router, 1, 0, 2 * a.e * a.dim},
+                         {a.logits, 1, 0, 4 * a.tokens * a.e},
+                         {a.w13, 1, 0, mx ? up * a.dim / 2 : up * a.dim},
+                         {a.s13, 1, 0, mx ? up * a.dim / kMxGroup : up * 2},
+                         {a.w2, 1, 0, mx ? down * a.f / 2 : down * a.f},
+                         {a.s2, 1, 0, mx ? down * a.f / kMxGroup : down * 2}};
+  for (int i = 0; i < 4; ++i) {
+    for (const ByteRows& r : in)
+      if (rows_meet(out[i], r)) return fail(WQ_ERR_SHAPE, "%s: y, sel and gates must overlap no input", name);
+    for (int j = 0; j < i; ++j)
+      if (rows_meet(out[i], out[j])) return fail(WQ_ERR_SHAPE, "%s: y, sel and gates must not overlap each other", name);
+  }
+  return WQ_OK;
+}
+
+// Pairs of row tiles per workgroup and waves per tile, for `items` experts in use: the
+// fewest units in the longest chain.
+static void up_plan(MoeArgs& a, int waves, int items) {
+  double best = 1e300;
+  for (int ways = 1; ways <= waves; ways *= 2) {
+    const int teams = waves / ways;
+    for (int t = 1; t <= kUpTiles / 2; ++t) {
+      const int per = t * teams, blocks = (a.pairs + per - 1) / per;
+      const int64_t rounds = ((int64_t)blocks * items + 255) / 256;
+      const double cost = (double)rounds * (2.0 * t * ((a.spans + ways - 1) / ways) + 2.0);
+      if (cost < best) {
+        best = cost;
+        a.per = per;
+        a.ways = ways;
+        a.blocks = blocks;
+      }
+    }
+  }
+}
+
+template <bool MX, int COLS, int WAVES, int P>
+static void up_launch(MoeArgs a, hipStream_t s) {
+  const int picks = a.tokens * a.top, used = std::min(a.e, picks);
+  up_plan(a, WAVES, used);
+  const dim3 grid((unsigned)((used + picks / COLS) * a.blocks));
+  if (MX && a.w13.srow % 4)
+    hipLaunchKernelGGL((moe_up_kernel<MX, MX, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
+  else
+    hipLaunchKernelGGL((moe_up_kernel<MX, false, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
+}
+
+template <bool MX, int COLS, int WAVES, int P, int TM>
+static void down_launch(const MoeArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.dim / 16));
+  if (MX && a.w2.srow % 4)
+    hipLaunchKernelGGL((moe_down_kernel<MX, MX, COLS, WAVES, P, TM>), grid, dim3(WAVES * 64), 0, s, a);
+  else
+    hipLaunchKernelGGL((moe_down_kernel<MX, false, COLS, WAVES, P, TM>), grid, dim3(WAVES * 64), 0, s, a);
+}
+
+template <bool MX>
+static void experts_launch(MoeArgs a, hipStream_t s) {
+  if (a.tokens <= 4)
+    up_launch<MX, 4, 8, 3>(a, s);
+  else if (a.tokens <= 8)
+    up_launch<MX, 8, 8, 2>(a, s);
+  else
+    up_launch<MX, 16, 4, 4>(a, s);
+  a.here = 0;
+  if (a.tokens * a.parts <= 4)
+    down_launch<MX, 4, 8, 2, 2>(a, s);
+  else
+    down_launch<MX, 8, 4, 2, 64>(a, s);
+}
+
+}  // namespace wq
+
+using namespace wq;
+
+extern "C" int64_t wq_moe_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t f, int64_t e, int32_t top) {
+  if (!moe_sizes_ok(tokens, dim, f, e, top)) return 0;
+  return moe_space(tokens, f, e, top).all + 16;
+}
+
+extern "C" int wq_moe_ffn_prepare(const wq_moe_ffn* a, void* workspace, int64_t workspace_bytes, wq_moe_ffn_plan* plan) {
+  const char* name = "wq_moe_ffn_prepare";
+  if (!a || !plan || !workspace) return fail(WQ_ERR_NULL, "%s: a, workspace and plan must be non-null", name);
+  int rc = moe_check(name, *a);
+  if (rc) return rc;
+  const int64_t need = wq_moe_ffn_workspace_bytes(a->tokens, a->dim, a->f, a->e, a->top);
+  if (workspace_bytes < need)
+    return fail(WQ_ERR_SHAPE, "%s: workspace_bytes = %lld, %lld are needed", name, (long long)workspace_bytes,
+                (long long)need);
+  if (!aligned16(workspace)) return fail(WQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", name);
+  if ((rc = moe_overlap(name, *a))) return rc;
+  wq_moe_ffn_plan p{};
+  if ((rc = plan_device(name, &p.device))) return rc;
+  p.made = kMoeMade;
+  p.workspace = workspace;
+  p.a = *a;
+  *plan = p;
+  return WQ_OK;
+}
+
+extern "C" int wq_moe_ffn_run(const wq_moe_ffn_plan* plan, void* stream) {
+  const char* name = "wq_moe_ffn_run";
+  if (!plan) return fail(WQ_ERR_NULL, "%s: plan must be non-null", name);
+  if (plan->made != kMoeMade) return fail(WQ_ERR_SHAPE, "%s: the plan was not made by wq_moe_ffn_prepare", name);
+  int rc = same_device(name, plan->device);
+  if (rc) return rc;
+  const wq_moe_ffn& m = plan->a;
+  if (m.tokens == 0) return WQ_OK;
+  const bool mx = m.format == WQ_FORMAT_MXFP4;
+  const MoeSpace at = moe_space(m.tokens, m.f, m.e, m.top);
+  char* ws = static_cast<char*>(plan->workspace);
+  MoeArgs a{};
+  a.x = m.x;
+  a.x_stride = m.x_stride;
+  a.router = m.router;
+  a.logits = m.logits;
+  a.sel = reinterpret_cast<int32_t*>(ws + at.sel);
+  a.gates = reinterpret_cast<float*>(ws + at.gates);
+  a.scores = m.router ? reinterpret_cast<double*>(ws + at.scores) : nullptr;
+  a.act = reinterpret_cast<uint16_t*>(ws + at.act);
+  a.user_sel = m.sel;
+  a.user_gates = m.gates;
+  const uint32_t up = (uint32_t)(mx ? m.dim / 2 : m.dim), down = (uint32_t)(mx ? m.f / 2 : m.f);
+  a.w13 = {static_cast<const uint8_t*>(m.w13), static_cast<const uint8_t*>(m.s13), m.e * 2 * m.f, up, (uint32_t)(m.dim / kMxGroup)};
+  a.w2 = {static_cast<const uint8_t*>(m.w2), static_cast<const uint8_t*>(m.s2), m.e * m.dim, down, (uint32_t)(m.f / kMxGroup)};
+  a.s13 = static_cast<const uint16_t*>(m.s13);
+  a.s2 = static_cast<const uint16_t*>(m.s2);
+  a.y32 = m.y_f32;
+  a.y16 = m.y_bf16;
+  a.y_stride = m.y_stride;
+  a.tokens = (int32_t)m.tokens;
+  a.dim = (int32_t)m.dim;
+  a.f = (int32_t)m.f;
+  a.e = (int32_t)m.e;
+  a.top = m.top;
+  a.renormalize = m.renormalize;
+  a.parts = m.y_f32 ? 3 : 2;
+  a.pairs = a.f / 16;
+  a.spans = (int32_t)((up + 255) / 256);
+  a.spans2 = (int32_t)((down + 255) / 256);
+  a.here = m.logits && m.tokens <= 8;
+  hipStream_t s = (hipStream_t)stream;
+  if (m.router) {
+    // a workgroup reads up to 128 KB of router rows
+    const int shares = (int)std::min<int64_t>(m.e, (m.e * m.dim + 65535) / 65536);
+    hipLaunchKernelGGL(moe_score_kernel, dim3((unsigned)m.tokens, (unsigned)shares), dim3(kScoreWaves * 64), 0, s, a);
+    if (shares > 1) hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)m.tokens), dim3(64), 0, s, a);
+  } else if (!a.here) {
+    hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)m.tokens), dim3(64), 0, s, a);
+  }
+  if (mx)
+    experts_launch<true>(a, s);
+  else
+    experts_launch<false>(a, s);
+  return launch_status(name);
+}
