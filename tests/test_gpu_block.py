@@ -190,7 +190,8 @@ def _product(wq, rng, m, n, k, xkind, out, pad=0):
 
 SHAPES = [(1, 1, 32), (1, 16, 64), (1, 17, 96), (2, 33, 128), (3, 100, 160), (4, 256, 512), (5, 129, 544), (8, 64, 1024),
           (7, 515, 1056), (9, 48, 2080), (15, 31, 512), (16, 1000, 4096), (1, 4100, 4096), (17, 70, 1504), (33, 130, 2048),
-          (63, 257, 608), (64, 128, 8192), (65, 96, 160), (129, 515, 1056), (200, 300, 2560), (257, 260, 96), (515, 129, 640)]
+          (63, 257, 608), (64, 128, 8192), (65, 96, 160), (129, 515, 1056), (200, 300, 2560), (257, 260, 96), (515, 129, 640),
+          (300, 260, 4096), (2051, 5600, 96), (1030, 12010, 64), (4100, 2900, 672)]
 
 
 @pytest.mark.parametrize("xkind", ["bf16", "mxfp4"])

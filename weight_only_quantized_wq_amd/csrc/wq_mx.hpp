@@ -17,6 +17,12 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int kMxGroup = 32;
 constexpr int64_t kMxMost = (int64_t)1 << 40;     // weights of one call
 
+// A constant index for a generic lambda.
+template <int V>
+struct At {
+  static constexpr int value = V;
+};
+
 // Scale byte `j` of a word, as the fp32 operand of the conversions below.  They look
 // at its exponent field only, so byte 0 stands for 2^-127 and 255 for NaN.
 __device__ __forceinline__ float mx_scale(uint32_t word, int j) {

@@ -9,6 +9,8 @@
 
 #include "wq_host.hpp"
 #include "wq_kv.hpp"
+#include "wq_mx_split.hpp"
+#include "wq_mx_tile.hpp"
 #include "wq_row_stream.hpp"
 
 namespace wq {
@@ -111,6 +113,65 @@ static int rows_launch(const char* name, MxRowsArgs a, hipStream_t s) {
   return launch_status(name);
 }
 
+// Bytes of a padded row of scales, and whether rows need padding.
+static uint32_t pad_stride(int64_t k) { return (uint32_t)((k / kMxGroup + 7) / 8 * 8); }
+static bool needs_pad(int64_t k) { return k / kMxGroup % 8 != 0; }
+
+constexpr int64_t kRowsMost = 16;                // rows of x that mx_rows_kernel takes
+
+template <bool XQ, int TN, int TM, int WN, int WM>
+static int tile_launch(const char* name, MxTileArgs a, hipStream_t s) {
+  using T = TileShape<XQ, TN, TM, WN, WM>;
+  a.tn = (a.n + T::BN - 1) / T::BN;
+  a.tm = (a.m + T::BM - 1) / T::BM;
+  const int per = (a.tn * a.tm + 7) / 8;
+  hipLaunchKernelGGL((mx_tile_kernel<XQ, TN, TM, WN, WM>), dim3((unsigned)(per * 8), 1), dim3(T::kWaves * 64), 0, s, a);
+  return launch_status(name);
+}
+
+// Tiles of mx_split_kernel: 128 rows of W (64 with 4-bit activations) x up to 64 of x.
+struct SplitPlan {
+  int tn, tm, tmt, splits, share;
+};
+static int stages_of(int64_t k, bool xq) { return (int)(xq ? (k + 255) / 256 : (k + 63) / 64); }
+static SplitPlan split_plan(int64_t m, int64_t n, int64_t k, bool xq) {
+  SplitPlan p;
+  p.tmt = m <= 32 ? 2 : 4;
+  p.tm = (int)((m + 16 * p.tmt - 1) / (16 * p.tmt));
+  const int bn = xq ? 64 : 128, stages = stages_of(k, xq);
+  p.tn = (int)((n + bn - 1) / bn);
+  // about one workgroup per CU, each wave at least two stages
+  const int64_t tiles = (int64_t)p.tn * p.tm, most = std::max(1, stages / (2 * kSplitWaves));
+  const int64_t want = std::max<int64_t>(1, 256 / tiles);
+  const int splits = (int)std::min(want, most);
+  p.share = (stages + splits - 1) / splits;
+  p.splits = (stages + p.share - 1) / p.share;
+  return p;
+}
+// Whether tiles of 256 x 256 are the faster: by rounds of workgroups over the 256 CUs, a
+// product in split tiles taking half as long again.
+static bool big_tiles(int64_t m, int64_t n, int64_t k, bool xq) {
+  const SplitPlan p = split_plan(m, n, k, xq);
+  const int64_t big = ((m + 255) / 256) * ((n + 255) / 256), small = (int64_t)p.tn * p.tm * p.splits;
+  const double part = (xq ? 64. : 128.) * 16 * p.tmt / (256. * 256.) / p.splits;
+  return (double)((big + 255) / 256) <= 1.5 * part * (double)((small + 255) / 256);
+}
+
+template <bool XQ, int TN, int TM, int P>
+static int split_launch(const char* name, MxTileArgs a, const SplitPlan& p, hipStream_t s) {
+  a.tn = p.tn;
+  a.tm = p.tm;
+  a.share = p.share;
+  if (p.splits == 1) a.part = nullptr;
+  hipLaunchKernelGGL((mx_split_kernel<XQ, TN, TM, P>), dim3((unsigned)(p.tn * p.tm), (unsigned)p.splits), dim3(kSplitWaves * 64), 0,
+                     s, a);
+  if (p.splits > 1) {
+    const int64_t quads = (int64_t)a.m * ((a.n + 3) / 4);
+    hipLaunchKernelGGL(mx_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, a, p.splits);
+  }
+  return launch_status(name);
+}
+
 static int gemm_check(const char* name, const wq_gemm_mxfp4& a) {
   if (!a.x == !a.xq) return fail(WQ_ERR_NULL, "%s: exactly one of x and xq must be given", name);
   if (a.xq && !a.x_scale) return fail(WQ_ERR_NULL, "%s: xq needs x_scale", name);
@@ -150,7 +211,17 @@ using namespace wq;
 
 extern "C" int64_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (m < 0 || m > kGemmMaxM || n < 0 || n > kGemmMaxN || k < kMxGroup || k > kGemmMaxK || k % kMxGroup) return 0;
-  return 16;
+  int64_t bytes = 16;
+  if (m <= kRowsMost) return bytes;
+  // padded scales, then shares of k (of either kind of activations)
+  if (needs_pad(k)) bytes += ((m + n) * pad_stride(k) + 15) / 16 * 16;
+  {
+    int most = 1;
+    for (bool xq : {false, true})
+      if (!big_tiles(m, n, k, xq)) most = std::max(most, split_plan(m, n, k, xq).splits);
+    if (most > 1) bytes += (int64_t)most * m * ((n + 3) / 4 * 4) * 4;
+  }
+  return bytes;
 }
 
 extern "C" int wq_gemm_mxfp4_prepare(const wq_gemm_mxfp4* a, void* workspace, int64_t workspace_bytes,
@@ -195,6 +266,43 @@ extern "C" int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream) {
   a.tiles = (int32_t)((g.n + 15) / 16);
   a.spans = (int32_t)((g.k + 511) / 512);
   hipStream_t s = (hipStream_t)stream;
+  if (g.m > kRowsMost) {
+    MxTileArgs t{};
+    t.w = g.q;
+    t.wscale = g.scale;
+    t.x = a.x;
+    t.xscale = g.x_scale;
+    t.x_stride = a.x_stride;
+    t.y32 = g.y_f32;
+    t.y16 = g.y_bf16;
+    t.y_stride = g.y_stride;
+    t.m = (int32_t)g.m;
+    t.n = (int32_t)g.n;
+    t.w_bytes = a.w.row_bytes;
+    t.x_bytes = a.x_bytes;
+    t.sstride = pad_stride(g.k);
+    t.stages = stages_of(g.k, g.xq);
+    t.vec = g.y_stride % 4 == 0 && aligned16(g.y_f32) && !((uintptr_t)g.y_bf16 & 7);
+    if (needs_pad(g.k)) {
+      uint8_t* to = static_cast<uint8_t*>(plan->workspace);
+      auto pad = [&](const uint8_t* from, int64_t rows) {
+        const int64_t blocks = std::min<int64_t>((rows * (t.sstride / 4) + 255) / 256, 2048);
+        hipLaunchKernelGGL(mx_pad_kernel, dim3((unsigned)blocks), dim3(256), 0, s, from, rows, a.w.srow, t.sstride, to);
+        const uint8_t* padded = to;
+        to += rows * t.sstride;
+        return padded;
+      };
+      t.wscale = pad(g.scale, g.n);
+      if (g.xq) t.xscale = pad(g.x_scale, g.m);
+    }
+    if (big_tiles(g.m, g.n, g.k, g.xq))
+      return g.xq ? tile_launch<true, 8, 4, 2, 4>(name, t, s) : tile_launch<false, 8, 4, 2, 4>(name, t, s);
+    t.part = reinterpret_cast<float*>(static_cast<char*>(plan->workspace) +
+                                      (needs_pad(g.k) ? ((g.m + g.n) * t.sstride + 15) / 16 * 16 : 0));
+    const SplitPlan p = split_plan(g.m, g.n, g.k, g.xq);
+    if (g.xq) return p.tmt == 2 ? split_launch<true, 4, 2, 2>(name, t, p, s) : split_launch<true, 4, 4, 2>(name, t, p, s);
+    return p.tmt == 2 ? split_launch<false, 8, 2, 4>(name, t, p, s) : split_launch<false, 8, 4, 3>(name, t, p, s);
+  }
   if (g.xq) return rows_launch<true, 16, 8, 3>(name, a, s);
   if (g.m <= 4) return rows_launch<false, 4, 8, 3>(name, a, s);
   if (g.m <= 8) return rows_launch<false, 8, 8, 2>(name, a, s);

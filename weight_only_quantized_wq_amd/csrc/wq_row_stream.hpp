@@ -34,10 +34,6 @@ struct StreamWeights {
 
 // step(0), step(1), ... below `count`, at most RT of them, with the index a constant (so
 // that registers can be indexed by it).
-template <int V>
-struct At {
-  static constexpr int value = V;
-};
 template <int RT, int T = 0, class F>
 __device__ __forceinline__ void for_tiles(int count, F step) {
   if constexpr (T < RT) {
