@@ -6,8 +6,8 @@
 //   route    the `top` largest scores of each token and their gates
 //   up       a workgroup takes a block of rows of W1 and W3 of one expert over the
 //            tokens that chose it: h1, h3 meet in LDS, silu(h1) h3 goes to the workspace
-//   down     a workgroup takes 16 rows of W2 of every expert in use, so that the sum
-//            over experts stays inside it; its waves split (expert, span of f)
+//   down     the same for rows of W2; results go to the workspace, weighted by the gate
+//   join     a token's experts are added in the order of its selection
 //
 // A token's experts are distinct and there are at most 64 tokens, so the tokens of an
 // expert are a 64-bit mask, which every workgroup builds itself from the selections.
@@ -36,6 +36,7 @@ struct MoeArgs {
   int32_t* user_sel;       // the caller's copies, or null
   float* user_gates;
   uint16_t* act;           // [tokens * top][parts][f], in the order of experts
+  float* sums;             // [tokens * top][dim], in the order of selection, weighted
   StreamWeights w13, w2;
   const uint16_t* s13;     // int8: row scales
   const uint16_t* s2;
@@ -45,31 +46,42 @@ struct MoeArgs {
   int32_t tokens, dim, f, e, top, renormalize;
   int32_t here;            // the selection is made by the up launch itself
   int32_t parts;
-  int32_t pairs, per, ways, blocks, spans;   // up: row tiles of W1 (and W3), of a workgroup; waves per tile
-  int32_t spans2;
+  int32_t spans, spans2;   // of a row of W1, of W2
+  // of a launch: pairs of row tiles (up) or tiles (down) of a workgroup, workgroups of an
+  // expert's rows, waves that share a tile's spans
+  int32_t pairs, per, blocks, ways;
 };
 
 // ---------------------------------------------------------------------------
 // Scores and selection
 
 constexpr int kScoreWaves = 16, kScoreBatch = 4;
+constexpr int kScoreParts = 16;                  // at most, of k
 
-template <int N>
-__device__ __forceinline__ double wave_sum64(double v) {
+// Wave-wide sums of four values; lane 16 i ends with that of v[i] (halves of the wave
+// keep two each, quarters one, so seven exchanges do for four sums).
+__device__ __forceinline__ double wave_sum4(const double (&v)[4]) {
+  const int lane = lane_id();
+  const bool high = lane & 32, odd = lane & 16;
+  const double a = (high ? v[2] : v[0]) + __shfl_xor(high ? v[0] : v[2], 32);
+  const double b = (high ? v[3] : v[1]) + __shfl_xor(high ? v[1] : v[3], 32);
+  double s = (odd ? b : a) + __shfl_xor(odd ? a : b, 16);
 #pragma unroll
-  for (int d = N / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  for (int d = 8; d >= 1; d >>= 1) s += __shfl_xor(s, d);
+  return s;
 }
 
-// Experts first .. last - 1 of token t, by the waves of a workgroup; put(e, score) is
-// called in one lane.
-template <class Put>
-__device__ __forceinline__ void score_experts(const MoeArgs& a, int t, int first, int last, Put put) {
-  const int lane = lane_id();
+// Sums of experts first .. last - 1 of token t over `parts` shares of k: the waves of a
+// workgroup take (four experts, share) units, part[share][expert - first].
+__device__ __forceinline__ void score_experts(const MoeArgs& a, int t, int first, int last, int parts,
+                                              double (&part)[kScoreParts][kMoeExperts]) {
+  const int lane = lane_id(), units = (last - first + kScoreBatch - 1) / kScoreBatch * parts;
+  const int share = (a.dim / 8 + parts * 64 - 1) / (parts * 64) * 512;
   const uint16_t* x = a.x + t * a.x_stride;
-  for (int e = first + wave_id() * kScoreBatch; e < last; e += kScoreWaves * kScoreBatch) {
+  for (int u = wave_id(); u < units; u += kScoreWaves) {
+    const int e = first + u / parts * kScoreBatch, p = u % parts, end = min((p + 1) * share, a.dim);
     double sum[kScoreBatch] = {0., 0., 0., 0.};
-    for (int i = lane * 8; i < a.dim; i += 512) {
+    for (int i = p * share + lane * 8; i < end; i += 512) {
       const u32x4 xv = load16(x + i);
       u32x4 wv[kScoreBatch];
 #pragma unroll
@@ -84,11 +96,8 @@ __device__ __forceinline__ void score_experts(const MoeArgs& a, int t, int first
         }
       }
     }
-#pragma unroll
-    for (int b = 0; b < kScoreBatch; ++b) {
-      const double v = wave_sum64<64>(sum[b]);
-      if (lane == 0 && e + b < last) put(e + b, v);
-    }
+    const double v = wave_sum4(sum);
+    if ((lane & 15) == 0 && e + (lane >> 4) < last) part[p][e + (lane >> 4) - first] = v;
   }
 }
 
@@ -177,21 +186,26 @@ __device__ __forceinline__ void put_selection(const MoeArgs& a, int t, int j, in
 }
 
 // Scores of a token's experts by one workgroup, which selects at once; or of a share of
-// them (gridDim.y > 1), for route_kernel.
+// them (gridDim.y > 1), for moe_route_kernel.
 __global__ __launch_bounds__(kScoreWaves * 64) void moe_score_kernel(MoeArgs a) {
-  __shared__ double score[kMoeExperts];
+  __shared__ double part[kScoreParts][kMoeExperts];
   const int t = (int)blockIdx.x, share = (a.e + (int)gridDim.y - 1) / (int)gridDim.y;
   const int first = (int)blockIdx.y * share, last = min(first + share, a.e);
-  score_experts(a, t, first, last, [&](int e, double v) {
-    if (gridDim.y == 1)
-      score[e] = v;
-    else
-      a.scores[t * a.e + e] = v;
-  });
-  if (gridDim.y > 1) return;
+  // enough units for the waves, each at least 512 inputs
+  const int batches = (last - first + kScoreBatch - 1) / kScoreBatch;
+  const int parts = max(1, min(min(kScoreParts, (kScoreWaves + batches - 1) / max(batches, 1)), (a.dim + 511) / 512));
+  score_experts(a, t, first, last, parts, part);
   __syncthreads();
-  if (wave_id() == 0)
-    select_experts(a, [&](int e) { return score[e]; }, [&](int j, int e, float g) { put_selection(a, t, j, e, g); });
+  auto score = [&](int e) {
+    double v = part[0][e - first];
+    for (int p = 1; p < parts; ++p) v += part[p][e - first];
+    return v;
+  };
+  if (gridDim.y > 1) {
+    for (int e = first + (int)threadIdx.x; e < last; e += kScoreWaves * 64) a.scores[t * a.e + e] = score(e);
+  } else if (wave_id() == 0) {
+    select_experts(a, score, [&](int j, int e, float g) { put_selection(a, t, j, e, g); });
+  }
 }
 
 __global__ __launch_bounds__(64) void moe_route_kernel(MoeArgs a) {
@@ -364,7 +378,98 @@ __global__ __launch_bounds__(WAVES * 64) void moe_up_kernel(MoeArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Second product and the sum over experts
+// Second products, and the sum over a token's experts
+
+template <bool MX, bool ODD, int COLS, int WAVES, int P>
+__global__ __launch_bounds__(WAVES * 64) void moe_down_kernel(MoeArgs a) {
+  using S = RowStream<MX, false, ODD, COLS, P>;
+  constexpr int kRed = WAVES * kUpTiles * 1024, kAll = WAVES * S::kBytes;
+  __shared__ __align__(1024) char lds[kAll > kRed ? kAll : kRed];
+  MoeTokens& all = *reinterpret_cast<MoeTokens*>(lds);
+  static_assert(sizeof(MoeTokens) <= sizeof(lds));
+  __shared__ float gate[COLS];
+  __shared__ int pick[COLS];
+  find_tokens<WAVES>(a, all);
+  const int chunk = COLS / a.parts;                 // tokens; a column for each of their parts
+  int expert, begin, slot;
+  if (!find_item(all, (int)blockIdx.x / a.blocks, chunk, expert, begin, slot)) return;
+  const uint64_t mask = all.mask[expert];
+  const int have = min(chunk, __popcll(mask) - begin);
+  if (wave_id() == 0) {
+    const int lane = lane_id(), rank = __popcll(mask & ((1ull << lane) - 1)) - begin;
+    if ((mask >> lane & 1) && rank >= 0 && rank < chunk)
+      for (int j = 0; j < a.top; ++j)
+        if (all.sel[lane * a.top + j] == expert) {
+          gate[rank] = all.gate[lane * a.top + j];
+          pick[rank] = lane * a.top + j;
+        }
+  }
+  __syncthreads();
+  const int wave = wave_id(), ways = a.ways, kw = wave % ways, tw = wave / ways, teams = WAVES / ways;
+  const S s(lds + wave * S::kBytes);
+  const int first = (int)blockIdx.x % a.blocks * a.per, mine = min(a.per, a.dim / 16 - first);
+  const int tiles = (mine - tw + teams - 1) / teams;
+  f32x4 acc[kUpTiles];
+#pragma unroll
+  for (int t = 0; t < kUpTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t rows0 = (int64_t)expert * a.dim;
+  const uint16_t* act = a.act + (int64_t)(slot + begin) * a.parts * a.f;
+  s.template run<kUpTiles>(
+      a.w2, tiles, kw, ways, a.spans2, (int)(a.w2.row_bytes / 16),
+      [&](int t, int64_t& row0, int& left) {
+        row0 = rows0 + (int64_t)(first + tw + t * teams) * 16;
+        left = 16;
+      },
+      // columns: part after part, `chunk` tokens each
+      [&](int col) {
+        const int part = min(col / chunk, a.parts - 1), tok = min(col % chunk, have - 1);
+        return reinterpret_cast<const char*>(act + (int64_t)(tok * a.parts + part) * a.f);
+      },
+      2u * a.f, nullptr, 0, 0, 1, acc);
+  __syncthreads();
+  for_tiles<kUpTiles>(tiles, [&](auto at) __attribute__((always_inline)) {
+    *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * 1024 + s.lane * 16) = acc[at.value];
+  });
+  __syncthreads();
+  for (int o = (int)threadIdx.x; o < mine * 16 * have; o += WAVES * 64) {
+    const int row = o & 15, tok = (o >> 4) % have, tile = (o >> 4) / have;
+    const char* from = lds + ((tile % teams) * ways * kUpTiles + tile / teams) * 1024 + ((row >> 2) * 16 + tok) * 16 + (row & 3) * 4;
+    float v = 0.f;
+    for (int q = a.parts - 1; q >= 0; --q)
+      for (int w = 0; w < ways; ++w) v += *reinterpret_cast<const float*>(from + w * kUpTiles * 1024 + q * chunk * 16);
+    const int r = (first + tile) * 16 + row;
+    if constexpr (!MX) v *= __uint_as_float((uint32_t)gmem(a.s2)[rows0 + r] << 16);
+    gmem(a.sums)[(int64_t)pick[tok] * a.dim + r] = gate[tok] * v;
+  }
+}
+
+// A token's experts summed in the order of selection.
+__global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
+  const int o = (int)(blockIdx.x * 256 + threadIdx.x), quads = a.dim / 4;
+  if (o >= a.tokens * quads) return;
+  const int t = o / quads, col = o % quads * 4;
+  const float* from = a.sums + (int64_t)t * a.top * a.dim + col;
+  f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < a.top; j += 4) {
+    f32x4 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *gmem(reinterpret_cast<const f32x4*>(from + (int64_t)min(j + i, a.top - 1) * a.dim));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (j + i < a.top) v += p[i];
+  }
+  const int64_t at = t * a.y_stride + col;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (a.y32) gmem(a.y32)[at + i] = v[i];
+    if (a.y16) gmem(a.y16)[at + i] = f32_to_bf16(v[i]);
+  }
+}
+
+// One token, or two: a workgroup takes 16 rows of W2 of every expert in use, so that the
+// sum over experts stays inside it and nothing is joined; its waves take (expert, span)
+// pairs in turn, each with the activations that meet it.  (One token of Mixtral's int8
+// layer: 25.4 us, where moe_down_kernel and the join take 26.9 and 4.7.)
 
 // The experts in use, in order.
 struct MoeDown {
@@ -374,7 +479,7 @@ struct MoeDown {
 };
 
 template <bool MX, bool ODD, int COLS, int WAVES, int P, int TM>
-__global__ __launch_bounds__(WAVES * 64) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
   using S = RowStream<MX, false, ODD, COLS, P>;
   // a unit is a span of W2's rows and of the activations that meet it; both have P slots
   constexpr int kWave0 = S::kXBytes * (P - 1) + S::kBytes;
@@ -515,6 +620,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_down_kernel(MoeArgs a) {
 // ---------------------------------------------------------------------------
 // Host side
 
+constexpr int64_t kScoreMost = 1 << 16;
 constexpr int64_t kMoeMade = 0x77715f6d6f656631;
 
 static bool moe_sizes_ok(int64_t tokens, int64_t dim, int64_t f, int64_t e, int32_t top) {
@@ -522,18 +628,19 @@ static bool moe_sizes_ok(int64_t tokens, int64_t dim, int64_t f, int64_t e, int3
          e >= 1 && e <= kMoeExperts && top >= 1 && top <= kMoeTop && top <= e;
 }
 
-// Workspace: selections, gates, scores, activations.
+// Workspace: selections, gates, scores, activations, weighted results.
 struct MoeSpace {
-  int64_t sel, gates, scores, act, all;
+  int64_t sel, gates, scores, act, sums, all;
 };
-static MoeSpace moe_space(int64_t tokens, int64_t f, int64_t e, int32_t top) {
+static MoeSpace moe_space(int64_t tokens, int64_t dim, int64_t f, int64_t e, int32_t top) {
   auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
   MoeSpace s;
   s.sel = 0;
   s.gates = s.sel + up(4 * tokens * top);
   s.scores = s.gates + up(4 * tokens * top);
   s.act = s.scores + up(8 * tokens * e);
-  s.all = s.act + up(tokens * top * 3 * f * 2);
+  s.sums = s.act + up(tokens * top * 3 * f * 2);
+  s.all = s.sums + up(tokens * top * dim * 4);
   return s;
 }
 
@@ -587,16 +694,16 @@ static int moe_overlap(const char* name, const wq_moe_ffn& a) {
   return WQ_OK;
 }
 
-// Pairs of row tiles per workgroup and waves per tile, for `items` experts in use: the
-// fewest units in the longest chain.
-static void up_plan(MoeArgs& a, int waves, int items) {
+// Row tiles of a workgroup (`each` at once, of `tiles` such) and waves per tile, for
+// `items` experts in use: the fewest units in the longest chain.
+static void rows_plan(MoeArgs& a, int waves, int items, int tiles, int each, int spans) {
   double best = 1e300;
   for (int ways = 1; ways <= waves; ways *= 2) {
     const int teams = waves / ways;
-    for (int t = 1; t <= kUpTiles / 2; ++t) {
-      const int per = t * teams, blocks = (a.pairs + per - 1) / per;
+    for (int t = 1; t <= kUpTiles / each; ++t) {
+      const int per = t * teams, blocks = (tiles + per - 1) / per;
       const int64_t rounds = ((int64_t)blocks * items + 255) / 256;
-      const double cost = (double)rounds * (2.0 * t * ((a.spans + ways - 1) / ways) + 2.0);
+      const double cost = (double)rounds * ((double)each * t * ((spans + ways - 1) / ways) + 2.0);
       if (cost < best) {
         best = cost;
         a.per = per;
@@ -610,7 +717,8 @@ static void up_plan(MoeArgs& a, int waves, int items) {
 template <bool MX, int COLS, int WAVES, int P>
 static void up_launch(MoeArgs a, hipStream_t s) {
   const int picks = a.tokens * a.top, used = std::min(a.e, picks);
-  up_plan(a, WAVES, used);
+  a.pairs = a.f / 16;
+  rows_plan(a, WAVES, used, a.pairs, 2, a.spans);
   const dim3 grid((unsigned)((used + picks / COLS) * a.blocks));
   if (MX && a.w13.srow % 4)
     hipLaunchKernelGGL((moe_up_kernel<MX, MX, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
@@ -618,28 +726,39 @@ static void up_launch(MoeArgs a, hipStream_t s) {
     hipLaunchKernelGGL((moe_up_kernel<MX, false, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
 }
 
-template <bool MX, int COLS, int WAVES, int P, int TM>
-static void down_launch(const MoeArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.dim / 16));
+template <bool MX, int COLS, int WAVES, int P>
+static void down_launch(MoeArgs a, hipStream_t s) {
+  const int picks = a.tokens * a.top, used = std::min(a.e, picks);
+  rows_plan(a, WAVES, used, a.dim / 16, 1, a.spans2);
+  const dim3 grid((unsigned)((used + picks / (COLS / a.parts)) * a.blocks));
   if (MX && a.w2.srow % 4)
-    hipLaunchKernelGGL((moe_down_kernel<MX, MX, COLS, WAVES, P, TM>), grid, dim3(WAVES * 64), 0, s, a);
+    hipLaunchKernelGGL((moe_down_kernel<MX, MX, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((moe_down_kernel<MX, false, COLS, WAVES, P, TM>), grid, dim3(WAVES * 64), 0, s, a);
+    hipLaunchKernelGGL((moe_down_kernel<MX, false, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
 }
 
 template <bool MX>
 static void experts_launch(MoeArgs a, hipStream_t s) {
+  const int mean = (a.tokens * a.top + a.e - 1) / a.e;      // tokens of an expert
   if (a.tokens <= 4)
     up_launch<MX, 4, 8, 3>(a, s);
-  else if (a.tokens <= 8)
+  else if (a.tokens <= 8 || 2 * mean <= 8)
     up_launch<MX, 8, 8, 2>(a, s);
   else
     up_launch<MX, 16, 4, 4>(a, s);
   a.here = 0;
-  if (a.tokens * a.parts <= 4)
-    down_launch<MX, 4, 8, 2, 2>(a, s);
+  if (a.tokens * a.parts <= 4) {
+    if (MX && a.w2.srow % 4)
+      hipLaunchKernelGGL((moe_few_kernel<MX, MX, 4, 8, 2, 2>), dim3((unsigned)(a.dim / 16)), dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((moe_few_kernel<MX, false, 4, 8, 2, 2>), dim3((unsigned)(a.dim / 16)), dim3(512), 0, s, a);
+    return;
+  }
+  if (a.tokens * a.parts <= 8 || 2 * mean * a.parts <= 8)
+    down_launch<MX, 8, 8, 2>(a, s);
   else
-    down_launch<MX, 8, 4, 2, 64>(a, s);
+    down_launch<MX, 16, 4, 4>(a, s);
+  hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.tokens * (a.dim / 4) + 255) / 256)), dim3(256), 0, s, a);
 }
 
 }  // namespace wq
@@ -648,7 +767,7 @@ using namespace wq;
 
 extern "C" int64_t wq_moe_ffn_workspace_bytes(int64_t tokens, int64_t dim, int64_t f, int64_t e, int32_t top) {
   if (!moe_sizes_ok(tokens, dim, f, e, top)) return 0;
-  return moe_space(tokens, f, e, top).all + 16;
+  return moe_space(tokens, dim, f, e, top).all + 16;
 }
 
 extern "C" int wq_moe_ffn_prepare(const wq_moe_ffn* a, void* workspace, int64_t workspace_bytes, wq_moe_ffn_plan* plan) {
@@ -680,7 +799,7 @@ extern "C" int wq_moe_ffn_run(const wq_moe_ffn_plan* plan, void* stream) {
   const wq_moe_ffn& m = plan->a;
   if (m.tokens == 0) return WQ_OK;
   const bool mx = m.format == WQ_FORMAT_MXFP4;
-  const MoeSpace at = moe_space(m.tokens, m.f, m.e, m.top);
+  const MoeSpace at = moe_space(m.tokens, m.dim, m.f, m.e, m.top);
   char* ws = static_cast<char*>(plan->workspace);
   MoeArgs a{};
   a.x = m.x;
@@ -691,6 +810,7 @@ extern "C" int wq_moe_ffn_run(const wq_moe_ffn_plan* plan, void* stream) {
   a.gates = reinterpret_cast<float*>(ws + at.gates);
   a.scores = m.router ? reinterpret_cast<double*>(ws + at.scores) : nullptr;
   a.act = reinterpret_cast<uint16_t*>(ws + at.act);
+  a.sums = reinterpret_cast<float*>(ws + at.sums);
   a.user_sel = m.sel;
   a.user_gates = m.gates;
   const uint32_t up = (uint32_t)(mx ? m.dim / 2 : m.dim), down = (uint32_t)(mx ? m.f / 2 : m.f);
@@ -708,14 +828,13 @@ extern "C" int wq_moe_ffn_run(const wq_moe_ffn_plan* plan, void* stream) {
   a.top = m.top;
   a.renormalize = m.renormalize;
   a.parts = m.y_f32 ? 3 : 2;
-  a.pairs = a.f / 16;
   a.spans = (int32_t)((up + 255) / 256);
   a.spans2 = (int32_t)((down + 255) / 256);
   a.here = m.logits && m.tokens <= 8;
   hipStream_t s = (hipStream_t)stream;
   if (m.router) {
     // a workgroup reads up to 128 KB of router rows
-    const int shares = (int)std::min<int64_t>(m.e, (m.e * m.dim + 65535) / 65536);
+    const int shares = (int)std::min<int64_t>(m.e, (m.e * m.dim + kScoreMost - 1) / kScoreMost);
     hipLaunchKernelGGL(moe_score_kernel, dim3((unsigned)m.tokens, (unsigned)shares), dim3(kScoreWaves * 64), 0, s, a);
     if (shares > 1) hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)m.tokens), dim3(64), 0, s, a);
   } else if (!a.here) {

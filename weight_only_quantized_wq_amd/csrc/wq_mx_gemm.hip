@@ -55,7 +55,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxRowsArgs a) {
         row0 = (int64_t)(first + tw + t * teams) * 16;
         left = (int)min((int64_t)16, a.w.rows - row0);
       },
-      [&](int col) { return x + min(col, cols - 1) * a.x_stride; }, a.x_bytes, a.xscale, a.m, m0, cols, acc);
+      [&](int col) { return x + min(col, cols - 1) * a.x_stride; }, a.x_bytes, a.xscale, a.m, m0, cols, acc, (int)blockIdx.x);
   // the waves' sums of a tile, lane by lane
   __syncthreads();
   for_tiles<kRowTiles>(tiles, [&](auto at) __attribute__((always_inline)) {
@@ -85,7 +85,8 @@ constexpr int64_t kGemmMaxM = 1 << 20, kGemmMaxN = 1 << 24, kGemmMaxK = 1 << 18;
 // two units' worth for what a workgroup costs besides.
 static void rows_plan(MxRowsArgs& a, int waves, int most, int64_t chunks) {
   double best = 1e300;
-  for (int ways = 1; ways <= waves; ways *= 2) {
+  for (int ways = 1; ways <= waves; ++ways) {
+    if (waves % ways) continue;
     const int teams = waves / ways;
     for (int t = 1; t <= most; ++t) {
       const int per = t * teams;
