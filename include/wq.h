@@ -707,8 +707,9 @@ int wq_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int64_t n, int64
  *   y     fp32 and / or bf16 [m][y_stride], either may be NULL but not both
  * Sums are fp32.  A weight is its value as wq_dequantize_mxfp4 gives it.
  * 0 <= m <= 2^20, 0 <= n <= 2^24, k a multiple of 32, 32 .. 2^18; x, xq, q
- * 16-byte aligned, x_stride a multiple of 8; scale and x_scale 4-byte aligned
- * (their last 4-byte word is read whole); y overlaps nothing (WQ_ERR_SHAPE).
+ * 16-byte aligned, x_stride a multiple of 8 up to 2^22; scale and x_scale 4-byte
+ * aligned (their last 4-byte word is read whole); y overlaps nothing
+ * (WQ_ERR_SHAPE).
  * A prepare and a run, as for the calls of a verify pass; `workspace` as there.
  */
 typedef struct {

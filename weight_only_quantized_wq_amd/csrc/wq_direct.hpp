@@ -28,6 +28,9 @@ __device__ __forceinline__ void request16(const void* base, uint32_t off, uint32
 __device__ __forceinline__ void request4(const void* from, uint32_t to) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(to), "v"(from) : "memory");
 }
+__device__ __forceinline__ void request4(const void* base, uint32_t off, uint32_t to) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" ::"{m0}"(to), "v"(off), "s"(base) : "memory");
+}
 // With the five wait states that a base written by a vector instruction (a value read
 // off a lane) needs.
 __device__ __forceinline__ void request16_late(const void* base, uint32_t off, uint32_t to) {

@@ -17,6 +17,13 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int kMxGroup = 32;
 constexpr int64_t kMxMost = (int64_t)1 << 40;     // weights of one call
 
+// 16 bytes of codes as the matrix instructions' operand, whose other half they do not read.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i32x8 mx_operand(u32x4 v) {
+  const i32x4 q = __builtin_bit_cast(i32x4, v);
+  return __builtin_shufflevector(q, q, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+
 // A constant index for a generic lambda.
 template <int V>
 struct At {

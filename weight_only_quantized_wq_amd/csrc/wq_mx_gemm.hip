@@ -126,7 +126,11 @@ static int tile_launch(const char* name, MxTileArgs a, hipStream_t s) {
   a.tn = (a.n + T::BN - 1) / T::BN;
   a.tm = (a.m + T::BM - 1) / T::BM;
   const int per = (a.tn * a.tm + 7) / 8;
-  hipLaunchKernelGGL((mx_tile_kernel<XQ, TN, TM, WN, WM>), dim3((unsigned)(per * 8), 1), dim3(T::kWaves * 64), 0, s, a);
+  // a row ends inside a stage
+  if (a.x_bytes % 128)
+    hipLaunchKernelGGL((mx_tile_kernel<XQ, true, TN, TM, WN, WM>), dim3((unsigned)(per * 8)), dim3(T::kWaves * 64), 0, s, a);
+  else
+    hipLaunchKernelGGL((mx_tile_kernel<XQ, false, TN, TM, WN, WM>), dim3((unsigned)(per * 8)), dim3(T::kWaves * 64), 0, s, a);
   return launch_status(name);
 }
 
@@ -182,8 +186,9 @@ static int gemm_check(const char* name, const wq_gemm_mxfp4& a) {
     return fail(WQ_ERR_SHAPE, "%s: m = %lld (0..2^20), n = %lld (0..2^24), k = %lld (a multiple of 32 up to 2^18)", name,
                 (long long)a.m, (long long)a.n, (long long)a.k);
   const int64_t most = (int64_t)1 << 40;
-  if (a.x && (a.x_stride < a.k || a.x_stride > most || a.x_stride % 8))
-    return fail(WQ_ERR_SHAPE, "%s: x_stride = %lld must be a multiple of 8 and hold a row", name, (long long)a.x_stride);
+  // (offsets inside a tile of 256 rows are 32 bits)
+  if (a.x && (a.x_stride < a.k || a.x_stride > (1 << 22) || a.x_stride % 8))
+    return fail(WQ_ERR_SHAPE, "%s: x_stride = %lld must be a multiple of 8 up to 2^22 and hold a row", name, (long long)a.x_stride);
   if (a.y_stride < a.n || a.y_stride > most)
     return fail(WQ_ERR_SHAPE, "%s: y_stride = %lld must hold a row", name, (long long)a.y_stride);
   if (!aligned16(a.x) || !aligned16(a.xq) || !aligned16(a.q))
@@ -297,7 +302,7 @@ extern "C" int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream) {
       if (g.xq) t.xscale = pad(g.x_scale, g.m);
     }
     if (big_tiles(g.m, g.n, g.k, g.xq))
-      return g.xq ? tile_launch<true, 8, 4, 2, 4>(name, t, s) : tile_launch<false, 8, 4, 2, 4>(name, t, s);
+      return g.xq ? tile_launch<true, 8, 4, 2, 4>(name, t, s) : tile_launch<false, 4, 8, 4, 2>(name, t, s);
     t.part = reinterpret_cast<float*>(static_cast<char*>(plan->workspace) +
                                       (needs_pad(g.k) ? ((g.m + g.n) * t.sstride + 15) / 16 * 16 : 0));
     const SplitPlan p = split_plan(g.m, g.n, g.k, g.xq);

@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kSplitWaves * 64) void mx_split_kernel(MxTileArgs a
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const u32x4 v = *reinterpret_cast<const u32x4*>(x + (c + t * 16) * 128 + (((2 * g + h) ^ ((c >> 1) & 7)) << 4));
-          b[h][t] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+          b[h][t] = mx_operand(v);
         }
       }
 #pragma unroll
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kSplitWaves * 64) void mx_split_kernel(MxTileArgs a
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const u32x4 v = *reinterpret_cast<const u32x4*>(w + (c + r * 16) * 128 + (((2 * g + h) ^ ((c >> 1) & 7)) << 4));
-          q[h][r] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+          q[h][r] = mx_operand(v);
         }
       }
       wait_lds();

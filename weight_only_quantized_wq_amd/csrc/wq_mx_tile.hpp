@@ -9,12 +9,13 @@
 // MXFP4 activations (XQ): stages of 256 inputs and v_mfma_scale_f32_16x16x128_f8f6f4,
 // which takes codes and scale bytes as they are.  A lane's groups are 2 g and 2 g + 1.
 //
-// 128-byte rows lie XOR-permuted by pieces of 16 bytes, so that 16 rows read at one
-// piece meet no bank twice.  Scale rows are multiples of 8 bytes here (windows of 256
+// Scale rows are multiples of 8 bytes here (windows of 256
 // inputs); others are padded beforehand (mx_pad_kernel).
 #pragma once
 
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "wq_direct.hpp"
 #include "wq_mx.hpp"
@@ -73,9 +74,28 @@ struct TileShape {
                 kSXOps * kWaves * 256 == kSX);
 };
 
-template <bool XQ, int TN, int TM, int WN, int WM>
+// Where 16-byte piece `p` of row `r` stands among the eight of a 128-byte row in LDS: XOR
+// by a permutation of the row's number.  A ds_read_b128 is served 16 lanes at a time, of
+// which eight read piece p of rows {0-3, 12-15} and eight piece p ^ 2 of rows {4-11} of a
+// tile (or the other way round), so the permutation keeps those halves' pieces apart
+// (4 cycles a read; with r / 2 itself 8).
+__device__ __forceinline__ int tile_piece(int p, int r) {
+  const int q = (r >> 1) & 7;
+  return p ^ (((q ^ (q << 1)) & 4) | ((q >> 1) & 2) | (q & 1));
+}
+
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void for_parts(F step) {
+  if constexpr (I < N) {
+    step(At<I>{});
+    for_parts<N, I + 1>(step);
+  }
+}
+
+template <bool XQ, bool TAIL, int TN, int TM, int WN, int WM>
 __global__ __launch_bounds__(WN * WM * 64) void mx_tile_kernel(MxTileArgs a) {
   using T = TileShape<XQ, TN, TM, WN, WM>;
+  constexpr int S = T::kStages;
   __shared__ __align__(1024) char lds[T::kLds];
   const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
   // Workgroups go to the eight XCDs in turn: each XCD takes a contiguous range of tiles,
@@ -85,28 +105,28 @@ __global__ __launch_bounds__(WN * WM * 64) void mx_tile_kernel(MxTileArgs a) {
   if (((int)blockIdx.x >> 3) >= per || tile >= tiles) return;
   const int panel = tile / (8 * a.tn), rest = tile - panel * 8 * a.tn, high = min(8, a.tm - panel * 8);
   const int n0 = rest / high * T::BN, m0 = (panel * 8 + rest % high) * T::BM;
-  const int count = a.stages;
 
   char* const xs = lds;
-  char* const ws = lds + T::kStages * T::kX;
-  char* const sw = ws + T::kStages * T::kW;
+  char* const ws = lds + S * T::kX;
+  char* const sw = ws + S * T::kW;
   char* const sx = sw + 2 * T::kSW;
   const int rows_w = a.n - 1 - n0, rows_x = a.m - 1 - m0;        // last row of the tile that is there
 
-  // offsets of this wave's pieces, rows past the end as the last
-  uint32_t xo[T::kXOps], wo[T::kWOps], swo[T::kSWOps], sxo[T::kSXOps > 0 ? T::kSXOps : 1];
-  uint32_t xp[T::kXOps], wp[T::kWOps];
+  // where this wave's pieces come from: offsets to a scalar base that moves with the
+  // stage, rows past the end as the last
+  uint32_t xo[T::kXOps], xp[T::kXOps], wo[T::kWOps], wp[T::kWOps], swo[T::kSWOps], sxo[T::kSXOps > 0 ? T::kSXOps : 1];
 #pragma unroll
   for (int i = 0; i < T::kXOps; ++i) {
     const int r = (i * T::kWaves + wave) * 8 + (lane >> 3);
-    xp[i] = (uint32_t)((lane & 7) ^ ((r >> 1) & 7)) * 16u;
-    xo[i] = (uint32_t)(min(r, rows_x));
+    xp[i] = (uint32_t)tile_piece(lane & 7, r) * 16u;
+    xo[i] = (uint32_t)min(r, rows_x) * (uint32_t)a.x_stride + xp[i];
   }
 #pragma unroll
   for (int i = 0; i < T::kWOps; ++i) {
+    // of 32-byte rows the halves change places from eight rows to the next, for ds_read_b32
     const int r = XQ ? (i * T::kWaves + wave) * 8 + (lane >> 3) : (i * T::kWaves + wave) * 32 + (lane >> 1);
-    wp[i] = XQ ? (uint32_t)((lane & 7) ^ ((r >> 1) & 7)) * 16u : (uint32_t)(lane & 1) * 16u;
-    wo[i] = (uint32_t)min(r, rows_w) * a.w_bytes;
+    wp[i] = XQ ? (uint32_t)tile_piece(lane & 7, r) * 16u : (uint32_t)((lane ^ (r >> 3)) & 1) * 16u;
+    wo[i] = (uint32_t)min(r, rows_w) * a.w_bytes + wp[i];
   }
 #pragma unroll
   for (int i = 0; i < T::kSWOps; ++i)
@@ -119,23 +139,68 @@ __global__ __launch_bounds__(WN * WM * 64) void mx_tile_kernel(MxTileArgs a) {
   const uint8_t* const swbase = a.wscale + (int64_t)n0 * a.sstride;
   const uint8_t* const sxbase = XQ ? a.xscale + (int64_t)m0 * a.sstride : nullptr;
 
-  auto request = [&](int s) {
-    const int at = s % T::kStages, window = XQ ? s : s >> 2;
-    const uint32_t xk = (uint32_t)s * 128u, wk = (uint32_t)s * T::kWRow;
+  // Request `op` of stage s, to the buffer of stage `to`.  In a row's last stage pieces
+  // past its end read its first instead (what they meet is 0 or cleared).
+  auto request_op = [&](int s, int to, auto op) __attribute__((always_inline)) {
+    constexpr int o = decltype(op)::value;
+    const int at = to % S, window = XQ ? s : s >> 2;
+    if constexpr (o < T::kXOps) {
+      const uint32_t k = (uint32_t)s * 128u;
+      uint32_t off = xo[o];
+      if (TAIL && k + xp[o] >= a.x_bytes) off -= xp[o];
+      request16(xbase + k, off, lds_offset(xs + at * T::kX + (o * T::kWaves + wave) * 1024));
+    } else if constexpr (o < T::kXOps + T::kWOps) {
+      constexpr int i = o - T::kXOps;
+      const uint32_t k = (uint32_t)s * T::kWRow;
+      uint32_t off = wo[i];
+      if (TAIL && k + wp[i] >= a.w_bytes) off -= wp[i];
+      request16(wbase + k, off, lds_offset(ws + at * T::kW + (i * T::kWaves + wave) * 1024));
+    } else if constexpr (o < T::kXOps + T::kWOps + T::kSWOps) {
+      constexpr int i = o - T::kXOps - T::kWOps;
+      request4(swbase + window * 8, swo[i], lds_offset(sw + (window & 1) * T::kSW + (i * T::kWaves + wave) * 256));
+    } else {
+      constexpr int i = o - T::kXOps - T::kWOps - T::kSWOps;
+      request4(sxbase + window * 8, sxo[i], lds_offset(sx + (window & 1) * T::kSX + (i * T::kWaves + wave) * 256));
+    }
+  };
+  const int rn = wave / WM * TN * 16 + c, rm = wave % WM * TM * 16 + c;   // this lane's first rows in the tile
+  // A stage is multiplied in parts: half h of its inputs with TN / RS of the row tiles.
+  constexpr int RS = XQ ? 2 : 1, TR = TN / RS, kParts = 2 * RS;
+  u32x4 bx[2][TM];                                       // of the two halves
+  typename std::conditional<XQ, u32x4, uint32_t>::type bw[2][TR];   // of even and odd parts
+  uint32_t fw[TN], fx[XQ ? TM : 1];                      // scales, of a whole stage
+  auto read = [&](int s, auto part) __attribute__((always_inline)) {
+    constexpr int p = decltype(part)::value, h = p / RS, rs = p % RS;
+    const char* const x = xs + s % S * T::kX;
+    const char* const w = ws + s % S * T::kW;
+    const int at = tile_piece(2 * g + h, c) << 4;
+    if constexpr (rs == 0) {
 #pragma unroll
-    for (int i = 0; i < T::kXOps; ++i)
-      request16(xbase + xo[i] * a.x_stride + min(xk + xp[i], a.x_bytes - 16u),
-                lds_offset(xs + at * T::kX + (i * T::kWaves + wave) * 1024));
+      for (int t = 0; t < TM; ++t) bx[h][t] = *reinterpret_cast<const u32x4*>(x + (rm + t * 16) * 128 + at);
+    }
 #pragma unroll
-    for (int i = 0; i < T::kWOps; ++i)
-      request16_late(wbase, wo[i] + min(wk + wp[i], a.w_bytes - 16u),
-                     lds_offset(ws + at * T::kW + (i * T::kWaves + wave) * 1024));
+    for (int r = 0; r < TR; ++r) {
+      const int row = rn + (rs * TR + r) * 16;
+      if constexpr (XQ)
+        bw[p & 1][r] = *reinterpret_cast<const u32x4*>(w + row * 128 + at);
+      else
+        bw[p & 1][r] = *reinterpret_cast<const uint32_t*>(w + row * 32 + (((g >> 1) ^ (c >> 3)) & 1) * 16 + (g & 1) * 8 + h * 4);
+    }
+  };
+  auto read_scales = [&](int s) __attribute__((always_inline)) {
+    const int window = XQ ? s : s >> 2;
+    const char* const f = sw + (window & 1) * T::kSW;
 #pragma unroll
-    for (int i = 0; i < T::kSWOps; ++i)
-      request4_late(swbase + window * 8, swo[i], lds_offset(sw + (window & 1) * T::kSW + (i * T::kWaves + wave) * 256));
+    for (int r = 0; r < TN; ++r) {
+      if constexpr (XQ)
+        fw[r] = *reinterpret_cast<const uint16_t*>(f + (rn + r * 16) * 8 + 2 * g);
+      else
+        fw[r] = *reinterpret_cast<const uint8_t*>(f + (rn + r * 16) * 8 + (s & 3) * 2 + (g >> 1));
+    }
+    if constexpr (XQ) {
 #pragma unroll
-    for (int i = 0; i < T::kSXOps; ++i)
-      request4_late(sxbase + window * 8, sxo[i], lds_offset(sx + (window & 1) * T::kSX + (i * T::kWaves + wave) * 256));
+      for (int t = 0; t < TM; ++t) fx[t] = *reinterpret_cast<const uint16_t*>(sx + (s & 1) * T::kSX + (rm + t * 16) * 8 + 2 * g);
+    }
   };
 
   f32x4 acc[TN][TM];
@@ -143,74 +208,70 @@ __global__ __launch_bounds__(WN * WM * 64) void mx_tile_kernel(MxTileArgs a) {
   for (int r = 0; r < TN; ++r)
 #pragma unroll
     for (int t = 0; t < TM; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int rn = wave / WM * TN * 16 + c, rm = wave % WM * TM * 16 + c;   // this lane's first rows in the tile
-
-#pragma unroll
-  for (int i = 0; i < T::kStages - 1; ++i)
-    if (i < count) request(i);
-  for (int s = 0; s < count; ++s) {
-    const int at = s % T::kStages;
-    if (T::kStages > 2 && s + 1 < count)
-      wait_requests<(T::kStages - 2) * T::kOps>();
-    else
-      wait_requests<0>();
-    meet();
-    if (s + T::kStages - 1 < count) request(s + T::kStages - 1);
-    const char* const x = xs + at * T::kX;
-    const char* const w = ws + at * T::kW;
-    if constexpr (XQ) {
-      const char* const fw = sw + (s & 1) * T::kSW;
-      const char* const fx = sx + (s & 1) * T::kSX;
-      uint32_t ps[TM];
-#pragma unroll
-      for (int t = 0; t < TM; ++t) ps[t] = *reinterpret_cast<const uint16_t*>(fx + (rm + t * 16) * 8 + 2 * g);
-      auto step = [&](auto at) __attribute__((always_inline)) {
-        constexpr int ks = decltype(at)::value;
-        i32x8 b[TM];
-#pragma unroll
-        for (int t = 0; t < TM; ++t) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(x + (rm + t * 16) * 128 + (((2 * g + ks) ^ ((c >> 1) & 7)) << 4));
-          b[t] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int r = 0; r < TN; ++r) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(w + (rn + r * 16) * 128 + (((2 * g + ks) ^ ((c >> 1) & 7)) << 4));
-          const i32x8 q = {(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
-          const int sc = *reinterpret_cast<const uint16_t*>(fw + (rn + r * 16) * 8 + 2 * g);
-#pragma unroll
-          for (int t = 0; t < TM; ++t)
-            acc[r][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q, b[t], acc[r][t], 4, 4, ks, sc, ks, (int)ps[t]);
-        }
-      };
-      step(At<0>{});
-      step(At<1>{});
-    } else {
-      const uint8_t* const fw = reinterpret_cast<const uint8_t*>(sw + ((s >> 2) & 1) * T::kSW) + (s & 3) * 2 + (g >> 1);
-      u32x4 b[TM][2];
-#pragma unroll
-      for (int t = 0; t < TM; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          b[t][h] = *reinterpret_cast<const u32x4*>(x + (rm + t * 16) * 128 + (((2 * g + h) ^ ((c >> 1) & 7)) << 4));
-      if ((uint32_t)(s + 1) * 128u > a.x_bytes && g >= 2) {
-        // half a stage past the end: the scales are 0 there, the activations anything
-#pragma unroll
-        for (int t = 0; t < TM; ++t) b[t][0] = b[t][1] = u32x4{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int r = 0; r < TN; ++r) {
-        const uint64_t v = *reinterpret_cast<const uint64_t*>(w + (rn + r * 16) * 32 + g * 8);
-        const float sc = __uint_as_float((uint32_t)fw[(rn + r * 16) * 8] << 23);
-        const bf16x8 lo = mx_bf16((uint32_t)v, sc), hi = mx_bf16((uint32_t)(v >> 32), sc);
+  auto multiply = [&](auto part, auto then) __attribute__((always_inline)) {
+    constexpr int p = decltype(part)::value, h = p / RS, rs = p % RS;
+    for_parts<TR>([&](auto at) __attribute__((always_inline)) {
+      constexpr int r = decltype(at)::value, r0 = rs * TR;
+      if constexpr (XQ) {
+        const i32x8 q = mx_operand(bw[p & 1][r]);
 #pragma unroll
         for (int t = 0; t < TM; ++t)
-          acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, __builtin_bit_cast(bf16x8, b[t][0]), acc[r][t], 0, 0, 0);
+          acc[r0 + r][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q, mx_operand(bx[h][t]), acc[r0 + r][t], 4, 4, h, (int)fw[r0 + r], h, (int)fx[t]);
+      } else {
+        const bf16x8 q = mx_bf16(bw[p & 1][r], __uint_as_float(fw[r0 + r] << 23));
 #pragma unroll
         for (int t = 0; t < TM; ++t)
-          acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, __builtin_bit_cast(bf16x8, b[t][1]), acc[r][t], 0, 0, 0);
+          acc[r0 + r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q, __builtin_bit_cast(bf16x8, bx[h][t]), acc[r0 + r][t], 0, 0, 0);
       }
+      then(at);
+    });
+  };
+  auto nothing = [](auto) __attribute__((always_inline)) {};
+  // half a stage past the end: the scales are 0 there, bf16 activations anything
+  auto clear = [&](int s, auto half) __attribute__((always_inline)) {
+    if constexpr (TAIL && !XQ) {
+      const uint32_t keep = (uint32_t)(s + 1) * 128u > a.x_bytes && g >= 2 ? 0u : ~0u;
+#pragma unroll
+      for (int t = 0; t < TM; ++t) bx[decltype(half)::value][t] &= u32x4{keep, keep, keep, keep};
     }
+  };
+
+  // Operands of a part are read while the part before is multiplied.  The wait and the
+  // barrier stand before a stage's last part: the next stage has arrived then, and this
+  // one's buffer has been read by all.  The loop has no branch: past the end the last
+  // stage is requested again, to buffers that nobody reads any more (its scales over
+  // themselves), and what lies there is read but not multiplied.  (With branches the
+  // compiler moves the products behind them, and their operands to memory.)
+  const int count = a.stages;
+#pragma unroll
+  for (int i = 0; i < S; ++i) for_parts<T::kOps>([&](auto op) __attribute__((always_inline)) { request_op(min(i, count - 1), i, op); });
+  wait_requests<(S - 1) * T::kOps>();
+  meet();
+  read(0, At<0>{});
+  read_scales(0);
+  for (int s = 0; s < count; ++s) {
+    clear(s, At<0>{});
+    for_parts<kParts - 1>([&](auto part) __attribute__((always_inline)) {
+      read(s, At<decltype(part)::value + 1>{});
+      multiply(part, nothing);
+      __builtin_amdgcn_sched_barrier(0);          // no reads from further ahead: registers
+    });
+    wait_requests<(S - 2) * T::kOps>();
+    meet();
+    clear(s, At<1>{});
+    read(s + 1, At<0>{});
+    // the requests of a stage between the products, so that the matrix pipe does not wait
+    // for all waves to have made theirs
+    multiply(At<kParts - 1>{}, [&](auto at) __attribute__((always_inline)) {
+      constexpr int r = decltype(at)::value, from = r * T::kOps / TR, to = (r + 1) * T::kOps / TR;
+      for_parts<to - from>([&](auto op) __attribute__((always_inline)) {
+        request_op(min(s + S, count - 1), s, At<from + decltype(op)::value>{});
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    read_scales(min(s + 1, count - 1));
   }
+  wait_requests<0>();
 
   // lane: rows 4 g + i of W's 16, one activation row
 #pragma unroll

@@ -176,9 +176,7 @@ struct RowStream {
   template <int J>
   __device__ __forceinline__ static f32x4 multiply4(const Unit& u, const u32x4 (&x)[kFrags], uint32_t xs, f32x4 acc) {
     // both operands as they are: 16 bytes of codes, scale byte J of either word
-    const i32x8 a = {(int)u.w[J][0], (int)u.w[J][1], (int)u.w[J][2], (int)u.w[J][3], 0, 0, 0, 0};
-    const i32x8 b = {(int)x[J][0], (int)x[J][1], (int)x[J][2], (int)x[J][3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, J, (int)u.s, J, (int)xs);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(u.w[J]), mx_operand(x[J]), acc, 4, 4, J, (int)u.s, J, (int)xs);
   }
 
   __device__ __forceinline__ static f32x4 multiply(const Unit& u, const u32x4 (&x)[kFrags], uint32_t xs, f32x4 acc) {
