@@ -359,16 +359,33 @@ def wq_gemm_smallM_int8(x, m, q, scale, n, k, y_f32=None, y_bf16=None, stream=No
           _ptr(y_bf16, ok and 2 * m * n, "y_bf16"), _stream(stream))
 
 
-def wq_quantize_mxfp4(w_f32, w_bf16, n, k, q, scale, stream=None):
+def _mx_call(fn, name, stream, n, k, a, b, c, d):
+    """A call over [n][k] values with buffers (tensor, bytes, what) before and behind the sizes.  They are checked as in
+    _ptr, and the current stream is asked for as in _run (a call on a few rows is bound by these lines)."""
     ok = _nonneg(n, k)
-    _call("wq_quantize_mxfp4", _ptr(w_f32, ok and 4 * n * k, "w_f32"), _ptr(w_bf16, ok and 2 * n * k, "w_bf16"), n, k,
-          _ptr(q, ok and n * k // 2, "q"), _ptr(scale, ok and n * k // 32, "scale"), _stream(stream))
+    a, b, c, d = (None if t is None else _ptr(t, ok and size, what) for t, size, what in (a, b, c, d))
+    _refuse_host((a, b, c, d))
+    rc = fn(a, b, n, k, c, d, _raw_stream(_current_device()) if stream is None else _stream(stream))
+    if rc != 0:
+        raise WQError(name, rc, lib.wq_last_error().decode(errors="replace"))
+
+
+def _current_device():
+    global _current_device
+    import torch
+    torch.cuda.current_device()               # initialises the runtime where nothing has yet
+    _current_device = torch._C._cuda_getDevice
+    return _current_device()
+
+
+def wq_quantize_mxfp4(w_f32, w_bf16, n, k, q, scale, stream=None):
+    _mx_call(lib.wq_quantize_mxfp4, "wq_quantize_mxfp4", stream, n, k, (w_f32, 4 * n * k, "w_f32"),
+             (w_bf16, 2 * n * k, "w_bf16"), (q, n * k // 2, "q"), (scale, n * k // 32, "scale"))
 
 
 def wq_dequantize_mxfp4(q, scale, n, k, y_f32=None, y_bf16=None, stream=None):
-    ok = _nonneg(n, k)
-    _call("wq_dequantize_mxfp4", _ptr(q, ok and n * k // 2, "q"), _ptr(scale, ok and n * k // 32, "scale"), n, k,
-          _ptr(y_f32, ok and 4 * n * k, "y_f32"), _ptr(y_bf16, ok and 2 * n * k, "y_bf16"), _stream(stream))
+    _mx_call(lib.wq_dequantize_mxfp4, "wq_dequantize_mxfp4", stream, n, k, (q, n * k // 2, "q"),
+             (scale, n * k // 32, "scale"), (y_f32, 4 * n * k, "y_f32"), (y_bf16, 2 * n * k, "y_bf16"))
 
 
 def _moe_bytes(e, dim, f):

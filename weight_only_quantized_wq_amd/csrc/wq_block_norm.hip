@@ -99,31 +99,47 @@ struct Factor<float> {
   __device__ float operator()(float v) const { return ldexpf(v * m, e); }
 };
 
-__device__ __forceinline__ float turned(float g) { return 1.f / (1.f + expf(-g)); }
+// sigmoid of eight gates (bf16 values).
+__device__ __forceinline__ void turned(const float (&x)[8], float (&g)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] = 1.f / (1.f + expf(-x[j]));
+}
 // 1 / (1 + 2^(n + t)), |t| <= 1/2, with 2^t = sum (t ln 2)^i / i! up to i = 10 (the rest
 // is below 3e-13) and two Newton steps on the hardware's reciprocal: a third of the
-// instructions of exp and a division, and far finer than what is rounded to 4 bits
-// can tell.
-__device__ __forceinline__ double turned(double g) {
-  double x = g * -1.4426950408889634;
-  x = x > 1020. ? 1020. : x < -1020. ? -1020. : x;        // NaN stays
-  const double n = rint(x), t = x - n;
-  double p = 7.0549116208011233e-09;
-  p = fma(p, t, 1.0178086009239699e-07);
-  p = fma(p, t, 1.3215486790144309e-06);
-  p = fma(p, t, 1.5252733804059841e-05);
-  p = fma(p, t, 1.5403530393381609e-04);
-  p = fma(p, t, 1.3333558146428443e-03);
-  p = fma(p, t, 9.6181291076284772e-03);
-  p = fma(p, t, 5.5504108664821580e-02);
-  p = fma(p, t, 2.4022650695910072e-01);
-  p = fma(p, t, 6.9314718055994531e-01);
-  p = fma(p, t, 1.);
-  const double d = 1. + ldexp(p, (int)n);
-  double r = __builtin_amdgcn_rcp(d);
-  r = fma(fma(-d, r, 1.), r, r);
-  r = fma(fma(-d, r, 1.), r, r);
-  return g == -(double)INFINITY ? 0. : r;
+// instructions of exp and a division, and far finer than what is rounded to 4 bits can
+// tell.  Gates past 700, infinities and NaN take exp itself.
+__device__ __forceinline__ void turned(const float (&x)[8], double (&g)[8]) {
+  float most = 0.f;
+  bool fine = true;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    most = fmaxf(most, fabsf(x[j]));
+    fine = fine && x[j] == x[j];
+  }
+  if (__any(!(most <= 700.f && fine))) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = 1. / (1. + exp(-(double)x[j]));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const double y = (double)x[j] * -1.4426950408889634, n = rint(y), t = y - n;
+    double p = 7.054911620801121e-09;
+    p = fma(p, t, 1.0178086009239696e-07);
+    p = fma(p, t, 1.3215486790144305e-06);
+    p = fma(p, t, 1.5252733804059838e-05);
+    p = fma(p, t, 1.5403530393381606e-04);
+    p = fma(p, t, 1.3333558146428441e-03);
+    p = fma(p, t, 9.618129107628477e-03);
+    p = fma(p, t, 5.5504108664821576e-02);
+    p = fma(p, t, 2.402265069591007e-01);
+    p = fma(p, t, 6.931471805599453e-01);
+    p = fma(p, t, 1.);
+    const double d = 1. + ldexp(p, (int)n);
+    double r = __builtin_amdgcn_rcp(d);
+    r = fma(fma(-d, r, 1.), r, r);
+    g[j] = fma(fma(-d, r, 1.), r, r);
+  }
 }
 
 __device__ __forceinline__ void store_f32(float* to, const float (&v)[8]) {
@@ -147,6 +163,23 @@ __device__ __forceinline__ float to_odd(double v) {
   uint32_t b = __float_as_uint(f);
   if (d != v) b = (b - (fabs(d) > fabs(v) ? 1u : 0u)) | 1u;
   return __uint_as_float(b);
+}
+// The codes of eight fp64 values.  Rounding to fp32 first matters only where it lands on
+// a border between two codes, whose 20 last bits are 0; those few are rounded to odd.
+__device__ __forceinline__ uint32_t mx_codes(const double (&v)[8], uint32_t byte) {
+  float o[8];
+  uint32_t low = ~0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    o[j] = (float)v[j];
+    const uint32_t b = __float_as_uint(o[j]) & 0xFFFFFu;
+    low = low < b ? low : b;
+  }
+  if (__any(low == 0)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = to_odd(v[j]);
+  }
+  return mx_codes(o, byte);
 }
 // What the fp64 value is in bf16.
 __device__ __forceinline__ float narrow(double v, bool to_bf16) { return to_bf16 ? to_odd(v) : (float)v; }
@@ -221,11 +254,11 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(NormArgs a) {
         // the choice stands outside the loops, whose eight chains then overlap
         as_f32(gr[i], x);
         A g[8];
+        if (a.kind == WQ_GATE_PLAIN) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = (A)x[j];
-        if (a.kind != WQ_GATE_PLAIN) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = turned(g[j]);
+          for (int j = 0; j < 8; ++j) g[j] = (A)x[j];
+        } else {
+          turned(x, g);
           if (a.kind == WQ_GATE_SILU) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[j] *= (A)x[j];
@@ -283,9 +316,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(NormArgs a) {
       // 2^(floor(log2) - 2) as for the quantiser; past fp32's range as an infinity
       const int e = (int)(quad_max(top) >> 20) - 1023;
       const uint32_t byte = e > 127 ? 255u : e < -125 ? 0u : (uint32_t)(e + 125);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = to_odd(v[i][j]);
-      const uint32_t codes = mx_codes(o, byte);
+      const uint32_t codes = mx_codes(v[i], byte);
       const int64_t piece = (row * a.dim + at) / 8;
       gmem(reinterpret_cast<uint32_t*>(a.q))[piece] = codes;
       if ((piece & 3) == 0) gmem(a.q_scale)[piece >> 2] = (uint8_t)byte;
@@ -364,7 +395,7 @@ static void norm_launch(const NormArgs& a, int64_t rows, hipStream_t s) {
   else if (pieces <= 512)
     hipLaunchKernelGGL((block_norm_kernel<A, 2, 256>), grid, dim3(256), 0, s, a);
   else if (pieces <= 1024)
-    hipLaunchKernelGGL((block_norm_kernel<A, 4, 256>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((block_norm_kernel<A, 2, 512>), grid, dim3(512), 0, s, a);
   else if (pieces <= 2048)
     hipLaunchKernelGGL((block_norm_kernel<A, 4, 512>), grid, dim3(512), 0, s, a);
   else
