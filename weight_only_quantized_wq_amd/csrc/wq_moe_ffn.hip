@@ -237,7 +237,7 @@ __device__ __forceinline__ void find_tokens(const MoeArgs& a, MoeTokens& all) {
   } else {
     for (int t = wave_id(); t < a.tokens; t += WAVES)
       select_experts(
-          a, [&](int e) { return (double)a.logits[t * a.e + e]; },
+          a, [&](int e) { return a.logits ? (double)a.logits[t * a.e + e] : a.scores[t * a.e + e]; },
           [&](int j, int e, float g) {
             all.sel[t * a.top + j] = e;
             if (blockIdx.x == 0) put_selection(a, t, j, e, g);
@@ -316,8 +316,9 @@ __device__ __forceinline__ void bf16_parts(float v, int parts, uint16_t (&p)[3])
 
 constexpr int kUpTiles = 16;
 
-template <bool MX, bool ODD, int COLS, int WAVES, int P>
-__global__ __launch_bounds__(WAVES * 64) void moe_up_kernel(MoeArgs a) {
+// TWO: two workgroups share a CU, and with it its registers.
+template <bool MX, bool ODD, int COLS, int WAVES, int P, bool TWO>
+__global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_up_kernel(MoeArgs a) {
   using S = RowStream<MX, false, ODD, COLS, P>;
   constexpr int kRed = WAVES * kUpTiles * 1024, kAll = WAVES * S::kBytes;
   __shared__ __align__(1024) char lds[kAll > kRed ? kAll : kRed];
@@ -380,8 +381,8 @@ __global__ __launch_bounds__(WAVES * 64) void moe_up_kernel(MoeArgs a) {
 // ---------------------------------------------------------------------------
 // Second products, and the sum over a token's experts
 
-template <bool MX, bool ODD, int COLS, int WAVES, int P>
-__global__ __launch_bounds__(WAVES * 64) void moe_down_kernel(MoeArgs a) {
+template <bool MX, bool ODD, int COLS, int WAVES, int P, bool TWO>
+__global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_down_kernel(MoeArgs a) {
   using S = RowStream<MX, false, ODD, COLS, P>;
   constexpr int kRed = WAVES * kUpTiles * 1024, kAll = WAVES * S::kBytes;
   __shared__ __align__(1024) char lds[kAll > kRed ? kAll : kRed];
@@ -694,15 +695,16 @@ static int moe_overlap(const char* name, const wq_moe_ffn& a) {
   return WQ_OK;
 }
 
-// Row tiles of a workgroup (`each` at once, of `tiles` such) and waves per tile, for
-// `items` experts in use: the fewest units in the longest chain.
-static void rows_plan(MoeArgs& a, int waves, int items, int tiles, int each, int spans) {
+// Row tiles of a workgroup (`each` streams at once, of `tiles` such) and waves per tile,
+// for `items` experts in use: the fewest units in the longest chain of a CU, which holds
+// one workgroup of eight waves or two of four.
+static void rows_plan(MoeArgs& a, int waves, int items, int tiles, int each, int spans, int64_t slots) {
   double best = 1e300;
   for (int ways = 1; ways <= waves; ways *= 2) {
     const int teams = waves / ways;
     for (int t = 1; t <= kUpTiles / each; ++t) {
       const int per = t * teams, blocks = (tiles + per - 1) / per;
-      const int64_t rounds = ((int64_t)blocks * items + 255) / 256;
+      const int64_t rounds = ((int64_t)blocks * items + slots - 1) / slots;
       const double cost = (double)rounds * ((double)each * t * ((spans + ways - 1) / ways) + 2.0);
       if (cost < best) {
         best = cost;
@@ -714,34 +716,41 @@ static void rows_plan(MoeArgs& a, int waves, int items, int tiles, int each, int
   }
 }
 
-template <bool MX, int COLS, int WAVES, int P>
+template <bool MX, int COLS, int WAVES, int P, bool TWO = false>
 static void up_launch(MoeArgs a, hipStream_t s) {
   const int picks = a.tokens * a.top, used = std::min(a.e, picks);
   a.pairs = a.f / 16;
-  rows_plan(a, WAVES, used, a.pairs, 2, a.spans);
+  rows_plan(a, WAVES, used, a.pairs, 2, a.spans, TWO ? 512 : 256);
   const dim3 grid((unsigned)((used + picks / COLS) * a.blocks));
   if (MX && a.w13.srow % 4)
-    hipLaunchKernelGGL((moe_up_kernel<MX, MX, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
+    hipLaunchKernelGGL((moe_up_kernel<MX, MX, COLS, WAVES, P, TWO>), grid, dim3(WAVES * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((moe_up_kernel<MX, false, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
+    hipLaunchKernelGGL((moe_up_kernel<MX, false, COLS, WAVES, P, TWO>), grid, dim3(WAVES * 64), 0, s, a);
 }
 
-template <bool MX, int COLS, int WAVES, int P>
+template <bool MX, int COLS, int WAVES, int P, bool TWO = false>
 static void down_launch(MoeArgs a, hipStream_t s) {
   const int picks = a.tokens * a.top, used = std::min(a.e, picks);
-  rows_plan(a, WAVES, used, a.dim / 16, 1, a.spans2);
+  rows_plan(a, WAVES, used, a.dim / 16, 1, a.spans2, TWO ? 512 : 256);
   const dim3 grid((unsigned)((used + picks / (COLS / a.parts)) * a.blocks));
   if (MX && a.w2.srow % 4)
-    hipLaunchKernelGGL((moe_down_kernel<MX, MX, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
+    hipLaunchKernelGGL((moe_down_kernel<MX, MX, COLS, WAVES, P, TWO>), grid, dim3(WAVES * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((moe_down_kernel<MX, false, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
+    hipLaunchKernelGGL((moe_down_kernel<MX, false, COLS, WAVES, P, TWO>), grid, dim3(WAVES * 64), 0, s, a);
 }
 
 template <bool MX>
 static void experts_launch(MoeArgs a, hipStream_t s) {
   const int mean = (a.tokens * a.top + a.e - 1) / a.e;      // tokens of an expert
+  // Many experts of a few tokens each: two workgroups of four waves on a CU, whose starts
+  // (the search for an expert's tokens, the first loads) and ends lie beside the other's
+  // streams.  61 tokens of 128 experts: 104 us, with one of eight waves 119; but 16 tokens
+  // of Mixtral's eight 182 and 166, its int8 layer for one token 79 and 75.
+  const bool many = a.tokens > 8 && a.e >= 64 && mean <= 4;
   if (a.tokens <= 4)
     up_launch<MX, 4, 8, 3>(a, s);
+  else if (many)
+    up_launch<MX, 8, 4, 2, true>(a, s);
   else if (a.tokens <= 8 || 2 * mean <= 8)
     up_launch<MX, 8, 8, 2>(a, s);
   else
@@ -754,7 +763,9 @@ static void experts_launch(MoeArgs a, hipStream_t s) {
       hipLaunchKernelGGL((moe_few_kernel<MX, false, 4, 8, 2, 2>), dim3((unsigned)(a.dim / 16)), dim3(512), 0, s, a);
     return;
   }
-  if (a.tokens * a.parts <= 8 || 2 * mean * a.parts <= 8)
+  if (many)
+    down_launch<MX, 8, 4, 2, true>(a, s);
+  else if (a.tokens * a.parts <= 8 || 2 * mean * a.parts <= 8)
     down_launch<MX, 8, 8, 2>(a, s);
   else
     down_launch<MX, 16, 4, 4>(a, s);
@@ -830,16 +841,15 @@ extern "C" int wq_moe_ffn_run(const wq_moe_ffn_plan* plan, void* stream) {
   a.parts = m.y_f32 ? 3 : 2;
   a.spans = (int32_t)((up + 255) / 256);
   a.spans2 = (int32_t)((down + 255) / 256);
-  a.here = m.logits && m.tokens <= 8;
   hipStream_t s = (hipStream_t)stream;
-  if (m.router) {
-    // a workgroup reads up to 128 KB of router rows
-    const int shares = (int)std::min<int64_t>(m.e, (m.e * m.dim + kScoreMost - 1) / kScoreMost);
+  // a workgroup reads up to 128 KB of router rows; where it reads a token's all, it selects
+  const int shares = m.router ? (int)std::min<int64_t>(m.e, (m.e * m.dim + kScoreMost - 1) / kScoreMost) : 0;
+  if (m.router)
     hipLaunchKernelGGL(moe_score_kernel, dim3((unsigned)m.tokens, (unsigned)shares), dim3(kScoreWaves * 64), 0, s, a);
-    if (shares > 1) hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)m.tokens), dim3(64), 0, s, a);
-  } else if (!a.here) {
-    hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)m.tokens), dim3(64), 0, s, a);
-  }
+  // Otherwise every workgroup of the next launch selects for itself where that is one
+  // token a wave (8 tokens of 128 experts: 47.5 us, with a launch of its own 48.9).
+  a.here = shares != 1 && m.tokens <= 8;
+  if (shares != 1 && !a.here) hipLaunchKernelGGL(moe_route_kernel, dim3((unsigned)m.tokens), dim3(64), 0, s, a);
   if (mx)
     experts_launch<true>(a, s);
   else
