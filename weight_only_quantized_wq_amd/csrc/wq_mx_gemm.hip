@@ -134,42 +134,61 @@ static int tile_launch(const char* name, MxTileArgs a, hipStream_t s) {
   return launch_status(name);
 }
 
-// Tiles of mx_split_kernel: 128 rows of W (64 with 4-bit activations) x up to 64 of x.
-struct SplitPlan {
-  int tn, tm, tmt, splits, share;
+// How a product of many rows is cut, and about how long that takes: rounds of workgroups
+// over the 256 CUs times what a workgroup multiplies (rows of W x rows of x x stages), at
+// the rates measured on 28672 x 4096 and 4096 x 14336 with 16 .. 2000 rows of x.
+//   tiles of 256 x 256 (rows = 256)
+//   tiles of `rows` of W x 16 tmt of x over shares of k (mx_split_kernel): 64 rows by eight
+//   waves (six with 64 of x, as many as have rings in LDS), which few tiles need; 128 by
+//   four, a third faster for what it multiplies; with 4-bit activations, whose stages
+//   are longer, 64 by four
+// 47 rows x 4096 x 14336: 16.4 us in tiles of 64, 20.2 of 128; 384 rows 99 and 73; 128 rows
+// x 28672 x 4096 61 and 52, 512 rows 110 (128) and 100 (256).
+struct TilePlan {
+  int rows, tn, tm, tmt, splits, share;
+  double us;
 };
 static int stages_of(int64_t k, bool xq) { return (int)(xq ? (k + 255) / 256 : (k + 63) / 64); }
-static SplitPlan split_plan(int64_t m, int64_t n, int64_t k, bool xq) {
-  SplitPlan p;
-  p.tmt = m <= 32 ? 2 : 4;
-  p.tm = (int)((m + 16 * p.tmt - 1) / (16 * p.tmt));
-  const int bn = xq ? 64 : 128, stages = stages_of(k, xq);
-  p.tn = (int)((n + bn - 1) / bn);
+
+static TilePlan split_plan(int64_t m, int64_t n, int64_t k, bool xq, int rows) {
+  TilePlan p{};
+  auto tiles_of = [&](int t) { return (int)((m + 16 * t - 1) / (16 * t)); };
+  // the fewest rows of padding
+  p.rows = rows;
+  p.tmt = rows == 128 ? 4 : m <= 32 ? 2 : xq || tiles_of(4) * 4 <= tiles_of(3) * 3 ? 4 : 3;
+  p.tm = tiles_of(p.tmt);
+  p.tn = (int)((n + rows - 1) / rows);
   // about one workgroup per CU, each wave at least two stages
-  const int64_t tiles = (int64_t)p.tn * p.tm, most = std::max(1, stages / (2 * kSplitWaves));
-  const int64_t want = std::max<int64_t>(1, 256 / tiles);
-  const int splits = (int)std::min(want, most);
+  const int stages = stages_of(k, xq), waves = xq || rows == 128 ? 4 : p.tmt == 4 ? 6 : 8;
+  const int64_t tiles = (int64_t)p.tn * p.tm, most = std::max(1, stages / (2 * waves));
+  const int splits = (int)std::min(std::max<int64_t>(1, 256 / tiles), most);
   p.share = (stages + splits - 1) / splits;
   p.splits = (stages + p.share - 1) / p.share;
+  p.us = (double)((tiles * p.splits + 255) / 256) * p.share * rows * 16e-6 * p.tmt * (xq ? 130. : rows == 128 ? 38. : 53.);
+  // the second launch, and the sums written and read
+  if (p.splits > 1) p.us += 3.5 + (double)p.splits * m * n * 8 / 3e6;
   return p;
 }
-// Whether tiles of 256 x 256 are the faster: by rounds of workgroups over the 256 CUs, a
-// product in split tiles taking half as long again.
-static bool big_tiles(int64_t m, int64_t n, int64_t k, bool xq) {
-  const SplitPlan p = split_plan(m, n, k, xq);
-  const int64_t big = ((m + 255) / 256) * ((n + 255) / 256), small = (int64_t)p.tn * p.tm * p.splits;
-  const double part = (xq ? 64. : 128.) * 16 * p.tmt / (256. * 256.) / p.splits;
-  return (double)((big + 255) / 256) <= 1.5 * part * (double)((small + 255) / 256);
+
+static TilePlan tile_plan(int64_t m, int64_t n, int64_t k, bool xq) {
+  TilePlan best{256, (int)((n + 255) / 256), (int)((m + 255) / 256), 16, 1, stages_of(k, xq), 0.};
+  best.us = (double)(((int64_t)best.tn * best.tm + 255) / 256) * best.share * 65536e-6 * (xq ? 32.5 : 23.);
+  for (int rows : {64, 128}) {
+    if (xq && rows == 128) continue;
+    const TilePlan p = split_plan(m, n, k, xq, rows);
+    if (p.us < best.us) best = p;
+  }
+  return best;
 }
 
-template <bool XQ, int TN, int TM, int P>
-static int split_launch(const char* name, MxTileArgs a, const SplitPlan& p, hipStream_t s) {
+template <bool XQ, int TN, int TM, int P, int WAVES>
+static int split_launch(const char* name, MxTileArgs a, const TilePlan& p, hipStream_t s) {
   a.tn = p.tn;
   a.tm = p.tm;
   a.share = p.share;
   if (p.splits == 1) a.part = nullptr;
-  hipLaunchKernelGGL((mx_split_kernel<XQ, TN, TM, P>), dim3((unsigned)(p.tn * p.tm), (unsigned)p.splits), dim3(kSplitWaves * 64), 0,
-                     s, a);
+  hipLaunchKernelGGL((mx_split_kernel<XQ, TN, TM, P, WAVES>), dim3((unsigned)(p.tn * p.tm), (unsigned)p.splits), dim3(WAVES * 64), 0, s,
+                     a);
   if (p.splits > 1) {
     const int64_t quads = (int64_t)a.m * ((a.n + 3) / 4);
     hipLaunchKernelGGL(mx_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, a, p.splits);
@@ -221,12 +240,9 @@ extern "C" int64_t wq_gemm_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k
   if (m <= kRowsMost) return bytes;
   // padded scales, then shares of k (of either kind of activations)
   if (needs_pad(k)) bytes += ((m + n) * pad_stride(k) + 15) / 16 * 16;
-  {
-    int most = 1;
-    for (bool xq : {false, true})
-      if (!big_tiles(m, n, k, xq)) most = std::max(most, split_plan(m, n, k, xq).splits);
-    if (most > 1) bytes += (int64_t)most * m * ((n + 3) / 4 * 4) * 4;
-  }
+  int64_t most = 1;
+  for (bool xq : {false, true}) most = std::max<int64_t>(most, tile_plan(m, n, k, xq).splits);
+  if (most > 1) bytes += most * m * ((n + 3) / 4 * 4) * 4;
   return bytes;
 }
 
@@ -301,13 +317,14 @@ extern "C" int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream) {
       t.wscale = pad(g.scale, g.n);
       if (g.xq) t.xscale = pad(g.x_scale, g.m);
     }
-    if (big_tiles(g.m, g.n, g.k, g.xq))
-      return g.xq ? tile_launch<true, 8, 4, 2, 4>(name, t, s) : tile_launch<false, 4, 8, 4, 2>(name, t, s);
+    const TilePlan p = tile_plan(g.m, g.n, g.k, g.xq);
+    if (p.rows == 256) return g.xq ? tile_launch<true, 8, 4, 2, 4>(name, t, s) : tile_launch<false, 4, 8, 4, 2>(name, t, s);
     t.part = reinterpret_cast<float*>(static_cast<char*>(plan->workspace) +
                                       (needs_pad(g.k) ? ((g.m + g.n) * t.sstride + 15) / 16 * 16 : 0));
-    const SplitPlan p = split_plan(g.m, g.n, g.k, g.xq);
-    if (g.xq) return p.tmt == 2 ? split_launch<true, 4, 2, 2>(name, t, p, s) : split_launch<true, 4, 4, 2>(name, t, p, s);
-    return p.tmt == 2 ? split_launch<false, 8, 2, 4>(name, t, p, s) : split_launch<false, 8, 4, 3>(name, t, p, s);
+    if (g.xq) return p.tmt == 2 ? split_launch<true, 4, 2, 2, 4>(name, t, p, s) : split_launch<true, 4, 4, 2, 4>(name, t, p, s);
+    if (p.rows == 128) return split_launch<false, 8, 4, 3, 4>(name, t, p, s);
+    if (p.tmt == 2) return split_launch<false, 4, 2, 3, 8>(name, t, p, s);
+    return p.tmt == 3 ? split_launch<false, 4, 3, 2, 8>(name, t, p, s) : split_launch<false, 4, 4, 2, 6>(name, t, p, s);
   }
   if (g.xq) return rows_launch<true, 16, 8, 3>(name, a, s);
   if (g.m <= 4) return rows_launch<false, 4, 8, 3>(name, a, s);

@@ -14,9 +14,7 @@
 
 namespace wq {
 
-constexpr int kSplitWaves = 4;
-
-template <bool XQ, int TN, int TM, int P>
+template <bool XQ, int TN, int TM, int P, int WAVES>
 struct SplitShape {
   static constexpr int BN = TN * 16, BM = TM * 16;
   static constexpr int kWRow = XQ ? 128 : 32;
@@ -27,14 +25,14 @@ struct SplitShape {
   static constexpr int kSlot = kX + kW + kSW + kSX;
   static constexpr int kXOps = kX / 1024, kWOps = kW / 1024, kSWOps = kSW / 256, kSXOps = kSX / 256;
   static constexpr int kOps = kXOps + kWOps + kSWOps + kSXOps;
-  static constexpr int kRing = kSplitWaves * P * kSlot, kSums = kSplitWaves * BN * BM * 4;
+  static constexpr int kRing = WAVES * P * kSlot, kSums = WAVES * BN * BM * 4;
   static constexpr int kLds = kRing > kSums ? kRing : kSums;
   static_assert(kXOps * 1024 == kX && kWOps * 1024 == kW && kSWOps * 256 == kSW && kSXOps * 256 == kSX && (P - 1) * kOps < 64);
 };
 
-template <bool XQ, int TN, int TM, int P>
-__global__ __launch_bounds__(kSplitWaves * 64) void mx_split_kernel(MxTileArgs a) {
-  using T = SplitShape<XQ, TN, TM, P>;
+template <bool XQ, int TN, int TM, int P, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void mx_split_kernel(MxTileArgs a) {
+  using T = SplitShape<XQ, TN, TM, P, WAVES>;
   __shared__ __align__(1024) char lds[T::kLds];
   const int lane = lane_id(), wave = wave_id(), g = lane >> 4, c = lane & 15;
   // the m tiles of one n tile and share next to each other
@@ -83,12 +81,12 @@ __global__ __launch_bounds__(kSplitWaves * 64) void mx_split_kernel(MxTileArgs a
 #pragma unroll
     for (int t = 0; t < TM; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int first = s0 + wave, count = first < s1 ? (s1 - first + kSplitWaves - 1) / kSplitWaves : 0;
+  const int first = s0 + wave, count = first < s1 ? (s1 - first + WAVES - 1) / WAVES : 0;
 #pragma unroll
   for (int p = 0; p < P; ++p)
-    if (p < count) request(first + p * kSplitWaves, p);
+    if (p < count) request(first + p * WAVES, p);
   for (int i = 0; i < count; ++i) {
-    const int s = first + i * kSplitWaves;
+    const int s = first + i * WAVES;
     if (count - i >= P)
       wait_requests<(P - 1) * T::kOps>();
     else if (P > 2 && count - i == 2)
@@ -121,7 +119,7 @@ __global__ __launch_bounds__(kSplitWaves * 64) void mx_split_kernel(MxTileArgs a
         }
       }
       wait_lds();
-      if (i + P < count) request(s + P * kSplitWaves, i % P);
+      if (i + P < count) request(s + P * WAVES, i % P);
 #pragma unroll
       for (int r = 0; r < TN; ++r)
 #pragma unroll
@@ -144,7 +142,7 @@ __global__ __launch_bounds__(kSplitWaves * 64) void mx_split_kernel(MxTileArgs a
         sc[r] = *reinterpret_cast<const uint8_t*>(w + T::kW + (c + r * 16) * 4 + (s & 1) * 2 + (g >> 1));
       }
       wait_lds();
-      if (i + P < count) request(s + P * kSplitWaves, i % P);
+      if (i + P < count) request(s + P * WAVES, i % P);
       if ((uint32_t)(s + 1) * 128u > a.x_bytes && g >= 2) {
         // half a stage past the end: the scales are 0 there, the activations anything
 #pragma unroll
@@ -170,13 +168,13 @@ __global__ __launch_bounds__(kSplitWaves * 64) void mx_split_kernel(MxTileArgs a
 #pragma unroll
     for (int t = 0; t < TM; ++t) *reinterpret_cast<f32x4*>(lds + ((wave * TN + r) * TM + t) * 1024 + lane * 16) = acc[r][t];
   __syncthreads();
-  for (int o = (int)threadIdx.x; o < T::BN / 4 * T::BM; o += kSplitWaves * 64) {
+  for (int o = (int)threadIdx.x; o < T::BN / 4 * T::BM; o += WAVES * 64) {
     const int quad = o % (T::BN / 4), row = o / (T::BN / 4);          // rows 4 quad .. of W, row `row` of x
     if (m0 + row >= a.m) break;
     const char* from = lds + ((quad >> 2) * TM + (row >> 4)) * 1024 + ((quad & 3) * 16 + (row & 15)) * 16;
     f32x4 v = *reinterpret_cast<const f32x4*>(from);
 #pragma unroll
-    for (int w = 1; w < kSplitWaves; ++w) v += *reinterpret_cast<const f32x4*>(from + w * TN * TM * 1024);
+    for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const f32x4*>(from + w * TN * TM * 1024);
     const int col = n0 + 4 * quad;
     if (a.part) {
       // rows of shares are multiples of 4 long
