@@ -191,7 +191,8 @@ def _product(wq, rng, m, n, k, xkind, out, pad=0):
 SHAPES = [(1, 1, 32), (1, 16, 64), (1, 17, 96), (2, 33, 128), (3, 100, 160), (4, 256, 512), (5, 129, 544), (8, 64, 1024),
           (7, 515, 1056), (9, 48, 2080), (15, 31, 512), (16, 1000, 4096), (1, 4100, 4096), (17, 70, 1504), (33, 130, 2048),
           (63, 257, 608), (64, 128, 8192), (65, 96, 160), (129, 515, 1056), (200, 300, 2560), (257, 260, 96), (515, 129, 640),
-          (300, 260, 4096), (2051, 5600, 96), (1030, 12010, 64), (4100, 2900, 672)]
+          (300, 260, 4096), (2051, 5600, 96), (1030, 12010, 64), (4100, 2900, 672),
+          (2051, 5600, 512), (600, 20000, 1024), (500, 4000, 512), (500, 4000, 544)]
 
 
 @pytest.mark.parametrize("xkind", ["bf16", "mxfp4"])
@@ -434,3 +435,270 @@ def test_an_infinity_or_nan_stays_in_its_row_and_group(wq):
     assert bad[1, 40] and bad.sum() == 1
     assert torch.isnan(u[1]).all() and torch.isfinite(u[[0, 2]]).all()
     assert (s[1] == 255).all() and (q[1] == 0).all() and (s[[0, 2]] != 255).all()
+
+
+# --- what must not reach other rows ----------------------------------------
+
+
+@pytest.mark.parametrize("xkind", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("m,n,k", [(4, 40, 96), (16, 40, 544), (40, 140, 1056), (2050, 5500, 96)])
+def test_infinities_and_nan_stay_in_their_rows_and_columns(wq, m, n, k, xkind):
+    """Rows of x with NaN and infinities between rows without (rows that end inside a stage read on past their end), rows
+    of W with a NaN group."""
+    import torch
+    rng = np.random.default_rng(m + k)
+    q, s = mx(rng, n, k)
+    s[1::7, -1] = 255
+    if xkind == "bf16":
+        x, xt = bf16(rng.normal(0, 1, (m, k)))
+        xt[1::2] = float("nan")
+        xt[2::4, 0] = float("inf")
+        xs, bad = None, np.isnan(f64(xt)).any(1) | np.isinf(f64(xt)).any(1)
+    else:
+        xq, xsc = mx(rng, m, k, spread=2)
+        xsc[1::2, 0] = 255
+        x, xt, xs = block.mx_values(xq, xsc), up(xq), up(xsc)
+        bad = np.isnan(x).any(1)
+    y = empty(m, n, fill=5)
+    wq.wq_gemm_mxfp4_run(wq.wq_gemm_mxfp4_prepare(xt, up(q), up(s), y, x_scale=xs))
+    got = f64(y)
+    gone = (s == 255).any(1)
+    assert np.isnan(got[:, gone]).all()
+    fine = ~bad[:, None] & ~gone[None]
+    w = block.mx_values(q, np.where(s == 255, 127, s))
+    x = np.where(np.isfinite(x) & ~bad[:, None], x, 0)
+    size = np.abs(x) @ np.abs(w).T
+    within(np.where(fine, got, 0), np.where(fine, x @ w.T, 0), (k + 16) * 2.0 ** -23 * size, "rows beside")
+    assert not np.isfinite(got[bad]).any()
+
+
+def test_a_token_of_nan_leaves_the_others_alone(wq):
+    rng = np.random.default_rng(8)
+    w13, t13 = _experts(rng, 4, 2 * 64, 96, "mxfp4")
+    w2, t2 = _experts(rng, 4, 96, 64, "mxfp4")
+    x, xt = bf16(rng.normal(0, 1, (12, 96)))
+    logits, lt = f32(rng.normal(0, 1, (12, 4)))
+    xt[5] = float("nan")
+    y = empty(12, 96)
+    wq.wq_moe_ffn_run(wq.wq_moe_ffn_prepare(xt, *t13, *t2, y, logits=lt))
+    x[5] = 0
+    want, sel, gates = block.moe_ffn(x, logits, w13, w2, 2)
+    got = f64(y)
+    assert np.isnan(got[5]).all()
+    got[5] = want[5] = 0
+    within(got, want, _moe_allowed(x, w13, w2, sel, gates, want, 3, "f32"), "others")
+
+
+def test_an_infinite_activation_between_the_products_is_no_nan_by_its_parts(wq):
+    import torch
+    w13 = torch.zeros(1, 64, 32, dtype=torch.int8, device="cuda")
+    w13[0, :, 0] = 127
+    s13 = torch.full((1, 64), 2.0 ** 100, dtype=torch.bfloat16, device="cuda")
+    w2, s2 = torch.ones(1, 32, 32, dtype=torch.int8, device="cuda"), torch.ones(1, 32, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(2, 32, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = torch.tensor([1.0, -1.0])
+    y = empty(2, 32)
+    wq.wq_moe_ffn_run(wq.wq_moe_ffn_prepare(x, w13, s13, w2, s2, y, logits=torch.zeros(2, 1, device="cuda"), top=1))
+    # silu(2^107) * 2^107 is infinite; silu(-2^107) is -0
+    assert (y[0] == float("inf")).all() and (y[1] == 0).all()
+
+
+# --- far offsets, streams, graphs, shared workspaces -----------------------
+
+
+def test_offsets_past_32_bits(wq):
+    """Weights of 4.6 GB: their last rows, for one row of x and for many; the quantiser over 4.4 billion values."""
+    import torch
+    n, k = 280000, 32768
+    q = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device="cuda")
+    s = torch.randint(125, 130, (n, k // 32), dtype=torch.uint8, device="cuda")
+    for m in (1, 20):
+        x, xt = bf16(np.random.default_rng(m).normal(0, 1, (m, k)))
+        y = empty(m, n)
+        wq.wq_gemm_mxfp4_run(wq.wq_gemm_mxfp4_prepare(xt, q, s, y))
+        for rows in (slice(0, 40), slice(131060, 131090), slice(n - 40, n)):
+            w = block.mx_values(q[rows].cpu().numpy(), s[rows].cpu().numpy())
+            within(f64(y[:, rows]), x @ w.T, (k + 16) * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T), f"rows {rows}")
+        del y
+    del q, s
+    n, k = 69000, 65536
+    w = torch.ones(n, k, dtype=torch.bfloat16, device="cuda")
+    w[-1] = torch.arange(k, device="cuda").remainder(8).to(torch.bfloat16)
+    q, s = empty(n, k // 2, dtype="uint8", fill=9), empty(n, k // 32, dtype="uint8", fill=9)
+    wq.wq_quantize_mxfp4(None, w, n, k, q, s)
+    want_q, want_s = block.mx_quantize(f64(w[-1:, :64]))
+    assert np.array_equal(q[-1, :32].cpu().numpy(), want_q[0]) and np.array_equal(s[-1, -2:].cpu().numpy(), want_s[0])
+    assert (q[:-1] == 0x66).all() and (s[:-1] == 125).all()
+    wq.wq_dequantize_mxfp4(q, s, n, k, None, w)
+    assert (w[:-1] == 1).all() and float(w[-1, -3]) == 4.0
+
+
+def _layer_state(wq, seed, tokens=6, dim=256, f=192, e=8):
+    """A block's buffers and plans: norm -> experts -> norm around them, into 4 bits -> product."""
+    import torch
+    rng = np.random.default_rng(seed)
+    v = {}
+    v["h"], h = f32(rng.normal(0, 2, (tokens, dim)))
+    v["norm"], norm = bf16(rng.normal(1, 0.1, dim))
+    v["post"], post = bf16(rng.normal(1, 0.1, dim))
+    v["next"], nxt = bf16(rng.normal(1, 0.1, dim))
+    v["router"], router = bf16(rng.normal(0, 0.1, (e, dim)))
+    v["w13"], t13 = _experts(rng, e, 2 * f, dim, "mxfp4")
+    v["w2"], t2 = _experts(rng, e, dim, f, "mxfp4")
+    wf, wt = f32(rng.normal(0, 0.05, (320, dim)))
+    q, s = empty(320, dim // 2, dtype="uint8"), empty(320, dim // 32, dtype="uint8")
+    wq.wq_quantize_mxfp4(wt, None, 320, dim, q, s)
+    v["w"] = block.mx_values(*block.mx_quantize(wf))
+    b = dict(h=h, u=empty(tokens, dim, dtype="bfloat16"), f=empty(tokens, dim), out=empty(tokens, dim),
+             uq=empty(tokens, dim // 2, dtype="uint8"), us=empty(tokens, dim // 32, dtype="uint8"), y=empty(tokens, 320))
+    ws = torch.empty(max(wq.wq_moe_ffn_workspace_bytes(tokens, dim, f, e, 2), wq.wq_gemm_mxfp4_workspace_bytes(tokens, 320, dim)),
+                     dtype=torch.uint8, device="cuda")
+    plans = [
+        (wq.wq_block_norm_run, wq.wq_block_norm_prepare(h, norm=norm, u=b["u"])),
+        (wq.wq_moe_ffn_run, wq.wq_moe_ffn_prepare(b["u"], *t13, *t2, b["f"], router=router, workspace=ws)),
+        (wq.wq_block_norm_run, wq.wq_block_norm_prepare(h, h_out=b["out"], f=b["f"], f_norm=post, scale=0.5, norm=nxt, q=b["uq"],
+                                                        q_scale=b["us"])),
+        (wq.wq_gemm_mxfp4_run, wq.wq_gemm_mxfp4_prepare(b["uq"], q, s, b["y"], x_scale=b["us"], workspace=ws)),
+    ]
+    return v, b, plans
+
+
+def _check_layer(v, b):
+    """Each step against the definition on what the step before it gave."""
+    _, u = block.block_norm(v["h"], norm=v["norm"], eps=float(np.float32(1e-6)))
+    within(f64(b["u"]), u, 2.0 ** -17 * np.abs(u) + BF16 * np.abs(u), "u")
+    u = f64(b["u"])
+    want, sel, gates = block.moe_ffn(u, u @ v["router"].T, v["w13"], v["w2"], 2)
+    within(f64(b["f"]), want, _moe_allowed(u, v["w13"], v["w2"], sel, gates, want, 3, "f32"), "experts")
+    out, nxt = block.block_norm(v["h"], f64(b["f"]), v["post"], scale=0.5, norm=v["next"], eps=float(np.float32(1e-6)))
+    within(f64(b["out"]), out, 2.0 ** -24 * np.abs(out), "out")
+    q, s = block.mx_quantize(nxt)
+    assert np.array_equal(b["uq"].cpu().numpy(), q) and np.array_equal(b["us"].cpu().numpy(), s)
+    x = block.mx_values(q, s)
+    within(f64(b["y"]), x @ v["w"].T, (x.shape[1] + 16) * 2.0 ** -23 * (np.abs(x) @ np.abs(v["w"]).T), "y")
+
+
+@pytest.mark.parametrize("tokens", [1, 6, 30])
+def test_a_block_of_a_decoder(wq, tokens):
+    v, b, plans = _layer_state(wq, tokens, tokens=tokens)
+    for run, plan in plans:
+        run(plan)
+    _check_layer(v, b)
+
+
+@pytest.mark.parametrize("tokens", [1, 6, 30])
+def test_a_block_captured_and_replayed_over_other_contents(wq, tokens):
+    import torch
+    v, b, plans = _layer_state(wq, 50 + tokens, tokens=tokens)
+    for run, plan in plans:
+        run(plan)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for run, plan in plans:
+            run(plan)
+    for seed in range(3):
+        v["h"], h = f32(np.random.default_rng(100 + seed).normal(0, 2, v["h"].shape))
+        b["h"].copy_(h)
+        for name in ("u", "f", "out", "uq", "us", "y"):
+            b[name].fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        _check_layer(v, b)
+        got = {name: t.clone() for name, t in b.items()}
+        for run, plan in plans:
+            run(plan)
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[name], t) for name, t in b.items()), "a replay differs from the calls"
+
+
+def test_two_blocks_on_two_streams_and_one_workspace_per_stream(wq):
+    import torch
+    states = [_layer_state(wq, 70 + i, tokens=20) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in states]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (_, _, plans), stream in zip(states, streams):
+            for run, plan in plans:
+                run(plan, stream)
+    torch.cuda.synchronize()
+    for v, b, _ in states:
+        _check_layer(v, b)
+
+
+def test_split_products_share_a_workspace_on_one_stream(wq):
+    """Shares of k meet in the workspace: two products in turn through one, and a capture of both."""
+    import torch
+    rng = np.random.default_rng(9)
+    k, m = 4096, 40
+    ws = torch.empty(wq.wq_gemm_mxfp4_workspace_bytes(m, 300, k), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 4 * m * 300                                  # there are shares
+    plans, outs, wants = [], [], []
+    for _ in range(2):
+        q, s = mx(rng, 300, k)
+        x, xt = bf16(rng.normal(0, 1, (m, k)))
+        y = empty(m, 300)
+        plans.append(wq.wq_gemm_mxfp4_prepare(xt, up(q), up(s), y, workspace=ws))
+        w = block.mx_values(q, s)
+        outs.append(y)
+        wants.append((x @ w.T, (k + 16) * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)))
+    for _ in range(2):
+        for p in plans:
+            wq.wq_gemm_mxfp4_run(p)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for p in plans:
+            wq.wq_gemm_mxfp4_run(p)
+    for _ in range(3):
+        for y in outs:
+            y.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for y, (want, allowed) in zip(outs, wants):
+            within(f64(y), want, allowed, "y")
+
+
+def test_empty_calls_touch_nothing(wq):
+    import torch
+    q, s = up(np.zeros((40, 32), np.uint8)), up(np.zeros((40, 2), np.uint8))
+    x, y = torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda"), empty(3, 40, fill=5)
+    wq.wq_gemm_mxfp4_run(wq.wq_gemm_mxfp4_prepare(x[:0], q, s, y[:0]))
+    wq.wq_gemm_mxfp4_run(wq.wq_gemm_mxfp4_prepare(x, q[:0], s[:0], y[:, :0]))
+    wq.wq_quantize_mxfp4(None, x, 0, 64, q, s)
+    w13, w2 = torch.zeros(4, 64, 64, dtype=torch.int8, device="cuda"), torch.zeros(4, 64, 32, dtype=torch.int8, device="cuda")
+    s13, s2 = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    out = empty(3, 64, fill=5)
+    wq.wq_moe_ffn_run(wq.wq_moe_ffn_prepare(x[:0], w13, s13, w2, s2, out[:0], logits=torch.zeros(0, 4, device="cuda")))
+    torch.cuda.synchronize()
+    assert (y == 5).all() and (out == 5).all()
+
+
+def test_gates_past_what_an_exponential_holds(wq):
+    """Gates of thousands, infinities and NaN, with results in bf16 and in 4 bits."""
+    import torch
+    rng = np.random.default_rng(11)
+    f = rng.normal(0, 1, (1, 128))
+    fv, ft = bf16(f)
+    hv, ht = f32(rng.normal(0, 1, (1, 128)))
+    g = rng.normal(0, 2, (1, 128))
+    g[0, :8] = [1e4, -1e4, 800, -800, 88.8, -88.8, 3e38, -3e38]
+    gv, gt = bf16(g)
+    for kind in ("sigmoid", "silu"):
+        with np.errstate(over="ignore"):
+            want, u = block.block_norm(hv, fv, None, gv, kind, 1.0, None, float(np.float32(1e-6)))
+        out, q, s = empty(1, 128), empty(1, 64, dtype="uint8"), empty(1, 4, dtype="uint8")
+        for plan in (wq.wq_block_norm_prepare(ht, h_out=out, f=ft, gate=gt, gate_kind=kind),
+                     wq.wq_block_norm_prepare(ht, h_out=out, f=ft, gate=gt, gate_kind=kind, q=q, q_scale=s)):
+            wq.wq_block_norm_run(plan)
+            got = f64(out)
+            fine = np.abs(want) < 3e38
+            within(np.where(fine, got, 0), np.where(fine, want, 0),
+                   2.0 ** -19 * (np.abs(hv) + np.abs(np.where(fine, want, 0) - hv)), kind)
+        if kind == "sigmoid":
+            assert np.array_equal(q.cpu().numpy(), block.mx_quantize(u)[0])
+    gt[0, 9] = float("nan")
+    wq.wq_block_norm_run(wq.wq_block_norm_prepare(ht, h_out=out, f=ft, gate=gt, gate_kind="sigmoid", q=q, q_scale=s))
+    assert torch.isnan(out[0, 9]) and torch.isfinite(out[0, 10:]).all() and (s == 255).all()
+    gt[0, 9], gt[0, 10] = float("-inf"), float("inf")
+    wq.wq_block_norm_run(wq.wq_block_norm_prepare(ht, h_out=out, f=ft, gate=gt, gate_kind="sigmoid", q=q, q_scale=s))
+    within(f64(out[0, 9:11]), hv[0, 9:11] + np.array([0.0, fv[0, 10]]), 2.0 ** -20, "infinite gates")
