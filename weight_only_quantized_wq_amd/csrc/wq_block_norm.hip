@@ -36,6 +36,7 @@ struct NormArgs {
   uint8_t* q;
   uint8_t* q_scale;
   int32_t dim;
+  int32_t rows;
   float scale;
   float eps;
   int32_t kind;
@@ -96,7 +97,9 @@ struct Factor<float> {
       e = 0;
     }
   }
-  __device__ float operator()(float v) const { return ldexpf(v * m, e); }
+  // the power first, which is exact: the product of a number below 2^-126 would be rounded
+  // (rows are divided by their own size, so nothing overflows)
+  __device__ float operator()(float v) const { return ldexpf(v, e) * m; }
 };
 
 // sigmoid of eight gates (bf16 values).
@@ -202,7 +205,8 @@ __device__ __forceinline__ double group_sum(double v, double (&part)[THREADS / 6
 template <class A, int CPT, int THREADS>
 __global__ __launch_bounds__(THREADS) void block_norm_kernel(NormArgs a) {
   __shared__ double part[2][THREADS / 64];
-  const int64_t row = blockIdx.x;
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= a.rows) return;
   const int tid = (int)threadIdx.x;
   const bool has_f = a.f32 || a.f16;
   Raw8 fr[CPT], hr[CPT];
@@ -328,7 +332,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(NormArgs a) {
 // Host side
 
 constexpr int64_t kNormMade = 0x77715f6e6f726d31;
-constexpr int64_t kNormMaxRows = 1 << 24, kNormMaxDim = 32768;
+constexpr int64_t kNormMaxRows = 1 << 24, kNormMaxDim = 32768, kNormGridX = 1 << 20;
 
 static int norm_check(const char* name, const wq_block_norm& a) {
   if (!a.h_f32 == !a.h_bf16) return fail(WQ_ERR_NULL, "%s: exactly one of h_f32 and h_bf16 must be given", name);
@@ -387,7 +391,9 @@ static int norm_overlap(const char* name, const wq_block_norm& a) {
 template <class A>
 static void norm_launch(const NormArgs& a, int64_t rows, hipStream_t s) {
   const int pieces = a.dim / 8;
-  const dim3 grid((unsigned)rows);
+  // a grid's axis holds less than 2^32 threads
+  const int64_t wide = rows < kNormGridX ? rows : kNormGridX;
+  const dim3 grid((unsigned)wide, (unsigned)((rows + wide - 1) / wide));
   if (pieces <= 64)
     hipLaunchKernelGGL((block_norm_kernel<A, 1, 64>), grid, dim3(64), 0, s, a);
   else if (pieces <= 256)
@@ -430,7 +436,7 @@ extern "C" int wq_block_norm_run(const wq_block_norm_plan* plan, void* stream) {
   if (n.rows == 0) return WQ_OK;
   const NormArgs a{n.h_f32,     n.h_bf16, n.h_stride,    n.out_f32, n.out_bf16, n.out_stride, n.f_f32, n.f_bf16,
                    n.f_stride,  n.f_norm, n.gate,        n.gate_stride, n.norm, n.u,          n.u_stride, n.q,
-                   n.q_scale,   (int32_t)n.dim, n.scale, n.eps,     n.gate_kind};
+                   n.q_scale,   (int32_t)n.dim, (int32_t)n.rows, n.scale, n.eps,     n.gate_kind};
   hipStream_t s = (hipStream_t)stream;
   if (n.q)
     norm_launch<double>(a, n.rows, s);
