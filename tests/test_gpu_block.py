@@ -702,3 +702,95 @@ def test_gates_past_what_an_exponential_holds(wq):
     gt[0, 9], gt[0, 10] = float("-inf"), float("inf")
     wq.wq_block_norm_run(wq.wq_block_norm_prepare(ht, h_out=out, f=ft, gate=gt, gate_kind="sigmoid", q=q, q_scale=s))
     within(f64(out[0, 9:11]), hv[0, 9:11] + np.array([0.0, fv[0, 10]]), 2.0 ** -20, "infinite gates")
+
+
+def test_a_buffer_of_another_device_is_refused(wq):
+    import torch
+
+    class Elsewhere:
+        """A tensor that says it is on the next device."""
+
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
+            return self.t.get_device() + 1
+
+    w, q, s = torch.zeros(2, 32, device="cuda"), empty(2, 16, dtype="uint8", fill=9), empty(2, 1, dtype="uint8", fill=9)
+    for call in (lambda: wq.wq_quantize_mxfp4(Elsewhere(w), None, 2, 32, q, s),
+                 lambda: wq.wq_quantize_mxfp4(w, None, 2, 32, q, Elsewhere(s), stream=torch.cuda.Stream()),
+                 lambda: wq.wq_dequantize_mxfp4(Elsewhere(q), s, 2, 32, w)):
+        with pytest.raises(ValueError, match="device"):
+            call()
+    torch.cuda.synchronize()
+    assert (q == 9).all() and (s == 9).all() and (w == 0).all()
+
+
+@pytest.mark.parametrize("post", [False, True])
+def test_norms_of_rows_below_the_normal_range(wq, post):
+    """Rows of a few units of 2^-149 without eps: results in bf16 are those of the formula, like any other row's."""
+    import torch
+    rng = np.random.default_rng(12)
+    v = rng.integers(-511, 512, (3, 264)) * 2.0 ** -149
+    xv, xt = f32(v)
+    assert np.array_equal(xv, v)
+    u = empty(3, 264, dtype="bfloat16")
+    if post:
+        # h' = 0 + norm(f), then as it is
+        one = torch.ones(264, dtype=torch.bfloat16, device="cuda")
+        plan = wq.wq_block_norm_prepare(torch.zeros(3, 264, device="cuda"), h_out=empty(3, 264), f=xt, f_norm=one, u=u, eps=0.0)
+    else:
+        plan = wq.wq_block_norm_prepare(xt, u=u, eps=0.0)
+    wq.wq_block_norm_run(plan)
+    want = v / np.sqrt((v * v).mean(1, keepdims=True))
+    # a factor good to 2^-24 and a product each (twice with `post`), then bf16
+    within(f64(u), want, (BF16 + 2.0 ** -20) * np.abs(want), "u")
+
+
+def test_norms_of_as_many_rows_as_documented(wq):
+    """2^24 rows of 520, more threads than one axis of a grid holds."""
+    import torch
+    rows, dim = 1 << 24, 520
+    rng = np.random.default_rng(13)
+    at = [0, 1, (1 << 20) - 1, 1 << 20, (1 << 23) + 5, rows - 2, rows - 1]
+    h = torch.ones(rows, dim, dtype=torch.bfloat16, device="cuda")
+    hv, ht = bf16(rng.normal(0, 3, (len(at), dim)))
+    h[at] = ht
+    u = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    wq.wq_block_norm_run(wq.wq_block_norm_prepare(h, u=u, eps=0.0))
+    _, want = block.block_norm(hv, eps=0.0)
+    within(f64(u[at]), want, (BF16 + 2.0 ** -18) * np.abs(want), "u")
+    u[at] = 1
+    # a row of ones stays one; by maximum and minimum, chunk by chunk
+    for part in u.view(-1).split(1 << 30):
+        assert float(part.max()) == 1 and float(part.min()) == 1
+
+
+@pytest.mark.parametrize("xkind", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("m,n,k", [(3, 70, 96), (16, 40, 544), (40, 140, 1056), (2050, 5500, 96)])
+def test_products_of_scales_far_apart(wq, m, n, k, xkind):
+    """Rows of W and of x from the smallest scales to the largest: a result is its own sum, not cut by either's range.
+    Sums that end below 2^-126 may lose what is below it."""
+    import torch
+    rng = np.random.default_rng(m)
+    q, s = mx(rng, n, k)
+    s[:] = rng.choice(np.array([0, 1, 30, 90, 127, 160, 220, 250], np.uint8), (n, 1))
+    w = block.mx_values(q, s)
+    if xkind == "bf16":
+        x, xt = bf16(rng.normal(0, 1, (m, k)) * 2.0 ** rng.choice([-120, -60, 0, 60, 119], (m, 1)))
+        xs = None
+    else:
+        xq, xsc = mx(rng, m, k)
+        xsc[:] = rng.choice(np.array([0, 2, 60, 127, 200, 246], np.uint8), (m, 1))
+        x, xt, xs = block.mx_values(xq, xsc), up(xq), up(xsc)
+    y = empty(m, n)
+    wq.wq_gemm_mxfp4_run(wq.wq_gemm_mxfp4_prepare(xt, up(q), up(s), y, x_scale=xs))
+    want, size = x @ w.T, np.abs(x) @ np.abs(w).T
+    fine = size < 2.0 ** 127
+    got = f64(y)
+    within(np.where(fine, got, 0), np.where(fine, want, 0),
+           np.where(fine, (k + 16) * 2.0 ** -23 * size + k * 2.0 ** -126, 0), "far scales")
+    assert (np.abs(want[fine]) > 2.0 ** -100).any() and (np.abs(want[fine]) < 2.0 ** -120).any()

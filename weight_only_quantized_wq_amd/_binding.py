@@ -363,9 +363,14 @@ def _mx_call(fn, name, stream, n, k, a, b, c, d):
     """A call over [n][k] values with buffers (tensor, bytes, what) before and behind the sizes.  They are checked as in
     _ptr, and the current stream is asked for as in _run (a call on a few rows is bound by these lines)."""
     ok = _nonneg(n, k)
+    tensors = [t[0] for t in (a, b, c, d) if t is not None and hasattr(t[0], "get_device")]
     a, b, c, d = (None if t is None else _ptr(t, ok and size, what) for t, size, what in (a, b, c, d))
     _refuse_host((a, b, c, d))
-    rc = fn(a, b, n, k, c, d, _raw_stream(_current_device()) if stream is None else _stream(stream))
+    device = _current_device() if tensors or stream is None else None
+    for t in tensors:
+        if t.get_device() != device:
+            raise ValueError(f"libwq: a buffer is on device {t.get_device()}, the current one is {device}")
+    rc = fn(a, b, n, k, c, d, _raw_stream(device) if stream is None else _stream(stream))
     if rc != 0:
         raise WQError(name, rc, lib.wq_last_error().decode(errors="replace"))
 
