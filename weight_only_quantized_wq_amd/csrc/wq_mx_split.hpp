@@ -52,13 +52,13 @@ __global__ __launch_bounds__(WAVES * 64) void mx_split_kernel(MxTileArgs a) {
 #pragma unroll
     for (int i = 0; i < T::kXOps; ++i) {
       const int r = i * 8 + (lane >> 3);
-      const uint32_t p = (uint32_t)((lane & 7) ^ ((r >> 1) & 7)) * 16u;
+      const uint32_t p = (uint32_t)tile_piece(lane & 7, r) * 16u;
       request16(xbase + min(r, rows_x) * a.x_stride + min(xk + p, a.x_bytes - 16u), lds_offset(to + i * 1024));
     }
 #pragma unroll
     for (int i = 0; i < T::kWOps; ++i) {
       const int r = XQ ? i * 8 + (lane >> 3) : i * 32 + (lane >> 1);
-      const uint32_t p = XQ ? (uint32_t)((lane & 7) ^ ((r >> 1) & 7)) * 16u : (uint32_t)(lane & 1) * 16u;
+      const uint32_t p = XQ ? (uint32_t)tile_piece(lane & 7, r) * 16u : (uint32_t)((lane ^ (r >> 3)) & 1) * 16u;
       request16_late(wbase, (uint32_t)min(r, rows_w) * a.w_bytes + min(wk + p, a.w_bytes - 16u), lds_offset(to + T::kX + i * 1024));
     }
     constexpr int words = T::kScale / 4;
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_split_kernel(MxTileArgs a) {
         px[t] = *reinterpret_cast<const uint16_t*>(fx + (c + t * 16) * 8 + 2 * g);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(x + (c + t * 16) * 128 + (((2 * g + h) ^ ((c >> 1) & 7)) << 4));
+          const u32x4 v = *reinterpret_cast<const u32x4*>(x + (c + t * 16) * 128 + (tile_piece(2 * g + h, c) << 4));
           b[h][t] = mx_operand(v);
         }
       }
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_split_kernel(MxTileArgs a) {
         pw[r] = *reinterpret_cast<const uint16_t*>(fw + (c + r * 16) * 8 + 2 * g);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(w + (c + r * 16) * 128 + (((2 * g + h) ^ ((c >> 1) & 7)) << 4));
+          const u32x4 v = *reinterpret_cast<const u32x4*>(w + (c + r * 16) * 128 + (tile_piece(2 * g + h, c) << 4));
           q[h][r] = mx_operand(v);
         }
       }
@@ -135,10 +135,10 @@ __global__ __launch_bounds__(WAVES * 64) void mx_split_kernel(MxTileArgs a) {
       for (int t = 0; t < TM; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          b[t][h] = *reinterpret_cast<const u32x4*>(x + (c + t * 16) * 128 + (((2 * g + h) ^ ((c >> 1) & 7)) << 4));
+          b[t][h] = *reinterpret_cast<const u32x4*>(x + (c + t * 16) * 128 + (tile_piece(2 * g + h, c) << 4));
 #pragma unroll
       for (int r = 0; r < TN; ++r) {
-        q[r] = *reinterpret_cast<const uint64_t*>(w + (c + r * 16) * 32 + g * 8);
+        q[r] = *reinterpret_cast<const uint64_t*>(w + (c + r * 16) * 32 + (((g >> 1) ^ (c >> 3)) & 1) * 16 + (g & 1) * 8);
         sc[r] = *reinterpret_cast<const uint8_t*>(w + T::kW + (c + r * 16) * 4 + (s & 1) * 2 + (g >> 1));
       }
       wait_lds();
