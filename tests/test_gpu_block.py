@@ -192,7 +192,9 @@ SHAPES = [(1, 1, 32), (1, 16, 64), (1, 17, 96), (2, 33, 128), (3, 100, 160), (4,
           (7, 515, 1056), (9, 48, 2080), (15, 31, 512), (16, 1000, 4096), (1, 4100, 4096), (17, 70, 1504), (33, 130, 2048),
           (63, 257, 608), (64, 128, 8192), (65, 96, 160), (129, 515, 1056), (200, 300, 2560), (257, 260, 96), (515, 129, 640),
           (300, 260, 4096), (2051, 5600, 96), (1030, 12010, 64), (4100, 2900, 672),
-          (2051, 5600, 512), (600, 20000, 1024), (500, 4000, 512), (500, 4000, 544)]
+          (2051, 5600, 512), (600, 20000, 1024), (500, 4000, 512), (500, 4000, 544),
+          # tiles of 256 x 128, and large tiles over shares of k, with rows that end inside a stage and without
+          (770, 5140, 1056), (1300, 1540, 2080), (1800, 1030, 4096), (770, 5140, 4128), (1800, 515, 8224), (770, 4100, 4096)]
 
 
 @pytest.mark.parametrize("xkind", ["bf16", "mxfp4"])
@@ -441,7 +443,8 @@ def test_an_infinity_or_nan_stays_in_its_row_and_group(wq):
 
 
 @pytest.mark.parametrize("xkind", ["bf16", "mxfp4"])
-@pytest.mark.parametrize("m,n,k", [(4, 40, 96), (16, 40, 544), (40, 140, 1056), (2050, 5500, 96)])
+@pytest.mark.parametrize("m,n,k", [(4, 40, 96), (16, 40, 544), (40, 140, 1056), (2050, 5500, 96), (1300, 1540, 2080),
+                                   (1800, 515, 8224)])
 def test_infinities_and_nan_stay_in_their_rows_and_columns(wq, m, n, k, xkind):
     """Rows of x with NaN and infinities between rows without (rows that end inside a stage read on past their end), rows
     of W with a NaN group."""
@@ -626,18 +629,18 @@ def test_two_blocks_on_two_streams_and_one_workspace_per_stream(wq):
         _check_layer(v, b)
 
 
-def test_split_products_share_a_workspace_on_one_stream(wq):
+@pytest.mark.parametrize("m,n,k", [(40, 300, 4096), (1300, 1540, 2080)])
+def test_split_products_share_a_workspace_on_one_stream(wq, m, n, k):
     """Shares of k meet in the workspace: two products in turn through one, and a capture of both."""
     import torch
     rng = np.random.default_rng(9)
-    k, m = 4096, 40
-    ws = torch.empty(wq.wq_gemm_mxfp4_workspace_bytes(m, 300, k), dtype=torch.uint8, device="cuda")
-    assert ws.numel() > 4 * m * 300                                  # there are shares
+    ws = torch.empty(wq.wq_gemm_mxfp4_workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 4 * m * n                                    # there are shares
     plans, outs, wants = [], [], []
     for _ in range(2):
-        q, s = mx(rng, 300, k)
+        q, s = mx(rng, n, k)
         x, xt = bf16(rng.normal(0, 1, (m, k)))
-        y = empty(m, 300)
+        y = empty(m, n)
         plans.append(wq.wq_gemm_mxfp4_prepare(xt, up(q), up(s), y, workspace=ws))
         w = block.mx_values(q, s)
         outs.append(y)

@@ -120,75 +120,109 @@ static bool needs_pad(int64_t k) { return k / kMxGroup % 8 != 0; }
 
 constexpr int64_t kRowsMost = 16;                // rows of x that mx_rows_kernel takes
 
-template <bool XQ, int TN, int TM, int WN, int WM>
-static int tile_launch(const char* name, MxTileArgs a, hipStream_t s) {
-  using T = TileShape<XQ, TN, TM, WN, WM>;
-  a.tn = (a.n + T::BN - 1) / T::BN;
-  a.tm = (a.m + T::BM - 1) / T::BM;
-  const int per = (a.tn * a.tm + 7) / 8;
-  // a row ends inside a stage
-  if (a.x_bytes % 128)
-    hipLaunchKernelGGL((mx_tile_kernel<XQ, true, TN, TM, WN, WM>), dim3((unsigned)(per * 8)), dim3(T::kWaves * 64), 0, s, a);
-  else
-    hipLaunchKernelGGL((mx_tile_kernel<XQ, false, TN, TM, WN, WM>), dim3((unsigned)(per * 8)), dim3(T::kWaves * 64), 0, s, a);
-  return launch_status(name);
-}
 
-// How a product of many rows is cut, and about how long that takes: rounds of workgroups
-// over the 256 CUs times what a workgroup multiplies (rows of W x rows of x x stages), at
-// the rates measured on 28672 x 4096 and 4096 x 14336 with 16 .. 2000 rows of x.
-//   tiles of 256 x 256 (rows = 256)
-//   tiles of `rows` of W x 16 tmt of x over shares of k (mx_split_kernel): 64 rows by eight
-//   waves (six with 64 of x, as many as have rings in LDS), which few tiles need; 128 by
-//   four, a third faster for what it multiplies; with 4-bit activations, whose stages
-//   are longer, 64 by four
-// 47 rows x 4096 x 14336: 16.4 us in tiles of 64, 20.2 of 128; 384 rows 99 and 73; 128 rows
-// x 28672 x 4096 61 and 52, 512 rows 110 (128) and 100 (256).
+// How a product of many rows is cut: tiles of `rows` of W x 16 tmt of x over `splits`
+// shares of k.
 struct TilePlan {
   int rows, tn, tm, tmt, splits, share;
   double us;
 };
 static int stages_of(int64_t k, bool xq) { return (int)(xq ? (k + 255) / 256 : (k + 63) / 64); }
 
-static TilePlan split_plan(int64_t m, int64_t n, int64_t k, bool xq, int rows) {
+// A kind of tile: what a workgroup pays for a stage of 16 x 16 of it and for its start and
+// end, in us (from the times of one to seven rounds over 4096 x 14336, 4096 x 4096 and
+// 28672 x 4096), and the fewest stages of a share.
+struct TileKind {
+  int rows, tmt;
+  double rate, start;
+  int least;
+};
+
+static void try_kind(TilePlan& best, int64_t m, int64_t n, int64_t k, bool xq, const TileKind& t) {
   TilePlan p{};
-  auto tiles_of = [&](int t) { return (int)((m + 16 * t - 1) / (16 * t)); };
-  // the fewest rows of padding
-  p.rows = rows;
-  p.tmt = rows == 128 ? 4 : m <= 32 ? 2 : xq || tiles_of(4) * 4 <= tiles_of(3) * 3 ? 4 : 3;
-  p.tm = tiles_of(p.tmt);
-  p.tn = (int)((n + rows - 1) / rows);
-  // about one workgroup per CU, each wave at least two stages
-  const int stages = stages_of(k, xq), waves = xq || rows == 128 ? 4 : p.tmt == 4 ? 6 : 8;
-  const int64_t tiles = (int64_t)p.tn * p.tm, most = std::max(1, stages / (2 * waves));
-  const int splits = (int)std::min(std::max<int64_t>(1, 256 / tiles), most);
-  p.share = (stages + splits - 1) / splits;
-  p.splits = (stages + p.share - 1) / p.share;
-  p.us = (double)((tiles * p.splits + 255) / 256) * p.share * rows * 16e-6 * p.tmt * (xq ? 130. : rows == 128 ? 38. : 53.);
-  // the second launch, and the sums written and read
-  if (p.splits > 1) p.us += 3.5 + (double)p.splits * m * n * 8 / 3e6;
-  return p;
+  p.rows = t.rows;
+  p.tmt = t.tmt;
+  p.tn = (int)((n + t.rows - 1) / t.rows);
+  p.tm = (int)((m + 16 * t.tmt - 1) / (16 * t.tmt));
+  const int stages = stages_of(k, xq);
+  const int64_t tiles = (int64_t)p.tn * p.tm;
+  for (int splits = 1; splits == 1 || (splits <= 16 && splits * t.least <= stages && tiles * (splits - 1) < 256); ++splits) {
+    p.share = (stages + splits - 1) / splits;
+    p.splits = (stages + p.share - 1) / p.share;
+    // rounds over the 256 CUs; shares cost a second launch, which reads what they write
+    const double rounds = (double)((tiles * p.splits + 255) / 256);
+    p.us = rounds * (p.share * t.rate * (t.rows / 16 * t.tmt) * 1e-3 + t.start) + (p.splits > 1 ? 3.5 + (double)p.splits * m * n * 8 / 5.3e6 : 0.);
+    if (p.us < best.us) best = p;
+  }
 }
 
+// The plan of the shortest estimate.  What each kind is for (us, the others in brackets):
+//   256 x 256 fills the chip: 4096 rows x 4096 x 14336 346 (256 x 128 401), and half of it
+//     with two shares of k: 2048 rows 198 (without shares 287)
+//   256 x 128 (bf16): 500 rows x 4096 x 14336 over four shares 67 (128 x 64 83)
+//   128 x 64 (bf16) by four waves: 256 rows x 4096 x 4096 17.5 (256 x 128 28)
+//   64 x 32, 48, 64 (mx_split_kernel by as many waves as have rings in LDS) where few
+//     tiles must fill the chip: 47 rows x 4096 x 14336 16.4 (128 x 64 20.2)
 static TilePlan tile_plan(int64_t m, int64_t n, int64_t k, bool xq) {
-  TilePlan best{256, (int)((n + 255) / 256), (int)((m + 255) / 256), 16, 1, stages_of(k, xq), 0.};
-  best.us = (double)(((int64_t)best.tn * best.tm + 255) / 256) * best.share * 65536e-6 * (xq ? 32.5 : 23.);
-  for (int rows : {64, 128}) {
-    if (xq && rows == 128) continue;
-    const TilePlan p = split_plan(m, n, k, xq, rows);
-    if (p.us < best.us) best = p;
+  TilePlan best{};
+  best.us = 1e300;
+  auto tiles_of = [&](int t) { return (int)((m + 16 * t - 1) / (16 * t)); };
+  if (xq) {
+    try_kind(best, m, n, k, xq, {256, 16, 7.2, 5., 6});
+    try_kind(best, m, n, k, xq, {64, m <= 32 ? 2 : 4, 29., 1.5, 8});
+  } else {
+    try_kind(best, m, n, k, xq, {256, 16, 5.9, 6.5, 8});
+    try_kind(best, m, n, k, xq, {256, 8, 6.8, 5., 8});
+    try_kind(best, m, n, k, xq, {128, 4, 11.2, 2., 8});
+    // the fewest rows of padding
+    const int tmt = m <= 32 ? 2 : tiles_of(4) * 4 <= tiles_of(3) * 3 ? 4 : 3;
+    try_kind(best, m, n, k, xq, {64, tmt, 13.6, 2., tmt == 4 ? 12 : 16});
   }
   return best;
 }
 
+template <bool XQ, int TN, int TM, int WN, int WM>
+static void tile_launch(const MxTileArgs& a, const TilePlan& p, hipStream_t s) {
+  const dim3 grid((unsigned)((a.tn * a.tm + 7) / 8 * 8), (unsigned)p.splits), block(WN * WM * 64);
+  // a row ends inside a stage
+  if (a.x_bytes % 128)
+    hipLaunchKernelGGL((mx_tile_kernel<XQ, true, TN, TM, WN, WM>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((mx_tile_kernel<XQ, false, TN, TM, WN, WM>), grid, block, 0, s, a);
+}
+
 template <bool XQ, int TN, int TM, int P, int WAVES>
-static int split_launch(const char* name, MxTileArgs a, const TilePlan& p, hipStream_t s) {
+static void split_launch(const MxTileArgs& a, const TilePlan& p, hipStream_t s) {
+  hipLaunchKernelGGL((mx_split_kernel<XQ, TN, TM, P, WAVES>), dim3((unsigned)(a.tn * a.tm), (unsigned)p.splits), dim3(WAVES * 64), 0, s,
+                     a);
+}
+
+static int tiles_launch(const char* name, MxTileArgs a, const TilePlan& p, bool xq, hipStream_t s) {
   a.tn = p.tn;
   a.tm = p.tm;
   a.share = p.share;
   if (p.splits == 1) a.part = nullptr;
-  hipLaunchKernelGGL((mx_split_kernel<XQ, TN, TM, P, WAVES>), dim3((unsigned)(p.tn * p.tm), (unsigned)p.splits), dim3(WAVES * 64), 0, s,
-                     a);
+  if (p.rows == 256) {
+    if (xq)
+      tile_launch<true, 8, 4, 2, 4>(a, p, s);
+    else if (p.tmt == 8)
+      tile_launch<false, 4, 4, 4, 2>(a, p, s);
+    else
+      tile_launch<false, 4, 8, 4, 2>(a, p, s);
+  } else if (xq) {
+    if (p.tmt == 2)
+      split_launch<true, 4, 2, 2, 4>(a, p, s);
+    else
+      split_launch<true, 4, 4, 2, 4>(a, p, s);
+  } else if (p.rows == 128) {
+    split_launch<false, 8, 4, 3, 4>(a, p, s);
+  } else if (p.tmt == 2) {
+    split_launch<false, 4, 2, 3, 8>(a, p, s);
+  } else if (p.tmt == 3) {
+    split_launch<false, 4, 3, 2, 8>(a, p, s);
+  } else {
+    split_launch<false, 4, 4, 2, 6>(a, p, s);
+  }
   if (p.splits > 1) {
     const int64_t quads = (int64_t)a.m * ((a.n + 3) / 4);
     hipLaunchKernelGGL(mx_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, a, p.splits);
@@ -318,13 +352,9 @@ extern "C" int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream) {
       if (g.xq) t.xscale = pad(g.x_scale, g.m);
     }
     const TilePlan p = tile_plan(g.m, g.n, g.k, g.xq);
-    if (p.rows == 256) return g.xq ? tile_launch<true, 8, 4, 2, 4>(name, t, s) : tile_launch<false, 4, 8, 4, 2>(name, t, s);
     t.part = reinterpret_cast<float*>(static_cast<char*>(plan->workspace) +
                                       (needs_pad(g.k) ? ((g.m + g.n) * t.sstride + 15) / 16 * 16 : 0));
-    if (g.xq) return p.tmt == 2 ? split_launch<true, 4, 2, 2, 4>(name, t, p, s) : split_launch<true, 4, 4, 2, 4>(name, t, p, s);
-    if (p.rows == 128) return split_launch<false, 8, 4, 3, 4>(name, t, p, s);
-    if (p.tmt == 2) return split_launch<false, 4, 2, 3, 8>(name, t, p, s);
-    return p.tmt == 3 ? split_launch<false, 4, 3, 2, 8>(name, t, p, s) : split_launch<false, 4, 4, 2, 6>(name, t, p, s);
+    return tiles_launch(name, t, p, g.xq, s);
   }
   if (g.xq) return rows_launch<true, 16, 8, 3>(name, a, s);
   if (g.m <= 4) return rows_launch<false, 4, 8, 3>(name, a, s);

@@ -176,13 +176,10 @@ __global__ __launch_bounds__(WAVES * 64) void mx_split_kernel(MxTileArgs a) {
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const f32x4*>(from + w * TN * TM * 1024);
     const int col = n0 + 4 * quad;
-    if (a.part) {
-      // rows of shares are multiples of 4 long
-      const int64_t width = (a.n + 3) / 4 * 4;
-      if (col < a.n) *gmem(reinterpret_cast<f32x4*>(a.part + ((int64_t)blockIdx.y * a.m + m0 + row) * width + col)) = v;
-    } else {
+    if (a.part)
+      store_part(a, m0 + row, col, v);
+    else
       store_quad(a, m0 + row, col, v);
-    }
   }
 }
 

@@ -34,7 +34,7 @@ struct MxTileArgs {
   float* part;              // [shares][m][n] sums of shares of k, or null
   int32_t m, n;
   uint32_t w_bytes, x_bytes, sstride;
-  int32_t stages, share;    // of a row; of a workgroup of mx_split_kernel
+  int32_t stages, share;    // of a row; of a workgroup
   int32_t tn, tm;           // tiles
   int32_t vec;              // y takes 4 elements at once
 };
@@ -56,6 +56,12 @@ __device__ __forceinline__ void store_quad(const MxTileArgs& a, int row, int col
         if (a.y16) gmem(a.y16)[to + i] = f32_to_bf16(v[i]);
       }
   }
+}
+
+// The same of a share of k, in rows of a multiple of 4.
+__device__ __forceinline__ void store_part(const MxTileArgs& a, int row, int col, f32x4 v) {
+  const int64_t width = (a.n + 3) / 4 * 4;
+  if (col < a.n) *gmem(reinterpret_cast<f32x4*>(a.part + ((int64_t)blockIdx.y * a.m + row) * width + col)) = v;
 }
 
 template <bool XQ, int TN, int TM, int WN, int WM>
@@ -242,14 +248,15 @@ __global__ __launch_bounds__(WN * WM * 64) void mx_tile_kernel(MxTileArgs a) {
   // stage is requested again, to buffers that nobody reads any more (its scales over
   // themselves), and what lies there is read but not multiplied.  (With branches the
   // compiler moves the products behind them, and their operands to memory.)
-  const int count = a.stages;
+  const int begin = (int)blockIdx.y * a.share, end = min(begin + a.share, a.stages);
 #pragma unroll
-  for (int i = 0; i < S; ++i) for_parts<T::kOps>([&](auto op) __attribute__((always_inline)) { request_op(min(i, count - 1), i, op); });
+  for (int i = 0; i < S; ++i)
+    for_parts<T::kOps>([&](auto op) __attribute__((always_inline)) { request_op(min(begin + i, end - 1), begin + i, op); });
   wait_requests<(S - 1) * T::kOps>();
   meet();
-  read(0, At<0>{});
-  read_scales(0);
-  for (int s = 0; s < count; ++s) {
+  read(begin, At<0>{});
+  read_scales(begin);
+  for (int s = begin; s < end; ++s) {
     clear(s, At<0>{});
     for_parts<kParts - 1>([&](auto part) __attribute__((always_inline)) {
       read(s, At<decltype(part)::value + 1>{});
@@ -265,11 +272,11 @@ __global__ __launch_bounds__(WN * WM * 64) void mx_tile_kernel(MxTileArgs a) {
     multiply(At<kParts - 1>{}, [&](auto at) __attribute__((always_inline)) {
       constexpr int r = decltype(at)::value, from = r * T::kOps / TR, to = (r + 1) * T::kOps / TR;
       for_parts<to - from>([&](auto op) __attribute__((always_inline)) {
-        request_op(min(s + S, count - 1), s, At<from + decltype(op)::value>{});
+        request_op(min(s + S, end - 1), s, At<from + decltype(op)::value>{});
       });
       __builtin_amdgcn_sched_barrier(0);
     });
-    read_scales(min(s + 1, count - 1));
+    read_scales(min(s + 1, end - 1));
   }
   wait_requests<0>();
 
@@ -281,7 +288,10 @@ __global__ __launch_bounds__(WN * WM * 64) void mx_tile_kernel(MxTileArgs a) {
 #pragma unroll
     for (int r = 0; r < TN; ++r) {
       const int col = n0 + wave / WM * TN * 16 + r * 16 + 4 * g;
-      store_quad(a, row, col, acc[r][t]);
+      if (a.part)
+        store_part(a, row, col, acc[r][t]);
+      else
+        store_quad(a, row, col, acc[r][t]);
     }
   }
 }
