@@ -359,18 +359,28 @@ def wq_gemm_smallM_int8(x, m, q, scale, n, k, y_f32=None, y_bf16=None, stream=No
           _ptr(y_bf16, ok and 2 * m * n, "y_bf16"), _stream(stream))
 
 
-def _mx_call(fn, name, stream, n, k, a, b, c, d):
-    """A call over [n][k] values with buffers (tensor, bytes, what) before and behind the sizes.  They are checked as in
-    _ptr, and the current stream is asked for as in _run (a call on a few rows is bound by these lines)."""
+def _mx_call(fn, name, stream, n, k, *buffers):
+    """A call over [n][k] values with two buffers (tensor, bytes, what) before and two behind the sizes.  They are checked
+    as in _ptr and must be on the current device, and the current stream is asked for as in _run (a call on a few rows is
+    bound by these lines)."""
     ok = _nonneg(n, k)
-    tensors = [t[0] for t in (a, b, c, d) if t is not None and hasattr(t[0], "get_device")]
-    a, b, c, d = (None if t is None else _ptr(t, ok and size, what) for t, size, what in (a, b, c, d))
-    _refuse_host((a, b, c, d))
-    device = _current_device() if tensors or stream is None else None
-    for t in tensors:
-        if t.get_device() != device:
-            raise ValueError(f"libwq: a buffer is on device {t.get_device()}, the current one is {device}")
-    rc = fn(a, b, n, k, c, d, _raw_stream(device) if stream is None else _stream(stream))
+    at, devices = [], set()
+    for t, nbytes, what in buffers:
+        if t is None or isinstance(t, int):
+            at.append(t)
+            continue
+        if ok and t.numel() * t.element_size() < nbytes:
+            raise ValueError(f"libwq: {what} holds {t.numel() * t.element_size()} bytes; the sizes given need {nbytes}")
+        if not t.is_contiguous():
+            raise ValueError(f"libwq: {what} must be contiguous")
+        devices.add(t.get_device())
+        at.append(t.data_ptr())
+    if -1 in devices:
+        _refuse_host((_HostBuffer(),))
+    device = _current_device() if devices or stream is None else None
+    if devices and devices != {device}:
+        raise ValueError(f"libwq: buffers on devices {sorted(devices)}, the current one is {device}")
+    rc = fn(at[0], at[1], n, k, at[2], at[3], _raw_stream(device) if stream is None else _stream(stream))
     if rc != 0:
         raise WQError(name, rc, lib.wq_last_error().decode(errors="replace"))
 

@@ -3,7 +3,9 @@
 //
 // A workgroup takes a row, a thread up to CPT pieces of eight elements, which it keeps
 // in registers from the first load to the last store; everything is requested before
-// the first sum.  Bound by HBM.
+// the first sum.  Bound by HBM: 4099 rows of 8192 (fp32 h in and out, bf16 f and gate, two
+// norms, 4-bit results; 424 MB) 110 us, 3.9 TB/s, with fp64 arithmetic about two thirds of
+// the time under way beside it.  One row of 4096: 3.5 us, a launch and two latencies.
 //
 // Sums of squares are fp64 (no row overflows or vanishes in them).  Elements are fp32
 // where u is bf16; a norm's factor is applied as mantissa and exponent, so that rows of
@@ -394,6 +396,9 @@ static void norm_launch(const NormArgs& a, int64_t rows, hipStream_t s) {
   // a grid's axis holds less than 2^32 threads
   const int64_t wide = rows < kNormGridX ? rows : kNormGridX;
   const dim3 grid((unsigned)wide, (unsigned)((rows + wide - 1) / wide));
+  // Enough threads that a row's loads are all under way, few enough that several rows share
+  // a CU while others sum or store: 4099 rows of 8192 in fp64 110 us with 512 threads of two
+  // pieces, 120 with 256 of four, 175 with 1024 of one.
   if (pieces <= 64)
     hipLaunchKernelGGL((block_norm_kernel<A, 1, 64>), grid, dim3(64), 0, s, a);
   else if (pieces <= 256)

@@ -13,6 +13,11 @@
 // expert are a 64-bit mask, which every workgroup builds itself from the selections.
 // The second product takes silu(h1) h3 in bf16 parts: three (24 bits), or two (16 bits)
 // where only bf16 results are asked for, as further columns of the matrix instruction.
+//
+// Measured (dim 4096, f 14336): one token of two int8 experts (352 MB) 76 us, 4.6 TB/s
+// (up 46, moe_few_kernel 26); 6 tokens of 8 experts in MXFP4 (616 MB) 141 us (scores 5.4,
+// up 67 to 80, down 55, join 4.7).  61 tokens of 128 experts (dim 2048, f 768, 316 MB) 97
+// us (scores 5.7, selection 4.8, up 45, down 38, join 4.7): many starts of short streams.
 #include <stdint.h>
 
 #include <algorithm>

@@ -2,7 +2,10 @@
 //
 // Few rows (mx_rows_kernel) are bound by W's bytes: a workgroup takes a block of 16-row
 // tiles, its waves split the row's spans (and, for short rows, the tiles), and their
-// sums meet in LDS in a fixed order.
+// sums meet in LDS in a fixed order.  5 rows x 57344 x 8192 (251 MB) 47.1 us, 5.3 TB/s;
+// 1 row x 12288 x 4096 (26.8 MB) 7.3 us, of which the start of a launch and of the loads
+// is about half.  More rows (mx_tile_kernel, mx_split_kernel) are bound by the matrix
+// pipe and what feeds it; tile_plan chooses.
 #include <stdint.h>
 
 #include <algorithm>
@@ -356,6 +359,10 @@ extern "C" int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream) {
                                       (needs_pad(g.k) ? ((g.m + g.n) * t.sstride + 15) / 16 * 16 : 0));
     return tiles_launch(name, t, p, g.xq, s);
   }
+  // as many columns as there are rows of x, since their LDS comes off the ring's: eight
+  // waves have three slots beside 4 columns, two beside 8; 16 columns leave room for four
+  // waves (of four slots), or six of two, which were no faster (4 waves with 4 or 8 columns
+  // are up to 10 % slower than eight)
   if (g.xq) return rows_launch<true, 16, 8, 3>(name, a, s);
   if (g.m <= 4) return rows_launch<false, 4, 8, 3>(name, a, s);
   if (g.m <= 8) return rows_launch<false, 8, 8, 2>(name, a, s);

@@ -1,11 +1,14 @@
 // Product of a middling number of rows with MXFP4 weights, where tiles of 256 x 256 do
 // not fill the chip: a workgroup takes 16 TN weight rows x 16 TM activation rows over a
-// share of k, and its four waves take the share's stages in turn, each with a ring of P
-// stages of its own (no barrier until the end; a wave's operands meet the whole tile, so
-// little LDS is read per product).  The waves' sums meet in LDS, the shares' in a second
-// launch, both in a fixed order.
+// share of k, and its waves take the share's stages in turn, each with a ring of P stages
+// of its own (no barrier until the end; a wave's operands meet the whole tile, so little
+// LDS is read per product).  The waves' sums meet in LDS, the shares' in a second launch,
+// both in a fixed order.
 //
-// Stages, operands and lanes are those of mx_tile_kernel.
+// Stages, operands and lanes are those of mx_tile_kernel.  47 rows x 4096 x 14336 (tiles
+// of 64 x 48, four shares): 16.4 us, about 13 in this launch and 3.5 in the second.  It is
+// bound by latencies: the start of both launches, and seven stages a wave of which two are
+// under way.
 #pragma once
 
 #include <stdint.h>
