@@ -797,3 +797,98 @@ def test_products_of_scales_far_apart(wq, m, n, k, xkind):
     within(np.where(fine, got, 0), np.where(fine, want, 0),
            np.where(fine, (k + 16) * 2.0 ** -23 * size + k * 2.0 ** -126, 0), "far scales")
     assert (np.abs(want[fine]) > 2.0 ** -100).any() and (np.abs(want[fine]) < 2.0 ** -120).any()
+
+
+@pytest.mark.parametrize("xkind", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("m,n,k,stride", [(1 << 20, 40, 32, 32), (3, 1 << 24, 32, 32), (20, 70, 1 << 18, 1 << 18), (2, 70, 1 << 18, 1 << 18),
+                                          (300, 80, 96, 1 << 22), (9, 80, 96, 1 << 22), (1 << 20, 300, 64, 64)])
+def test_products_at_the_documented_limits(wq, m, n, k, stride, xkind):
+    """As many rows, columns and inputs and as long a stride as documented; rows and columns here and there against 64
+    bits."""
+    import torch
+    rng = np.random.default_rng(14)
+    q = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device="cuda")
+    s = torch.randint(124, 131, (n, k // 32), dtype=torch.uint8, device="cuda")
+    if xkind == "bf16":
+        x = torch.empty(m, stride, dtype=torch.bfloat16, device="cuda")[:, :k]
+        x.normal_()
+        xs = None
+    else:
+        x = torch.randint(0, 256, (m, k // 2), dtype=torch.uint8, device="cuda")
+        xs = torch.randint(125, 130, (m, k // 32), dtype=torch.uint8, device="cuda")
+    y = empty(m, n, dtype="bfloat16" if m * n > 1 << 26 else "float32")
+    wq.wq_gemm_mxfp4_run(wq.wq_gemm_mxfp4_prepare(x, q, s, y, x_scale=xs))
+    rows = np.unique(np.r_[0, m - 1, rng.integers(0, m, 40)])
+    cols = np.unique(np.r_[0, n - 1, rng.integers(0, n, 60)])
+    take = torch.from_numpy
+    xv = f64(x[take(rows)]) if xs is None else block.mx_values(x[take(rows)].cpu().numpy(), xs[take(rows)].cpu().numpy())
+    w = block.mx_values(q[take(cols)].cpu().numpy(), s[take(cols)].cpu().numpy())
+    want, size = xv @ w.T, np.abs(xv) @ np.abs(w).T
+    allowed = (k + 16) * 2.0 ** -23 * size
+    if y.dtype == torch.bfloat16:
+        allowed = allowed + BF16 * (np.abs(want) + allowed)
+    within(f64(y[take(rows)][:, take(cols)]), want, allowed, "y")
+
+
+def test_a_norm_of_one_row_at_the_longest_stride(wq):
+    """Strides far past a row: the offsets of the last rows pass 32 bits."""
+    import torch
+    rows, dim, stride = 3, 64, 1 << 31
+    rng = np.random.default_rng(15)
+    hv, ht = bf16(rng.normal(0, 1, (rows, dim)))
+    wide = torch.empty((rows - 1) * stride + dim, dtype=torch.bfloat16, device="cuda")
+    h = wide.as_strided((rows, dim), (stride, 1))
+    h.copy_(ht)
+    u = torch.empty_like(wide).as_strided((rows, dim), (stride, 1))
+    wq.wq_block_norm_run(wq.wq_block_norm_prepare(h, u=u, eps=0.0))
+    _, want = block.block_norm(hv, eps=0.0)
+    within(f64(u), want, (BF16 + 2.0 ** -18) * np.abs(want), "u")
+
+
+@pytest.mark.parametrize("weights", ["int8", "mxfp4"])
+@pytest.mark.parametrize("tokens", [1, 64])
+def test_experts_at_the_documented_limits(wq, tokens, weights):
+    """dim and f of 32768, the second expert's weights past 32 bits of offset: sampled columns against 64 bits."""
+    import torch
+    dim = f = 32768
+    e = 2 if weights == "int8" else 3
+    if weights == "int8":
+        w13 = torch.randint(-127, 128, (e, 2 * f, dim), dtype=torch.int8, device="cuda")
+        w2 = torch.randint(-127, 128, (e, dim, f), dtype=torch.int8, device="cuda")
+        s13 = torch.full((e, 2 * f), 2.0 ** -14, dtype=torch.bfloat16, device="cuda")
+        s2 = torch.full((e, dim), 2.0 ** -14, dtype=torch.bfloat16, device="cuda")
+
+        def values(q, s):
+            return q.double() * s.double()[:, None]
+    else:
+        w13 = torch.randint(0, 256, (e, 2 * f, dim // 2), dtype=torch.uint8, device="cuda")
+        w2 = torch.randint(0, 256, (e, dim, f // 2), dtype=torch.uint8, device="cuda")
+        s13 = torch.randint(117, 120, (e, 2 * f, dim // 32), dtype=torch.uint8, device="cuda")
+        s2 = torch.randint(117, 120, (e, dim, f // 32), dtype=torch.uint8, device="cuda")
+        table = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64, device="cuda")
+
+        def values(q, s):
+            v = torch.stack([table[(q & 15).long()], table[(q >> 4).long()]], -1).flatten(-2)
+            return v * torch.exp2(s.double() - 127).repeat_interleave(32, -1)
+    _, x = bf16(np.random.default_rng(16).normal(0, 1, (tokens, dim)))
+    logits = torch.zeros(tokens, e, device="cuda")
+    logits[:, e - 1] = 3
+    y = empty(tokens, dim)
+    wq.wq_moe_ffn_run(wq.wq_moe_ffn_prepare(x, w13, s13, w2, s2, y, logits=logits, top=1))
+    h = []
+    for half in range(2):
+        parts = [x.double() @ values(w13[-1, r:r + 2048], s13[-1, r:r + 2048]).T for r in range(half * f, (half + 1) * f, 2048)]
+        h.append(torch.cat(parts, 1))
+    act = h[0] / (1 + torch.exp(-h[0])) * h[1]
+    cols = torch.tensor([0, 1, 17, 4095, 20000, dim - 2, dim - 1], device="cuda")
+    w = values(w2[-1, cols], s2[-1, cols])
+    want, size = act @ w.T, act.abs() @ w.abs().T
+    # sums of `dim` products behind act (its errors meet at random; here at most (dim + 16) 2^-23 of |x| |w13|, as in the
+    # other layers' bound) and of 3 f parts
+    biggest = values(w13[-1, :2048], s13[-1, :2048]).abs()
+    d = (dim + 16) * 2.0 ** -23 * float((x.double().abs() @ biggest.T).max()) * 1.1
+    da = 1.1 * d * (h[1].abs() + d) + act.abs() * 2.0 ** -19 + d * h[0].abs()
+    allowed = da @ w.abs().T + ((3 * f + 16) * 2.0 ** -23 + 2.0 ** -19) * size
+    within(f64(y[:, cols]), f64(want), f64(allowed), "y")
+    # what the bound above is for: no piece of a sum is missing or doubled
+    assert float((y[:, cols].double() - want).abs().max()) < 1e-3 * float(size.max())
