@@ -759,8 +759,7 @@ int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream);
  *   sel     int32 [tokens][top], gates fp32 [tokens][top], each may be NULL
  * Scores are fp64 sums, so that no order of summation decides which experts run;
  * products are summed in fp32, and silu(W1 x) * (W3 x) is carried to the second
- * in bf16 parts: three (24 bits), or two (16 bits) where only y_bf16 is asked
- * for.  Weights past the largest finite bf16 (MXFP4 scale bytes of 253 and 254)
+ * in 24 bits (three bf16 parts), whichever results are asked for.  Weights past the largest finite bf16 (MXFP4 scale bytes of 253 and 254)
  * give results that are not finite.  Only the selected experts' weights are
  * read; routing happens on the device.  tokens 0..64, e 1..256, top 1..16 (at
  * most e), dim and f multiples of 16 (MXFP4: 32) up to 32768; x, w13, w2, router

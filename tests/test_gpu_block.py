@@ -288,6 +288,22 @@ def test_expert_layer(wq, tokens, e, top, dim, f, weights):
          renormalize=i % 5 != 0, pad=i % 2)
 
 
+@pytest.mark.parametrize("weights", ["mxfp4", "int8"])
+@pytest.mark.parametrize("tokens,e,top,dim,f", LAYERS + [(2, 8, 6, 64, 96), (16, 8, 2, 96, 1056), (50, 8, 2, 64, 512), (20, 64, 6, 64, 96)])
+def test_a_bf16_result_is_the_rounded_fp32_result(wq, tokens, e, top, dim, f, weights):
+    """What is carried between the products does not depend on the results' type."""
+    import torch
+    rng = np.random.default_rng(tokens * 5 + e + dim + f)
+    _, t13 = _experts(rng, e, 2 * f, dim, weights)
+    _, t2 = _experts(rng, e, dim, f, weights)
+    _, x = bf16(rng.normal(0, 1, (tokens, dim)))
+    _, logits = f32(rng.normal(0, 1.5, (tokens, e)))
+    y32, y16 = empty(tokens, dim), empty(tokens, dim, dtype="bfloat16")
+    for y in (y32, y16):
+        wq.wq_moe_ffn_run(wq.wq_moe_ffn_prepare(x, *t13, *t2, y, logits=logits, top=top))
+    assert torch.equal(y32.to(torch.bfloat16), y16)
+
+
 @pytest.mark.parametrize("tokens", [1, 3, 20])
 def test_int8_experts_of_odd_sixteens(wq, tokens):
     _moe(wq, np.random.default_rng(tokens), tokens, 5, 2, 48, 272, "int8", "router", "f32")

@@ -11,8 +11,8 @@
 //
 // A token's experts are distinct and there are at most 64 tokens, so the tokens of an
 // expert are a 64-bit mask, which every workgroup builds itself from the selections.
-// The second product takes silu(h1) h3 in bf16 parts: three (24 bits), or two (16 bits)
-// where only bf16 results are asked for, as further columns of the matrix instruction.
+// The second product takes silu(h1) h3 in three bf16 parts (24 bits, an fp32 value's), as
+// further columns of the matrix instruction.
 //
 // Measured (dim 4096, f 14336): one token of two int8 experts (352 MB) 76 us, 4.6 TB/s
 // (up 46, moe_few_kernel 26); 6 tokens of 8 experts in MXFP4 (616 MB) 141 us (scores 5.4,
@@ -29,6 +29,7 @@
 namespace wq {
 
 constexpr int kMoeTokens = 64, kMoeExperts = 256, kMoeTop = 16;
+constexpr int kParts = 3;                        // of silu(h1) h3
 
 struct MoeArgs {
   const uint16_t* x;
@@ -40,7 +41,7 @@ struct MoeArgs {
   float* gates;
   int32_t* user_sel;       // the caller's copies, or null
   float* user_gates;
-  uint16_t* act;           // [tokens * top][parts][f], in the order of experts
+  uint16_t* act;           // [tokens * top][kParts][f], in the order of experts
   float* sums;             // [tokens * top][dim], in the order of selection, weighted
   StreamWeights w13, w2;
   const uint16_t* s13;     // int8: row scales
@@ -50,7 +51,6 @@ struct MoeArgs {
   int64_t y_stride;
   int32_t tokens, dim, f, e, top, renormalize;
   int32_t here;            // the selection is made by the up launch itself
-  int32_t parts;
   int32_t spans, spans2;   // of a row of W1, of W2
   // of a launch: pairs of row tiles (up) or tiles (down) of a workgroup, workgroups of an
   // expert's rows, waves that share a tile's spans
@@ -296,9 +296,9 @@ __device__ __forceinline__ bool find_item(const MoeTokens& all, int item, int ch
   return true;
 }
 
-// bf16 parts of v whose sum is v (three), or v to 16 bits (two).  Truncated, so that
+// bf16 parts of v, whose sum is v (but for what lies below 2^-133).  Truncated, so that
 // none overflows; infinities and NaN are the first part alone.
-__device__ __forceinline__ void bf16_parts(float v, int parts, uint16_t (&p)[3]) {
+__device__ __forceinline__ void bf16_parts(float v, uint16_t (&p)[kParts]) {
   p[1] = p[2] = 0;
   if (!(fabsf(v) < INFINITY)) {
     p[0] = f32_to_bf16(v);
@@ -307,13 +307,9 @@ __device__ __forceinline__ void bf16_parts(float v, int parts, uint16_t (&p)[3])
   const uint32_t b = __float_as_uint(v);
   p[0] = (uint16_t)(b >> 16);
   const float rest = v - __uint_as_float(b & 0xFFFF0000u);
-  if (parts == 2) {
-    p[1] = f32_to_bf16(rest);
-  } else {
-    const uint32_t m = __float_as_uint(rest);
-    p[1] = (uint16_t)(m >> 16);
-    p[2] = f32_to_bf16(rest - __uint_as_float(m & 0xFFFF0000u));
-  }
+  const uint32_t m = __float_as_uint(rest);
+  p[1] = (uint16_t)(m >> 16);
+  p[2] = f32_to_bf16(rest - __uint_as_float(m & 0xFFFF0000u));
 }
 
 // ---------------------------------------------------------------------------
@@ -344,9 +340,9 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_up_kernel(MoeArgs
   const S s(lds + wave * S::kBytes);
   const int first = (int)blockIdx.x % a.blocks * a.per, mine = min(a.per, a.pairs - first);
   const int pairs = (mine - tw + teams - 1) / teams;
-  f32x4 acc[kUpTiles];
+  f32x4 acc[kUpTiles][1];
 #pragma unroll
-  for (int t = 0; t < kUpTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < kUpTiles; ++t) acc[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int64_t rows0 = (int64_t)expert * 2 * a.f;
   // a tile of W1, then the same rows of W3
   s.template run<kUpTiles>(
@@ -359,7 +355,7 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_up_kernel(MoeArgs
       0, 1, acc);
   __syncthreads();
   for_tiles<kUpTiles>(2 * pairs, [&](auto at) __attribute__((always_inline)) {
-    *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * 1024 + s.lane * 16) = acc[at.value];
+    *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * 1024 + s.lane * 16) = acc[at.value][0];
   });
   __syncthreads();
   for (int o = (int)threadIdx.x; o < mine * 16 * cols; o += WAVES * 64) {
@@ -376,10 +372,11 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_up_kernel(MoeArgs
       h3 *= __uint_as_float((uint32_t)gmem(a.s13)[rows0 + a.f + r] << 16);
     }
     const float v = h1 / (1.f + expf(-h1)) * h3;
-    uint16_t p[3];
-    bf16_parts(v, a.parts, p);
-    uint16_t* to = a.act + (int64_t)(slot + begin + col) * a.parts * a.f + r;
-    for (int q = 0; q < a.parts; ++q) gmem(to)[q * a.f] = p[q];
+    uint16_t p[kParts];
+    bf16_parts(v, p);
+    uint16_t* to = a.act + (int64_t)(slot + begin + col) * kParts * a.f + r;
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) gmem(to)[q * a.f] = p[q];
   }
 }
 
@@ -389,14 +386,14 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_up_kernel(MoeArgs
 template <bool MX, bool ODD, int COLS, int WAVES, int P, bool TWO>
 __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_down_kernel(MoeArgs a) {
   using S = RowStream<MX, false, ODD, COLS, P>;
-  constexpr int kRed = WAVES * kUpTiles * 1024, kAll = WAVES * S::kBytes;
+  constexpr int kTile = S::kSets * 1024, kRed = WAVES * kUpTiles * kTile, kAll = WAVES * S::kBytes;
   __shared__ __align__(1024) char lds[kAll > kRed ? kAll : kRed];
   MoeTokens& all = *reinterpret_cast<MoeTokens*>(lds);
   static_assert(sizeof(MoeTokens) <= sizeof(lds));
   __shared__ float gate[COLS];
   __shared__ int pick[COLS];
   find_tokens<WAVES>(a, all);
-  const int chunk = COLS / a.parts;                 // tokens; a column for each of their parts
+  constexpr int chunk = COLS / kParts;              // tokens; a column for each of their parts
   int expert, begin, slot;
   if (!find_item(all, (int)blockIdx.x / a.blocks, chunk, expert, begin, slot)) return;
   const uint64_t mask = all.mask[expert];
@@ -415,11 +412,13 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_down_kernel(MoeAr
   const S s(lds + wave * S::kBytes);
   const int first = (int)blockIdx.x % a.blocks * a.per, mine = min(a.per, a.dim / 16 - first);
   const int tiles = (mine - tw + teams - 1) / teams;
-  f32x4 acc[kUpTiles];
+  f32x4 acc[kUpTiles][S::kSets];
 #pragma unroll
-  for (int t = 0; t < kUpTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < kUpTiles; ++t)
+#pragma unroll
+    for (int q = 0; q < S::kSets; ++q) acc[t][q] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int64_t rows0 = (int64_t)expert * a.dim;
-  const uint16_t* act = a.act + (int64_t)(slot + begin) * a.parts * a.f;
+  const uint16_t* act = a.act + (int64_t)(slot + begin) * kParts * a.f;
   s.template run<kUpTiles>(
       a.w2, tiles, kw, ways, a.spans2, (int)(a.w2.row_bytes / 16),
       [&](int t, int64_t& row0, int& left) {
@@ -428,21 +427,27 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_down_kernel(MoeAr
       },
       // columns: part after part, `chunk` tokens each
       [&](int col) {
-        const int part = min(col / chunk, a.parts - 1), tok = min(col % chunk, have - 1);
-        return reinterpret_cast<const char*>(act + (int64_t)(tok * a.parts + part) * a.f);
+        const int part = min(col / chunk, kParts - 1), tok = min(col % chunk, have - 1);
+        return reinterpret_cast<const char*>(act + (int64_t)(tok * kParts + part) * a.f);
       },
       2u * a.f, nullptr, 0, 0, 1, acc);
   __syncthreads();
   for_tiles<kUpTiles>(tiles, [&](auto at) __attribute__((always_inline)) {
-    *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * 1024 + s.lane * 16) = acc[at.value];
+#pragma unroll
+    for (int q = 0; q < S::kSets; ++q)
+      *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * kTile + q * 1024 + s.lane * 16) = acc[at.value][q];
   });
   __syncthreads();
   for (int o = (int)threadIdx.x; o < mine * 16 * have; o += WAVES * 64) {
     const int row = o & 15, tok = (o >> 4) % have, tile = (o >> 4) / have;
-    const char* from = lds + ((tile % teams) * ways * kUpTiles + tile / teams) * 1024 + ((row >> 2) * 16 + tok) * 16 + (row & 3) * 4;
+    const char* from = lds + ((tile % teams) * ways * kUpTiles + tile / teams) * kTile + (row >> 2) * 256 + (row & 3) * 4;
     float v = 0.f;
-    for (int q = a.parts - 1; q >= 0; --q)
-      for (int w = 0; w < ways; ++w) v += *reinterpret_cast<const float*>(from + w * kUpTiles * 1024 + q * chunk * 16);
+#pragma unroll
+    for (int q = kParts - 1; q >= 0; --q) {
+      const int col = q * chunk + tok;
+      for (int w = 0; w < ways; ++w)
+        v += *reinterpret_cast<const float*>(from + w * kUpTiles * kTile + (col >> 4) * 1024 + (col & 15) * 16);
+    }
     const int r = (first + tile) * 16 + row;
     if constexpr (!MX) v *= __uint_as_float((uint32_t)gmem(a.s2)[rows0 + r] << 16);
     gmem(a.sums)[(int64_t)pick[tok] * a.dim + r] = gate[tok] * v;
@@ -517,7 +522,8 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
   }
   for (int i = lane; i < TM * 16; i += 64) sums[wave][i] = 0.f;
   __syncthreads();
-  const int used = down.used, chunk = COLS / a.parts;
+  constexpr int chunk = COLS / kParts;
+  const int used = down.used;
   const int64_t tile = (int64_t)blockIdx.x * 16;
   char* const base = lds + wave * kWave0;
   const int g = lane >> 4, c = lane & 15;
@@ -542,13 +548,13 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
     const int u = q.pair / a.spans2, span = q.pair % a.spans2;
     const int expert = __builtin_amdgcn_readfirstlane(down.expert[u]), row = __builtin_amdgcn_readfirstlane(down.slot[u]);
     const int have = min(chunk, tokens_of(q.pair) - q.chunk * chunk);
-    const uint16_t* act = a.act + (int64_t)(row + q.chunk * chunk) * a.parts * a.f;
+    const uint16_t* act = a.act + (int64_t)(row + q.chunk * chunk) * kParts * a.f;
     // columns: part after part, `chunk` tokens each
     const S x(base + slot * S::kXBytes);
     x.request_x(
         [&](int col) {
-          const int part = min(col / chunk, a.parts - 1), tok = min(col % chunk, have - 1);
-          return reinterpret_cast<const char*>(act + (int64_t)(tok * a.parts + part) * a.f);
+          const int part = min(col / chunk, kParts - 1), tok = min(col % chunk, have - 1);
+          return reinterpret_cast<const char*>(act + (int64_t)(tok * kParts + part) * a.f);
         },
         2u * a.f, span);
     const S w(base + (P - 1) * S::kXBytes);
@@ -562,7 +568,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
       request(ask, made++ % P);
       next(ask);
     }
-  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
   constexpr int kOps = S::kOps + S::kXOps;
   const int pieces = (int)(a.w2.row_bytes / 16);
   while (now.pair < pairs) {
@@ -573,7 +579,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
       wait_requests<(P - 1) * kOps>();
     else
       wait_requests<0>();
-    u32x4 x[S::kFrags];
+    u32x4 x[1][S::kFrags];
     S(base + slot * S::kXBytes).read_x(x, span, pieces);
     const auto unit = S(base + (P - 1) * S::kXBytes).read_unit(a.w2, (int64_t)expert * a.dim + tile, 16, span, pieces, slot);
     wait_lds();
@@ -582,16 +588,17 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
       ++made;
       next(ask);
     }
-    acc = S::multiply(unit, x, 0u, acc);
+    S::multiply(unit, x, 0u, acc);
     ++done;
     Cursor after = now;
     next(after);
     if (after.pair >= pairs || after.chunk != now.chunk || after.pair / a.spans2 != u) {
       // columns of a token's parts meet, then go to its row of this wave's sums
-      f32x4 v = acc;
-      for (int q = 1; q < a.parts; ++q)
+      f32x4 v = acc[0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += __shfl(acc[i], lane + q * chunk);
+      for (int q = 1; q < kParts; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __shfl(acc[0][i], lane + q * chunk);
       const uint64_t mask = all.mask[expert];
       const int begin = now.chunk * chunk, have = min(chunk, __popcll(mask) - begin);
       if (c < have) {
@@ -609,7 +616,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
           sums[wave][t * 16 + 4 * g + i] += gate * o;
         }
       }
-      acc = f32x4{0.f, 0.f, 0.f, 0.f};
+      acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     now = after;
   }
@@ -735,13 +742,26 @@ static void up_launch(MoeArgs a, hipStream_t s) {
 
 template <bool MX, int COLS, int WAVES, int P, bool TWO = false>
 static void down_launch(MoeArgs a, hipStream_t s) {
+  constexpr int chunk = COLS / kParts;
   const int picks = a.tokens * a.top, used = std::min(a.e, picks);
-  rows_plan(a, WAVES, used, a.dim / 16, 1, a.spans2, TWO ? 512 : 256);
-  const dim3 grid((unsigned)((used + picks / (COLS / a.parts)) * a.blocks));
+  // items of `chunk` tokens, as expected where experts have about as many tokens each
+  // (planned for the experts alone, 16 tokens of Mixtral's eight in MXFP4 take 200 us, not 161)
+  const int items = std::max(used, (picks + used * (chunk - 1) / 2 + chunk - 1) / chunk);
+  rows_plan(a, WAVES, items, a.dim / 16, 1, a.spans2, TWO ? 512 : 256);
+  const dim3 grid((unsigned)((used + picks / chunk) * a.blocks));
   if (MX && a.w2.srow % 4)
     hipLaunchKernelGGL((moe_down_kernel<MX, MX, COLS, WAVES, P, TWO>), grid, dim3(WAVES * 64), 0, s, a);
   else
     hipLaunchKernelGGL((moe_down_kernel<MX, false, COLS, WAVES, P, TWO>), grid, dim3(WAVES * 64), 0, s, a);
+}
+
+template <bool MX, int TOKENS, int WAVES>
+static void few_launch(const MoeArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.dim / 16)), block(WAVES * 64);
+  if (MX && a.w2.srow % 4)
+    hipLaunchKernelGGL((moe_few_kernel<MX, MX, TOKENS * kParts, WAVES, 2, TOKENS>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((moe_few_kernel<MX, false, TOKENS * kParts, WAVES, 2, TOKENS>), grid, block, 0, s, a);
 }
 
 template <bool MX>
@@ -761,19 +781,27 @@ static void experts_launch(MoeArgs a, hipStream_t s) {
   else
     up_launch<MX, 16, 4, 4>(a, s);
   a.here = 0;
-  if (a.tokens * a.parts <= 4) {
-    if (MX && a.w2.srow % 4)
-      hipLaunchKernelGGL((moe_few_kernel<MX, MX, 4, 8, 2, 2>), dim3((unsigned)(a.dim / 16)), dim3(512), 0, s, a);
-    else
-      hipLaunchKernelGGL((moe_few_kernel<MX, false, 4, 8, 2, 2>), dim3((unsigned)(a.dim / 16)), dim3(512), 0, s, a);
-    return;
+  // Nothing to join, where LDS holds a token's three parts beside enough weights: two tokens
+  // in seven waves (of Mixtral's experts in MXFP4 69 us, with moe_down_kernel and the join
+  // 77; but of 6 of 64 small experts 34 and 32, of Mixtral's in int8 151 and 141).
+  if (a.tokens == 1) return few_launch<MX, 1, 8>(a, s);
+  if constexpr (MX) {
+    if (a.tokens == 2 && a.top <= 4) return few_launch<MX, 2, 7>(a, s);
   }
+  // Columns are three for a token.  Two tokens at once leave room for eight waves of three
+  // slots (8 tokens of 128 experts 46 us, five at once 49).  Eight at once pay where a span's
+  // activations are few bytes and one pass over W2 does for nearly all experts: int8, 16
+  // tokens of Mixtral's 302 us, five at once 337; but 32 tokens 433 and 379, and in MXFP4 16
+  // tokens, seven at once, 251 and 200 (both planned for eight items).
+  constexpr int kMost = MX ? 15 : 24;
   if (many)
-    down_launch<MX, 8, 4, 2, true>(a, s);
-  else if (a.tokens * a.parts <= 8 || 2 * mean * a.parts <= 8)
-    down_launch<MX, 8, 8, 2>(a, s);
+    down_launch<MX, 9, 4, 2, true>(a, s);
+  else if (mean <= 1)
+    down_launch<MX, 6, 8, 3>(a, s);
+  else if (!MX && mean > 2 && mean < 8)
+    down_launch<MX, kMost, 4, 4>(a, s);
   else
-    down_launch<MX, 16, 4, 4>(a, s);
+    down_launch<MX, 15, 4, 4>(a, s);
   hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.tokens * (a.dim / 4) + 255) / 256)), dim3(256), 0, s, a);
 }
 
@@ -843,7 +871,6 @@ extern "C" int wq_moe_ffn_run(const wq_moe_ffn_plan* plan, void* stream) {
   a.e = (int32_t)m.e;
   a.top = m.top;
   a.renormalize = m.renormalize;
-  a.parts = m.y_f32 ? 3 : 2;
   a.spans = (int32_t)((up + 255) / 256);
   a.spans2 = (int32_t)((down + 255) / 256);
   hipStream_t s = (hipStream_t)stream;

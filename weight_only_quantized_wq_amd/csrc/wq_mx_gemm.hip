@@ -47,9 +47,9 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxRowsArgs a) {
   const int first = (int)blockIdx.x * a.per, mine = min(a.per, a.tiles - first);
   const int64_t m0 = (int64_t)blockIdx.y * COLS;
   const int cols = (int)min((int64_t)COLS, a.m - m0);
-  f32x4 acc[kRowTiles];
+  f32x4 acc[kRowTiles][1];
 #pragma unroll
-  for (int t = 0; t < kRowTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < kRowTiles; ++t) acc[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int tiles = (mine - tw + teams - 1) / teams;
   const char* x = a.x + m0 * a.x_stride;
   s.template run<kRowTiles>(
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxRowsArgs a) {
   // the waves' sums of a tile, lane by lane
   __syncthreads();
   for_tiles<kRowTiles>(tiles, [&](auto at) __attribute__((always_inline)) {
-    *reinterpret_cast<f32x4*>(lds + (wave * kRowTiles + at.value) * 1024 + s.lane * 16) = acc[at.value];
+    *reinterpret_cast<f32x4*>(lds + (wave * kRowTiles + at.value) * 1024 + s.lane * 16) = acc[at.value][0];
   });
   __syncthreads();
   for (int o = (int)threadIdx.x; o < mine * 16 * cols; o += WAVES * 64) {
