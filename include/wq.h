@@ -757,8 +757,8 @@ int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream);
  *           rows 0..f-1 of w13: W1 (gate), rows f..2f-1: W3 (up)
  *   y       fp32 and / or bf16 [tokens][y_stride], either may be NULL but not both
  *   sel     int32 [tokens][top], gates fp32 [tokens][top], each may be NULL
- * Scores are fp64 sums, so that no order of summation decides which experts run;
- * products are summed in fp32, and silu(W1 x) * (W3 x) is carried to the second
+ * Scores are fp64 sums in one order for all experts, so that equal router rows
+ * score the same; products are summed in fp32, and silu(W1 x) * (W3 x) is carried to the second
  * in 24 bits (three bf16 parts), whichever results are asked for.  Weights past the largest finite bf16 (MXFP4 scale bytes of 253 and 254)
  * give results that are not finite.  Only the selected experts' weights are
  * read; routing happens on the device.  tokens 0..64, e 1..256, top 1..16 (at

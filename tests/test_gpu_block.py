@@ -323,6 +323,23 @@ def test_equal_router_rows_tie_to_the_lower_index(wq):
     _moe(wq, rng, 6, 9, 3, 64, 32, "int8", "router", "bf16", router=np.repeat(row, 9, 0))
 
 
+@pytest.mark.parametrize("e,dim", [(22, 9216), (10, 32768), (129, 4096), (256, 1024), (9, 8192)])
+def test_equal_router_rows_score_the_same_in_every_workgroup(wq, e, dim):
+    """x with a few inputs 2^40 times the others, whose sums round: equal rows still tie, wherever they are summed."""
+    import torch
+    rng = np.random.default_rng(e + dim)
+    x = rng.normal(0, 1, (64, dim))
+    for row in x:
+        row[rng.integers(0, dim, 4)] *= 2.0 ** 40
+    _, x = bf16(x)
+    _, router = bf16(np.repeat(rng.normal(0, 1, (1, dim)), e, 0))
+    w13, w2 = torch.zeros(e, 32, dim, dtype=torch.int8, device="cuda"), torch.zeros(e, dim, 16, dtype=torch.int8, device="cuda")
+    s13, s2 = torch.ones(e, 32, dtype=torch.bfloat16, device="cuda"), torch.ones(e, dim, dtype=torch.bfloat16, device="cuda")
+    y, sel, gates = empty(64, dim), empty(64, 8, dtype="int32", fill=-1), empty(64, 8, fill=-1)
+    wq.wq_moe_ffn_run(wq.wq_moe_ffn_prepare(x, w13, s13, w2, s2, y, router=router, top=8, sel=sel, gates=gates))
+    assert (sel.cpu() == torch.arange(8)).all() and (gates == 0.125).all()
+
+
 @pytest.mark.parametrize("tokens", [2, 30])
 def test_nan_logits_select_distinct_experts_in_range(wq, tokens):
     import torch

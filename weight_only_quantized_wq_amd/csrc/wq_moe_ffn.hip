@@ -1,8 +1,8 @@
 // A whole mixture-of-experts layer for a few tokens: router, selected experts (SwiGLU)
 // and their weighted sum.  Bound by the bytes of the experts in use, each read once.
 //
-//   scores   x router^T in fp64 (bf16 products are exact there: which experts run does
-//            not depend on an order of summation); where the caller gives logits, none
+//   scores   x router^T in fp64, every expert's sum in the same order, so that equal
+//            router rows score the same; where the caller gives logits, none
 //   route    the `top` largest scores of each token and their gates
 //   up       a workgroup takes a block of rows of W1 and W3 of one expert over the
 //            tokens that chose it: h1, h3 meet in LDS, silu(h1) h3 goes to the workspace
@@ -196,9 +196,10 @@ __global__ __launch_bounds__(kScoreWaves * 64) void moe_score_kernel(MoeArgs a) 
   __shared__ double part[kScoreParts][kMoeExperts];
   const int t = (int)blockIdx.x, share = (a.e + (int)gridDim.y - 1) / (int)gridDim.y;
   const int first = (int)blockIdx.y * share, last = min(first + share, a.e);
-  // enough units for the waves, each at least 512 inputs
-  const int batches = (last - first + kScoreBatch - 1) / kScoreBatch;
-  const int parts = max(1, min(min(kScoreParts, (kScoreWaves + batches - 1) / max(batches, 1)), (a.dim + 511) / 512));
+  // enough units for the waves, each at least 512 inputs; of a whole share in the last one
+  // too, or its experts' sums would be split in another way
+  const int batches = (share + kScoreBatch - 1) / kScoreBatch;
+  const int parts = max(1, min(min(kScoreParts, (kScoreWaves + batches - 1) / batches), (a.dim + 511) / 512));
   score_experts(a, t, first, last, parts, part);
   __syncthreads();
   auto score = [&](int e) {
