@@ -686,8 +686,8 @@ int wq_lora_run(const wq_lora_plan* plan, void* stream);
  *                             smallest byte for a group of zeros
  * code = the nearest to w / 2^(scale - 127), ties to the even code, magnitudes
  * past 6 to 6.  A group that holds an infinity or a NaN gets scale 255 and
- * codes 0.  17/32 byte per weight.  w, q 16-byte aligned; n * k <= 2^40;
- * nothing overlaps (WQ_ERR_SHAPE).  Bit-identical to the CPU oracle.
+ * codes 0.  17/32 byte per weight.  w, q 16-byte aligned; n * k <= 2^37 -
+ * 2^13; nothing overlaps (WQ_ERR_SHAPE).  Bit-identical to the CPU oracle.
  */
 int wq_quantize_mxfp4(const float* w_f32, const uint16_t* w_bf16, int64_t n, int64_t k, uint8_t* q, uint8_t* scale,
                       void* stream);
@@ -695,7 +695,7 @@ int wq_quantize_mxfp4(const float* w_f32, const uint16_t* w_bf16, int64_t n, int
 /*
  * The values that codes stand for, as fp32 or bf16 [n][k] (exactly one; both
  * hold them exactly, but values past the largest finite one, which scale bytes
- * of 253 and 254 reach, are infinite).  q, y 16-byte aligned.
+ * of 253 and 254 reach, are infinite).  q, y 16-byte aligned; n * k as above.
  */
 int wq_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int64_t n, int64_t k, float* y_f32, uint16_t* y_bf16,
                         void* stream);

@@ -149,6 +149,15 @@ def test_quantiser_refusals():
     assert d(OK, 2 * FAR, 0, 32, FAR, None, None) == 0
 
 
+def test_the_quantiser_takes_no_more_than_a_grid_holds():
+    # a thread for 32 values, less than 2^32 of them; a size that is taken ends at the misaligned address behind it
+    q, d = lib.wq_quantize_mxfp4, lib.wq_dequantize_mxfp4
+    for n, k, rc in [((1 << 32) - 256, 32, 3), ((1 << 32) - 255, 32, 2), (1 << 32, 32, 2), (1, (1 << 37) - (1 << 13), 3),
+                     (1, 1 << 37, 2), (1 << 18, 1 << 20, 2), (1 << 20, 1 << 16, 3), (1 << 16, 1 << 22, 2)]:
+        assert q(BAD, None, n, k, FAR, 2 * FAR, None) == rc and q(None, BAD, n, k, FAR, 2 * FAR, None) == rc
+        assert d(OK, OK, n, k, BAD, None, None) == rc and d(OK, OK, n, k, None, BAD, None) == rc
+
+
 def test_null_descriptions_and_foreign_plans():
     assert lib.wq_block_norm_prepare(None, OK) == 1
     for name in ("wq_gemm_mxfp4", "wq_moe_ffn"):

@@ -15,7 +15,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMxGroup = 32;
-constexpr int64_t kMxMost = (int64_t)1 << 40;     // weights of one call
+// Weights of one call: the quantiser and its inverse take a thread for 32, and a grid's axis
+// holds less than 2^32 threads.
+constexpr int64_t kMxMost = ((int64_t)1 << 37) - (1 << 13);
 
 // 16 bytes of codes as the matrix instructions' operand, whose other half they do not read.
 typedef int i32x4 __attribute__((ext_vector_type(4)));

@@ -16,6 +16,7 @@ namespace wq {
 
 constexpr int kMxThreads = 256;
 constexpr int kPieces = 4;
+static_assert((kMxMost / (8 * kPieces) + kMxThreads - 1) / kMxThreads * kMxThreads < (int64_t)1 << 32);
 
 template <bool F32>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const void* w, int64_t eights, uint8_t* q, uint8_t* scale) {
@@ -111,7 +112,7 @@ extern "C" int wq_quantize_mxfp4(const float* w_f32, const uint16_t* w_bf16, int
   if (!w_f32 == !w_bf16) return fail(WQ_ERR_NULL, "%s: exactly one of w_f32 and w_bf16 must be given", name);
   if (!q || !scale) return fail(WQ_ERR_NULL, "%s: q and scale must be non-null", name);
   if (!mx_sizes_ok(n, k))
-    return fail(WQ_ERR_SHAPE, "%s: n = %lld, k = %lld (need n, k >= 0, k %% 32 == 0, n * k <= 2^40)", name, (long long)n,
+    return fail(WQ_ERR_SHAPE, "%s: n = %lld, k = %lld (need n, k >= 0, k %% 32 == 0, n * k <= 2^37 - 2^13)", name, (long long)n,
                 (long long)k);
   const void* w = w_f32 ? (const void*)w_f32 : (const void*)w_bf16;
   if (!aligned16(w) || !aligned16(q)) return fail(WQ_ERR_ALIGN, "%s: w and q must be 16-byte aligned", name);
@@ -137,7 +138,7 @@ extern "C" int wq_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int64
   if (!q || !scale) return fail(WQ_ERR_NULL, "%s: q and scale must be non-null", name);
   if (!y_f32 == !y_bf16) return fail(WQ_ERR_NULL, "%s: exactly one of y_f32 and y_bf16 must be given", name);
   if (!mx_sizes_ok(n, k))
-    return fail(WQ_ERR_SHAPE, "%s: n = %lld, k = %lld (need n, k >= 0, k %% 32 == 0, n * k <= 2^40)", name, (long long)n,
+    return fail(WQ_ERR_SHAPE, "%s: n = %lld, k = %lld (need n, k >= 0, k %% 32 == 0, n * k <= 2^37 - 2^13)", name, (long long)n,
                 (long long)k);
   void* y = y_f32 ? (void*)y_f32 : (void*)y_bf16;
   if (!aligned16(q) || !aligned16(y)) return fail(WQ_ERR_ALIGN, "%s: q and y must be 16-byte aligned", name);
