@@ -763,8 +763,8 @@ int wq_gemm_mxfp4_run(const wq_gemm_mxfp4_plan* plan, void* stream);
  * give results that are not finite.  Only the selected experts' weights are
  * read; routing happens on the device.  tokens 0..64, e 1..256, top 1..16 (at
  * most e), dim and f multiples of 16 (MXFP4: 32) up to 32768; x, w13, w2, router
- * 16-byte, s13 and s2 4-byte aligned (MXFP4: their last 4-byte word is read
- * whole), x_stride a multiple of 8; results overlap nothing (WQ_ERR_SHAPE).
+ * 16-byte, s13 and s2 2-byte aligned (MXFP4: 4-byte, and their last 4-byte word
+ * is read whole), x_stride a multiple of 8; results overlap nothing (WQ_ERR_SHAPE).
  */
 typedef struct {
   const uint16_t* x;

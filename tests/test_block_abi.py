@@ -131,6 +131,14 @@ def test_neighbours_are_no_overlap(call, kw):
     assert status(call, **kw) == 4, wq.last_error()
 
 
+@pytest.mark.parametrize("kw,rc", [(dict(format=2, s13=OK + 2), 4), (dict(format=2, s2=OK + 6), 4), (dict(format=2, s13=BAD), 3),
+                                   (dict(format=2, s2=BAD), 3), (dict(format=8, s2=OK + 2), 3)], ids=str)
+def test_int8_scales_need_the_alignment_of_their_elements(kw, rc):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are fake")
+    assert status("moe", x=OK, **kw) == rc, wq.last_error()
+
+
 def test_quantiser_refusals():
     q, d = lib.wq_quantize_mxfp4, lib.wq_dequantize_mxfp4
     assert q(None, None, 1, 32, OK, FAR, None) == 1 and q(OK, OK, 1, 32, FAR, FAR, None) == 1

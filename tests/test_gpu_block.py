@@ -304,6 +304,27 @@ def test_a_bf16_result_is_the_rounded_fp32_result(wq, tokens, e, top, dim, f, we
     assert torch.equal(y32.to(torch.bfloat16), y16)
 
 
+@pytest.mark.parametrize("tokens", [1, 2, 9])
+def test_int8_scales_at_an_odd_element(wq, tokens):
+    """Scales that start behind one other bf16, as a slice of a checkpoint's buffer does."""
+    import torch
+    rng = np.random.default_rng(tokens)
+    e, dim, f = 4, 48, 80
+    w13, (q13, s13) = _experts(rng, e, 2 * f, dim, "int8")
+    w2, (q2, s2) = _experts(rng, e, dim, f, "int8")
+    x, xt = bf16(rng.normal(0, 1, (tokens, dim)))
+    logits, lt = f32(rng.normal(0, 1.5, (tokens, e)))
+
+    def behind(s):
+        t = torch.full((s.numel() + 2,), float("nan"), dtype=s.dtype, device="cuda")
+        t[1:-1] = s.flatten()
+        return t[1:-1].view(s.shape)
+    y = empty(tokens, dim)
+    wq.wq_moe_ffn_run(wq.wq_moe_ffn_prepare(xt, q13, behind(s13), q2, behind(s2), y, logits=lt))
+    want, sel, gates = block.moe_ffn(x, logits, w13, w2, 2)
+    within(f64(y), want, _moe_allowed(x, w13, w2, sel, gates, want, 3, "f32"), "y")
+
+
 @pytest.mark.parametrize("tokens", [1, 3, 20])
 def test_int8_experts_of_odd_sixteens(wq, tokens):
     _moe(wq, np.random.default_rng(tokens), tokens, 5, 2, 48, 272, "int8", "router", "f32")

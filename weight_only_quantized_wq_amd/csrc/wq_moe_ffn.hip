@@ -679,9 +679,11 @@ static int moe_check(const char* name, const wq_moe_ffn& a) {
     return fail(WQ_ERR_SHAPE, "%s: y_stride = %lld must hold a row", name, (long long)a.y_stride);
   if (!aligned16(a.x) || !aligned16(a.w13) || !aligned16(a.w2) || !aligned16(a.router))
     return fail(WQ_ERR_ALIGN, "%s: x, w13, w2 and router must be 16-byte aligned", name);
-  if (((uintptr_t)a.s13 & 3) || ((uintptr_t)a.s2 & 3) || ((uintptr_t)a.logits & 3) || ((uintptr_t)a.y_f32 & 3) ||
+  // int8 scales are read one by one, MXFP4 ones in words
+  const uintptr_t part = a.format == WQ_FORMAT_INT8 ? 1 : 3;
+  if (((uintptr_t)a.s13 & part) || ((uintptr_t)a.s2 & part) || ((uintptr_t)a.logits & 3) || ((uintptr_t)a.y_f32 & 3) ||
       ((uintptr_t)a.y_bf16 & 1) || ((uintptr_t)a.sel & 3) || ((uintptr_t)a.gates & 3))
-    return fail(WQ_ERR_ALIGN, "%s: s13 and s2 must be 4-byte aligned, logits, y, sel and gates to their elements", name);
+    return fail(WQ_ERR_ALIGN, "%s: s13 and s2 must be %d-byte aligned, logits, y, sel and gates to their elements", name, (int)part + 1);
   return WQ_OK;
 }
 
