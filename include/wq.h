@@ -705,7 +705,9 @@ int wq_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int64_t n, int64
  *   x     bf16 [m][x_stride], or in MXFP4 xq [m][k/2] with x_scale [m][k/32]
  *         (exactly one of x and xq)
  *   y     fp32 and / or bf16 [m][y_stride], either may be NULL but not both
- * Sums are fp32.  A weight is its value as wq_dequantize_mxfp4 gives it.
+ * Sums are fp32.  A weight is its value as wq_dequantize_mxfp4 gives it, but
+ * meets an MXFP4 xq as it is: weights past the largest finite bf16 (scale bytes
+ * of 253 and 254) are infinite beside a bf16 x only.
  * 0 <= m <= 2^20, 0 <= n <= 2^24, k a multiple of 32, 32 .. 2^18; x, xq, q
  * 16-byte aligned, x_stride a multiple of 8 up to 2^22; scale and x_scale 4-byte
  * aligned (their last 4-byte word is read whole); y overlaps nothing

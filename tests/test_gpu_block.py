@@ -854,6 +854,32 @@ def test_products_of_scales_far_apart(wq, m, n, k, xkind):
 
 
 @pytest.mark.parametrize("xkind", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("m,n,k", [(3, 70, 96), (16, 40, 544), (40, 140, 1056), (2050, 5500, 96), (300, 700, 1056)])
+def test_weights_at_and_past_the_largest_finite_value(wq, m, n, k, xkind):
+    """A group of scale byte 252, 253 or 254 in a row of W: past 2^128 a weight is infinite where x is bf16, and its own
+    value where x is MXFP4, whose products are finite here."""
+    rng = np.random.default_rng(m + n)
+    q, s = mx(rng, n, k)
+    for byte, first in ((252, 0), (253, 1), (254, 2)):
+        s[first::4, byte % s.shape[1]] = byte
+    w = block.mx_values(q, s)
+    if xkind == "bf16":
+        x, xt = bf16(rng.choice([-1.0, 1.0], (m, k)) * rng.uniform(1, 2, (m, k)) * 2.0 ** -30)
+        xs = None
+        lost = (np.abs(w) >= 2.0 ** 128).any(1)
+        assert lost.any() and not lost[0::4].any()
+    else:
+        xq, xsc = mx(rng, m, k)
+        xsc -= 30
+        x, xt, xs, lost = block.mx_values(xq, xsc), up(xq), up(xsc), np.zeros(n, bool)
+    y = empty(m, n)
+    wq.wq_gemm_mxfp4_run(wq.wq_gemm_mxfp4_prepare(xt, up(q), up(s), y, x_scale=xs))
+    got, size = f64(y), np.abs(x) @ np.abs(w).T
+    assert not np.isfinite(got[:, lost]).any()
+    within(got[:, ~lost], (x @ w.T)[:, ~lost], (k + 16) * 2.0 ** -23 * size[:, ~lost], "weights to the end of the range")
+
+
+@pytest.mark.parametrize("xkind", ["bf16", "mxfp4"])
 @pytest.mark.parametrize("m,n,k,stride", [(1 << 20, 40, 32, 32), (3, 1 << 24, 32, 32), (20, 70, 1 << 18, 1 << 18), (2, 70, 1 << 18, 1 << 18),
                                           (300, 80, 96, 1 << 22), (9, 80, 96, 1 << 22), (1 << 20, 300, 64, 64)])
 def test_products_at_the_documented_limits(wq, m, n, k, stride, xkind):
