@@ -353,7 +353,7 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_up_kernel(MoeArgs
         left = 16;
       },
       [&](int col) { return reinterpret_cast<const char*>(a.x + list[min(col, cols - 1)] * a.x_stride); }, 2u * a.dim, nullptr, 0,
-      0, 1, acc);
+      acc);
   __syncthreads();
   for_tiles<kUpTiles>(2 * pairs, [&](auto at) __attribute__((always_inline)) {
     *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * 1024 + s.lane * 16) = acc[at.value][0];
@@ -431,7 +431,7 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_down_kernel(MoeAr
         const int part = min(col / chunk, kParts - 1), tok = min(col % chunk, have - 1);
         return reinterpret_cast<const char*>(act + (int64_t)(tok * kParts + part) * a.f);
       },
-      2u * a.f, nullptr, 0, 0, 1, acc);
+      2u * a.f, nullptr, 0, acc);
   __syncthreads();
   for_tiles<kUpTiles>(tiles, [&](auto at) __attribute__((always_inline)) {
 #pragma unroll
@@ -671,7 +671,6 @@ static int moe_check(const char* name, const wq_moe_ffn& a) {
                 name, (long long)a.tokens, (long long)a.dim, (long long)a.f, (long long)a.e, a.top);
   if (a.format == WQ_FORMAT_MXFP4 && (a.dim % kMxGroup || a.f % kMxGroup))
     return fail(WQ_ERR_SHAPE, "%s: dim = %lld, f = %lld must be multiples of 32 for MXFP4", name, (long long)a.dim, (long long)a.f);
-  if (a.router && a.dim % 8) return fail(WQ_ERR_SHAPE, "%s: dim must be a multiple of 8", name);
   const int64_t most = (int64_t)1 << 40;
   if (a.x_stride < a.dim || a.x_stride > most || a.x_stride % 8)
     return fail(WQ_ERR_SHAPE, "%s: x_stride = %lld must be a multiple of 8 and hold a row", name, (long long)a.x_stride);

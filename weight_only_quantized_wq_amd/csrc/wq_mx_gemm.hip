@@ -45,20 +45,18 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxRowsArgs a) {
   const int wave = wave_id(), ways = a.ways, kw = wave % ways, tw = wave / ways, teams = WAVES / ways;
   const S s(lds + wave * S::kBytes);
   const int first = (int)blockIdx.x * a.per, mine = min(a.per, a.tiles - first);
-  const int64_t m0 = (int64_t)blockIdx.y * COLS;
-  const int cols = (int)min((int64_t)COLS, a.m - m0);
+  const int cols = (int)a.m;                       // at most COLS
   f32x4 acc[kRowTiles][1];
 #pragma unroll
   for (int t = 0; t < kRowTiles; ++t) acc[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int tiles = (mine - tw + teams - 1) / teams;
-  const char* x = a.x + m0 * a.x_stride;
   s.template run<kRowTiles>(
       a.w, tiles, kw, ways, a.spans, (int)a.w.srow,
       [&](int t, int64_t& row0, int& left) {
         row0 = (int64_t)(first + tw + t * teams) * 16;
         left = (int)min((int64_t)16, a.w.rows - row0);
       },
-      [&](int col) { return x + min(col, cols - 1) * a.x_stride; }, a.x_bytes, a.xscale, a.m, m0, cols, acc, (int)blockIdx.x);
+      [&](int col) { return a.x + min(col, cols - 1) * a.x_stride; }, a.x_bytes, a.xscale, cols, acc, (int)blockIdx.x);
   // the waves' sums of a tile, lane by lane
   __syncthreads();
   for_tiles<kRowTiles>(tiles, [&](auto at) __attribute__((always_inline)) {
@@ -72,7 +70,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxRowsArgs a) {
     for (int w = 0; w < ways; ++w) v += *reinterpret_cast<const float*>(from + w * kRowTiles * 1024);
     const int64_t r = (int64_t)(first + tile) * 16 + row;
     if (r >= a.w.rows) continue;
-    const int64_t at = (m0 + col) * a.y_stride + r;
+    const int64_t at = col * a.y_stride + r;
     if (a.y32) gmem(a.y32)[at] = v;
     if (a.y16) gmem(a.y16)[at] = f32_to_bf16(v);
   }
@@ -86,15 +84,14 @@ constexpr int64_t kGemmMaxM = 1 << 20, kGemmMaxN = 1 << 24, kGemmMaxK = 1 << 18;
 
 // Tiles per workgroup and waves per tile: the fewest units in the longest chain, with
 // two units' worth for what a workgroup costs besides.
-static void rows_plan(MxRowsArgs& a, int waves, int most, int64_t chunks) {
+static void rows_plan(MxRowsArgs& a, int waves, int most) {
   double best = 1e300;
   for (int ways = 1; ways <= waves; ++ways) {
     if (waves % ways) continue;
     const int teams = waves / ways;
     for (int t = 1; t <= most; ++t) {
       const int per = t * teams;
-      const int64_t groups = (int64_t)((a.tiles + per - 1) / per) * chunks;
-      const int64_t rounds = (groups + 255) / 256;
+      const int groups = (a.tiles + per - 1) / per, rounds = (groups + 255) / 256;
       const double cost = (double)rounds * ((double)t * ((a.spans + ways - 1) / ways) + 2.0);
       if (cost < best) {
         best = cost;
@@ -107,9 +104,8 @@ static void rows_plan(MxRowsArgs& a, int waves, int most, int64_t chunks) {
 
 template <bool XQ, int COLS, int WAVES, int P>
 static int rows_launch(const char* name, MxRowsArgs a, hipStream_t s) {
-  const int64_t chunks = (a.m + COLS - 1) / COLS;
-  rows_plan(a, WAVES, row_tiles(XQ), chunks);
-  const dim3 grid((unsigned)((a.tiles + a.per - 1) / a.per), (unsigned)chunks);
+  rows_plan(a, WAVES, row_tiles(XQ));
+  const dim3 grid((unsigned)((a.tiles + a.per - 1) / a.per));
   if (a.w.srow % 4)
     hipLaunchKernelGGL((mx_rows_kernel<XQ, true, COLS, WAVES, P>), grid, dim3(WAVES * 64), 0, s, a);
   else

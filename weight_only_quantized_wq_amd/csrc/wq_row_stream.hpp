@@ -228,7 +228,7 @@ struct RowStream {
   // tile's rows; the loop waits for a unit by the number of requests made after it.
   template <int RT, class Tile, class Row>
   __device__ __forceinline__ void run(const StreamWeights& a, int tiles, int first, int step, int spans, int pieces, Tile tile,
-                                      Row row, uint32_t x_bytes, const uint8_t* xscale, int64_t xrows, int64_t xrow0, int xleft,
+                                      Row row, uint32_t x_bytes, const uint8_t* xscale, int xrows,
                                       f32x4 (&acc)[RT][kSets], int turn = 0) const {
     const int mine = first < spans ? (spans - first + step - 1) / step : 0;
     const int total = mine * tiles;
@@ -256,7 +256,7 @@ struct RowStream {
     };
     auto request_span = [&](int span) {
       request_x(row, x_bytes, span);
-      if constexpr (XQ) request_scales(xscale, a.srow, xrows, xrow0, xleft, span, lds_offset(lds + kXBytes));
+      if constexpr (XQ) request_scales(xscale, a.srow, xrows, 0, xrows, span, lds_offset(lds + kXBytes));
     };
     request_span(span_at(0));
 #pragma unroll
@@ -274,7 +274,7 @@ struct RowStream {
         if constexpr (t == 0) {
           wait_later<P - 1>(min(made - u - 1, made - before));
           read_x(x, span, pieces);
-          if constexpr (XQ) xs = scales(lds + kXBytes, ODD ? (uint32_t)((xrow0 + min(c, xleft - 1)) * a.srow) & 3u : 0u, span, pieces);
+          if constexpr (XQ) xs = scales(lds + kXBytes, ODD ? (uint32_t)min(c, xrows - 1) * a.srow & 3u : 0u, span, pieces);
         } else if (t < P && si + 1 < mine && made - u == P) {
           wait_requests<(P - 1) * kOps + kXOps>();    // the next span's activations come after this unit
         } else {
