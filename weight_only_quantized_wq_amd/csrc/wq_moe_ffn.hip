@@ -254,17 +254,6 @@ __device__ __forceinline__ void find_tokens(const MoeArgs& a, MoeTokens& all) {
   __syncthreads();
 }
 
-// Sum over the lower lanes (and the lane's own) of v.
-__device__ __forceinline__ int wave_prefix(int v) {
-  const int lane = lane_id();
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-
 // Item `item` of the experts in use, `chunk` tokens an item: its expert, the first of
 // its tokens among the expert's, and the expert's first row of `act`; false past the
 // last item.
@@ -278,7 +267,7 @@ __device__ __forceinline__ bool find_item(const MoeTokens& all, int item, int ch
     items += (c + chunk - 1) / chunk;
     rows += c;
   }
-  const int before = wave_prefix(items) - items, row0 = wave_prefix(rows) - rows;
+  const int before = wave_scan(items) - items, row0 = wave_scan(rows) - rows;
   const uint64_t at = __ballot(item >= before && item < before + items);
   if (!at) return false;
   const int l = __ffsll((unsigned long long)at) - 1;
@@ -490,13 +479,14 @@ struct MoeDown {
   int32_t used;
 };
 
-template <bool MX, bool ODD, int COLS, int WAVES, int P, int TM>
+// TOKENS: of the call, so that an expert has no more.
+template <bool MX, bool ODD, int TOKENS, int WAVES, int P>
 __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
-  using S = RowStream<MX, false, ODD, COLS, P>;
+  using S = RowStream<MX, false, ODD, TOKENS * kParts, P>;
   // a unit is a span of W2's rows and of the activations that meet it; both have P slots
   constexpr int kWave0 = S::kXBytes * (P - 1) + S::kBytes;
   __shared__ __align__(1024) char lds[WAVES * kWave0];
-  __shared__ __align__(16) float sums[WAVES][TM * 16];
+  __shared__ __align__(16) float sums[WAVES][TOKENS * 16];
   __shared__ MoeTokens all;
   __shared__ MoeDown down;
   find_tokens<WAVES>(a, all);
@@ -510,7 +500,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
       used += c > 0;
       rows += c;
     }
-    int at = wave_prefix(used) - used, row = wave_prefix(rows) - rows;
+    int at = wave_scan(used) - used, row = wave_scan(rows) - rows;
     for (int i = 0; i < N; ++i) {
       const int c = __popcll(all.mask[lane * N + i]);
       if (c) {
@@ -521,59 +511,43 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
     }
     if (lane == 63) down.used = at;
   }
-  for (int i = lane; i < TM * 16; i += 64) sums[wave][i] = 0.f;
+  for (int i = lane; i < TOKENS * 16; i += 64) sums[wave][i] = 0.f;
   __syncthreads();
-  constexpr int chunk = COLS / kParts;
-  const int used = down.used;
   const int64_t tile = (int64_t)blockIdx.x * 16;
   char* const base = lds + wave * kWave0;
   const int g = lane >> 4, c = lane & 15;
 
-  // this wave's units: (expert in use, span) pairs wave, wave + WAVES, ..., each over
-  // the chunks of the expert's tokens
-  struct Cursor {
-    int pair, chunk;
-  };
-  const int pairs = used * a.spans2;
-  auto tokens_of = [&](int pair) { return __builtin_amdgcn_readfirstlane(__popcll(all.mask[down.expert[pair / a.spans2]])); };
-  auto next = [&](Cursor& q) {
-    if ((q.chunk + 1) * chunk < tokens_of(q.pair)) {
-      ++q.chunk;
-    } else {
-      q.chunk = 0;
-      q.pair += WAVES;
-    }
-  };
-  // slots of weights lie behind those of activations
-  auto request = [&](const Cursor& q, int slot) {
-    const int u = q.pair / a.spans2, span = q.pair % a.spans2;
+  // this wave's units: (expert in use, span) pairs wave, wave + WAVES, ...; slots of
+  // weights lie behind those of activations
+  const int pairs = down.used * a.spans2;
+  auto request = [&](int pair, int slot) {
+    const int u = pair / a.spans2, span = pair % a.spans2;
     const int expert = __builtin_amdgcn_readfirstlane(down.expert[u]), row = __builtin_amdgcn_readfirstlane(down.slot[u]);
-    const int have = min(chunk, tokens_of(q.pair) - q.chunk * chunk);
-    const uint16_t* act = a.act + (int64_t)(row + q.chunk * chunk) * kParts * a.f;
-    // columns: part after part, `chunk` tokens each
+    const int have = TOKENS == 1 ? 1 : __builtin_amdgcn_readfirstlane(__popcll(all.mask[expert]));
+    const uint16_t* act = a.act + (int64_t)row * kParts * a.f;
+    // columns: part after part, TOKENS each
     const S x(base + slot * S::kXBytes);
     x.request_x(
         [&](int col) {
-          const int part = min(col / chunk, kParts - 1), tok = min(col % chunk, have - 1);
+          const int part = min(col / TOKENS, kParts - 1), tok = min(col % TOKENS, have - 1);
           return reinterpret_cast<const char*>(act + (int64_t)(tok * kParts + part) * a.f);
         },
         2u * a.f, span);
     const S w(base + (P - 1) * S::kXBytes);
     w.request_unit(a.w2, (int64_t)expert * a.dim + tile, 16, span, slot);
   };
-  Cursor ask{wave, 0}, now{wave, 0};
-  int made = 0, done = 0;
+  int made = 0;
 #pragma unroll
   for (int p = 0; p < P; ++p)
-    if (ask.pair < pairs) {
-      request(ask, made++ % P);
-      next(ask);
+    if (wave + made * WAVES < pairs) {
+      request(wave + made * WAVES, p);
+      ++made;
     }
   f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
   constexpr int kOps = S::kOps + S::kXOps;
   const int pieces = (int)(a.w2.row_bytes / 16);
-  while (now.pair < pairs) {
-    const int u = now.pair / a.spans2, span = now.pair % a.spans2;
+  for (int done = 0, pair = wave; pair < pairs; ++done, pair += WAVES) {
+    const int u = pair / a.spans2, span = pair % a.spans2;
     const int expert = __builtin_amdgcn_readfirstlane(down.expert[u]);
     const int slot = done % P;
     if (made - done == P)
@@ -584,28 +558,22 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
     S(base + slot * S::kXBytes).read_x(x, span, pieces);
     const auto unit = S(base + (P - 1) * S::kXBytes).read_unit(a.w2, (int64_t)expert * a.dim + tile, 16, span, pieces, slot);
     wait_lds();
-    if (ask.pair < pairs) {
-      request(ask, slot);
+    if (wave + made * WAVES < pairs) {
+      request(wave + made * WAVES, slot);
       ++made;
-      next(ask);
     }
     S::multiply(unit, x, 0u, acc);
-    ++done;
-    Cursor after = now;
-    next(after);
-    if (after.pair >= pairs || after.chunk != now.chunk || after.pair / a.spans2 != u) {
+    if (pair + WAVES >= pairs || (pair + WAVES) / a.spans2 != u) {
       // columns of a token's parts meet, then go to its row of this wave's sums
       f32x4 v = acc[0];
 #pragma unroll
       for (int q = 1; q < kParts; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += __shfl(acc[0][i], lane + q * chunk);
-      const uint64_t mask = all.mask[expert];
-      const int begin = now.chunk * chunk, have = min(chunk, __popcll(mask) - begin);
-      if (c < have) {
-        // the (begin + c)-th token of the mask
-        uint64_t m = mask;
-        for (int i = 0; i < begin + c; ++i) m &= m - 1;
+        for (int i = 0; i < 4; ++i) v[i] += __shfl(acc[0][i], lane + q * TOKENS);
+      uint64_t m = all.mask[expert];
+      if (c < __popcll(m)) {
+        // the c-th token of the mask
+        for (int i = 0; i < c; ++i) m &= m - 1;
         const int t = __ffsll((unsigned long long)m) - 1;
         float gate = 0.f;
         for (int j = 0; j < a.top; ++j)
@@ -619,7 +587,6 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
       }
       acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    now = after;
   }
   __syncthreads();
   for (int o = (int)threadIdx.x; o < a.tokens * 16; o += WAVES * 64) {
@@ -761,9 +728,9 @@ template <bool MX, int TOKENS, int WAVES>
 static void few_launch(const MoeArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.dim / 16)), block(WAVES * 64);
   if (MX && a.w2.srow % 4)
-    hipLaunchKernelGGL((moe_few_kernel<MX, MX, TOKENS * kParts, WAVES, 2, TOKENS>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((moe_few_kernel<MX, MX, TOKENS, WAVES, 2>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((moe_few_kernel<MX, false, TOKENS * kParts, WAVES, 2, TOKENS>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((moe_few_kernel<MX, false, TOKENS, WAVES, 2>), grid, block, 0, s, a);
 }
 
 template <bool MX>
