@@ -20,6 +20,8 @@
 // us (scores 5.7, selection 4.8, up 45, down 38, join 4.7): many starts of short streams.
 #include <stdint.h>
 
+#include <math.h>
+
 #include <algorithm>
 
 #include "wq_host.hpp"
@@ -330,9 +332,9 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_up_kernel(MoeArgs
   const S s(lds + wave * S::kBytes);
   const int first = (int)blockIdx.x % a.blocks * a.per, mine = min(a.per, a.pairs - first);
   const int pairs = (mine - tw + teams - 1) / teams;
-  f32x4 acc[kUpTiles][1];
+  f32x4 acc[kUpTiles];
 #pragma unroll
-  for (int t = 0; t < kUpTiles; ++t) acc[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < kUpTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int64_t rows0 = (int64_t)expert * 2 * a.f;
   // a tile of W1, then the same rows of W3
   s.template run<kUpTiles>(
@@ -345,7 +347,7 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_up_kernel(MoeArgs
       acc);
   __syncthreads();
   for_tiles<kUpTiles>(2 * pairs, [&](auto at) __attribute__((always_inline)) {
-    *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * 1024 + s.lane * 16) = acc[at.value][0];
+    *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * 1024 + s.lane * 16) = acc[at.value];
   });
   __syncthreads();
   for (int o = (int)threadIdx.x; o < mine * 16 * cols; o += WAVES * 64) {
@@ -376,7 +378,7 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_up_kernel(MoeArgs
 template <bool MX, bool ODD, int COLS, int WAVES, int P, bool TWO>
 __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_down_kernel(MoeArgs a) {
   using S = RowStream<MX, false, ODD, COLS, P>;
-  constexpr int kTile = S::kSets * 1024, kRed = WAVES * kUpTiles * kTile, kAll = WAVES * S::kBytes;
+  constexpr int kRed = WAVES * kUpTiles * 1024, kAll = WAVES * S::kBytes;
   __shared__ __align__(1024) char lds[kAll > kRed ? kAll : kRed];
   MoeTokens& all = *reinterpret_cast<MoeTokens*>(lds);
   static_assert(sizeof(MoeTokens) <= sizeof(lds));
@@ -402,11 +404,9 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_down_kernel(MoeAr
   const S s(lds + wave * S::kBytes);
   const int first = (int)blockIdx.x % a.blocks * a.per, mine = min(a.per, a.dim / 16 - first);
   const int tiles = (mine - tw + teams - 1) / teams;
-  f32x4 acc[kUpTiles][S::kSets];
+  f32x4 acc[kUpTiles];
 #pragma unroll
-  for (int t = 0; t < kUpTiles; ++t)
-#pragma unroll
-    for (int q = 0; q < S::kSets; ++q) acc[t][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < kUpTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int64_t rows0 = (int64_t)expert * a.dim;
   const uint16_t* act = a.act + (int64_t)(slot + begin) * kParts * a.f;
   s.template run<kUpTiles>(
@@ -423,21 +423,16 @@ __global__ __launch_bounds__(WAVES * 64, TWO ? 2 : 1) void moe_down_kernel(MoeAr
       2u * a.f, nullptr, 0, acc);
   __syncthreads();
   for_tiles<kUpTiles>(tiles, [&](auto at) __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = 0; q < S::kSets; ++q)
-      *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * kTile + q * 1024 + s.lane * 16) = acc[at.value][q];
+    *reinterpret_cast<f32x4*>(lds + (wave * kUpTiles + at.value) * 1024 + s.lane * 16) = acc[at.value];
   });
   __syncthreads();
   for (int o = (int)threadIdx.x; o < mine * 16 * have; o += WAVES * 64) {
     const int row = o & 15, tok = (o >> 4) % have, tile = (o >> 4) / have;
-    const char* from = lds + ((tile % teams) * ways * kUpTiles + tile / teams) * kTile + (row >> 2) * 256 + (row & 3) * 4;
+    const char* from = lds + ((tile % teams) * ways * kUpTiles + tile / teams) * 1024 + ((row >> 2) * 16 + tok) * 16 + (row & 3) * 4;
     float v = 0.f;
 #pragma unroll
-    for (int q = kParts - 1; q >= 0; --q) {
-      const int col = q * chunk + tok;
-      for (int w = 0; w < ways; ++w)
-        v += *reinterpret_cast<const float*>(from + w * kUpTiles * kTile + (col >> 4) * 1024 + (col & 15) * 16);
-    }
+    for (int q = kParts - 1; q >= 0; --q)
+      for (int w = 0; w < ways; ++w) v += *reinterpret_cast<const float*>(from + w * kUpTiles * 1024 + q * chunk * 16);
     const int r = (first + tile) * 16 + row;
     if constexpr (!MX) v *= __uint_as_float((uint32_t)gmem(a.s2)[rows0 + r] << 16);
     gmem(a.sums)[(int64_t)pick[tok] * a.dim + r] = gate[tok] * v;
@@ -543,7 +538,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
       request(wave + made * WAVES, p);
       ++made;
     }
-  f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
   constexpr int kOps = S::kOps + S::kXOps;
   const int pieces = (int)(a.w2.row_bytes / 16);
   for (int done = 0, pair = wave; pair < pairs; ++done, pair += WAVES) {
@@ -554,7 +549,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
       wait_requests<(P - 1) * kOps>();
     else
       wait_requests<0>();
-    u32x4 x[1][S::kFrags];
+    u32x4 x[S::kFrags];
     S(base + slot * S::kXBytes).read_x(x, span, pieces);
     const auto unit = S(base + (P - 1) * S::kXBytes).read_unit(a.w2, (int64_t)expert * a.dim + tile, 16, span, pieces, slot);
     wait_lds();
@@ -562,14 +557,14 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
       request(wave + made * WAVES, slot);
       ++made;
     }
-    S::multiply(unit, x, 0u, acc);
+    acc = S::multiply(unit, x, 0u, acc);
     if (pair + WAVES >= pairs || (pair + WAVES) / a.spans2 != u) {
       // columns of a token's parts meet, then go to its row of this wave's sums
-      f32x4 v = acc[0];
+      f32x4 v = acc;
 #pragma unroll
       for (int q = 1; q < kParts; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += __shfl(acc[0][i], lane + q * TOKENS);
+        for (int i = 0; i < 4; ++i) v[i] += __shfl(acc[i], lane + q * TOKENS);
       uint64_t m = all.mask[expert];
       if (c < __popcll(m)) {
         // the c-th token of the mask
@@ -585,7 +580,7 @@ __global__ __launch_bounds__(WAVES * 64) void moe_few_kernel(MoeArgs a) {
           sums[wave][t * 16 + 4 * g + i] += gate * o;
         }
       }
-      acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
+      acc = f32x4{0.f, 0.f, 0.f, 0.f};
     }
   }
   __syncthreads();
@@ -697,6 +692,21 @@ static void rows_plan(MoeArgs& a, int waves, int items, int tiles, int each, int
   }
 }
 
+// Items of `chunk` tokens over all experts, as expected where a token picks any of them
+// alike, and a tenth more: an item too many for one round of workgroups costs a second
+// (MXFP4 layers of 4 to 60 experts, 6 to 64 tokens: 1 % shorter in the mean than without the
+// tenth, 10 % instead of 20 behind the best plan at the worst).
+static int expected_items(int tokens, int top, int e, int chunk) {
+  if (top == e) return e * ((tokens + chunk - 1) / chunk);
+  const double odds = (double)top / (e - top);
+  double p = pow(1. - (double)top / e, tokens), items = 0.;   // p: that an expert has c tokens
+  for (int c = 1; c <= tokens; ++c) {
+    p *= odds * (tokens - c + 1) / c;
+    items += p * ((c + chunk - 1) / chunk);
+  }
+  return (int)ceil(1.1 * e * items);
+}
+
 template <bool MX, int COLS, int WAVES, int P, bool TWO = false>
 static void up_launch(MoeArgs a, hipStream_t s) {
   const int picks = a.tokens * a.top, used = std::min(a.e, picks);
@@ -713,10 +723,7 @@ template <bool MX, int COLS, int WAVES, int P, bool TWO = false>
 static void down_launch(MoeArgs a, hipStream_t s) {
   constexpr int chunk = COLS / kParts;
   const int picks = a.tokens * a.top, used = std::min(a.e, picks);
-  // items of `chunk` tokens, as expected where experts have about as many tokens each
-  // (planned for the experts alone, 16 tokens of Mixtral's eight in MXFP4 take 200 us, not 161)
-  const int items = std::max(used, (picks + used * (chunk - 1) / 2 + chunk - 1) / chunk);
-  rows_plan(a, WAVES, items, a.dim / 16, 1, a.spans2, TWO ? 512 : 256);
+  rows_plan(a, WAVES, std::max(used, expected_items(a.tokens, a.top, a.e, chunk)), a.dim / 16, 1, a.spans2, TWO ? 512 : 256);
   const dim3 grid((unsigned)((used + picks / chunk) * a.blocks));
   if (MX && a.w2.srow % 4)
     hipLaunchKernelGGL((moe_down_kernel<MX, MX, COLS, WAVES, P, TWO>), grid, dim3(WAVES * 64), 0, s, a);
@@ -758,17 +765,14 @@ static void experts_launch(MoeArgs a, hipStream_t s) {
     if (a.tokens == 2 && a.top <= 4) return few_launch<MX, 2, 7>(a, s);
   }
   // Columns are three for a token.  Two tokens at once leave room for eight waves of three
-  // slots (8 tokens of 128 experts 46 us, five at once 49).  Eight at once pay where a span's
-  // activations are few bytes and one pass over W2 does for nearly all experts: int8, 16
-  // tokens of Mixtral's 302 us, five at once 337; but 32 tokens 433 and 379, and in MXFP4 16
-  // tokens, seven at once, 251 and 200 (both planned for eight items).
-  constexpr int kMost = MX ? 15 : 24;
+  // slots (8 tokens of 128 experts 46 us, five at once 49).  (Seven or eight at once, as two
+  // products of the same weights, need 21 KB a wave for a span's activations in MXFP4:
+  // Mixtral, 24 tokens 218 to 307 us, five at once 206 to 211; in int8, where that is 12, the
+  // same within 1 % over 42 layers.)
   if (many)
     down_launch<MX, 9, 4, 2, true>(a, s);
   else if (mean <= 1)
     down_launch<MX, 6, 8, 3>(a, s);
-  else if (!MX && mean > 2 && mean < 8)
-    down_launch<MX, kMost, 4, 4>(a, s);
   else
     down_launch<MX, 15, 4, 4>(a, s);
   hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((a.tokens * (a.dim / 4) + 255) / 256)), dim3(256), 0, s, a);

@@ -46,9 +46,9 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxRowsArgs a) {
   const S s(lds + wave * S::kBytes);
   const int first = (int)blockIdx.x * a.per, mine = min(a.per, a.tiles - first);
   const int cols = (int)a.m;                       // at most COLS
-  f32x4 acc[kRowTiles][1];
+  f32x4 acc[kRowTiles];
 #pragma unroll
-  for (int t = 0; t < kRowTiles; ++t) acc[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < kRowTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int tiles = (mine - tw + teams - 1) / teams;
   s.template run<kRowTiles>(
       a.w, tiles, kw, ways, a.spans, (int)a.w.srow,
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_rows_kernel(MxRowsArgs a) {
   // the waves' sums of a tile, lane by lane
   __syncthreads();
   for_tiles<kRowTiles>(tiles, [&](auto at) __attribute__((always_inline)) {
-    *reinterpret_cast<f32x4*>(lds + (wave * kRowTiles + at.value) * 1024 + s.lane * 16) = acc[at.value][0];
+    *reinterpret_cast<f32x4*>(lds + (wave * kRowTiles + at.value) * 1024 + s.lane * 16) = acc[at.value];
   });
   __syncthreads();
   for (int o = (int)threadIdx.x; o < mine * 16 * cols; o += WAVES * 64) {

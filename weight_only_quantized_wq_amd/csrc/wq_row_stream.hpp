@@ -12,8 +12,7 @@
 //
 // Activations (up to COLS rows) of a span come by direct loads too, and stay in
 // registers while the units of the wave's row tiles go by: RT tiles share one read.
-// D: lane l holds rows 4 (l / 16) + r of column l % 16; columns past 16 are a second
-// product of the same weights.
+// D: lane l holds rows 4 (l / 16) + r of column l % 16.
 #pragma once
 
 #include <stdint.h>
@@ -60,8 +59,6 @@ struct RowStream {
   static constexpr int kSlot = 4096 + 256 * kWords;
   static constexpr int kBytes = kXBytes + 256 * kXWords + P * kSlot; // LDS of a wave
   static constexpr int kFrags = XQ ? 4 : kSpan / 32;                 // 16-byte pieces of activations per lane
-  static constexpr int kSets = (COLS + 15) / 16;                     // of 16 columns
-  static_assert(!XQ || kSets == 1, "one word of activation scales per lane");
 
   char* lds;
   int lane, g, c;
@@ -123,23 +120,18 @@ struct RowStream {
   }
 
   // The activations of a span in registers, zeros past the end (`pieces` in all).
-  __device__ __forceinline__ void read_x(u32x4 (&x)[kSets][kFrags], int span, int pieces) const {
+  __device__ __forceinline__ void read_x(u32x4 (&x)[kFrags], int span, int pieces) const {
     constexpr int per = kFrags / 4;                                   // of one weight piece
+    const int col = min(c, COLS - 1);
 #pragma unroll
-    for (int s = 0; s < kSets; ++s) {
-      const int col = min(16 * s + c, COLS - 1);
-#pragma unroll
-      for (int f = 0; f < kFrags; ++f) {
-        const int piece = (4 * g + f / per) * per + f % per;
-        x[s][f] = *reinterpret_cast<const u32x4*>(lds + col * kXRow + ((piece ^ (col & 15)) << 4));
-      }
+    for (int f = 0; f < kFrags; ++f) {
+      const int piece = (4 * g + f / per) * per + f % per;
+      x[f] = *reinterpret_cast<const u32x4*>(lds + col * kXRow + ((piece ^ col) << 4));
     }
     if ((span + 1) * 16 > pieces) {
 #pragma unroll
-      for (int s = 0; s < kSets; ++s)
-#pragma unroll
-        for (int f = 0; f < kFrags; ++f)
-          if (span * 16 + 4 * g + f / per >= pieces) x[s][f] = u32x4{0, 0, 0, 0};
+      for (int f = 0; f < kFrags; ++f)
+        if (span * 16 + 4 * g + f / per >= pieces) x[f] = u32x4{0, 0, 0, 0};
     }
   }
 
@@ -187,30 +179,29 @@ struct RowStream {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(u.w[J]), mx_operand(x[J]), acc, 4, 4, J, (int)u.s, J, (int)xs);
   }
 
-  __device__ __forceinline__ static void multiply(const Unit& u, const u32x4 (&x)[kSets][kFrags], uint32_t xs, f32x4 (&acc)[kSets]) {
+  __device__ __forceinline__ static f32x4 multiply(const Unit& u, const u32x4 (&x)[kFrags], uint32_t xs, f32x4 acc) {
     if constexpr (XQ) {
-      acc[0] = multiply4<0>(u, x[0], xs, acc[0]);
-      acc[0] = multiply4<1>(u, x[0], xs, acc[0]);
-      acc[0] = multiply4<2>(u, x[0], xs, acc[0]);
-      acc[0] = multiply4<3>(u, x[0], xs, acc[0]);
+      acc = multiply4<0>(u, x, xs, acc);
+      acc = multiply4<1>(u, x, xs, acc);
+      acc = multiply4<2>(u, x, xs, acc);
+      acc = multiply4<3>(u, x, xs, acc);
     } else {
-      constexpr int per = kFrags / 4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float f = MX ? mx_scale(u.s, j) : 0.f;
+        if constexpr (MX) {
+          const float s = mx_scale(u.s, j);
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
-          bf16x8 w;
-          if constexpr (MX)
-            w = mx_bf16(u.w[j][i], f);
-          else
-            w = i8_bf16(u.w[j][2 * i], u.w[j][2 * i + 1]);
+          for (int i = 0; i < 4; ++i)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_bf16(u.w[j][i], s), __builtin_bit_cast(bf16x8, x[4 * j + i]), acc, 0, 0, 0);
+        } else {
 #pragma unroll
-          for (int s = 0; s < kSets; ++s)
-            acc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, x[s][per * j + i]), acc[s], 0, 0, 0);
+          for (int i = 0; i < 2; ++i)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(i8_bf16(u.w[j][2 * i], u.w[j][2 * i + 1]),
+                                                          __builtin_bit_cast(bf16x8, x[2 * j + i]), acc, 0, 0, 0);
         }
       }
     }
+    return acc;
   }
 
   template <int K>
@@ -229,7 +220,7 @@ struct RowStream {
   template <int RT, class Tile, class Row>
   __device__ __forceinline__ void run(const StreamWeights& a, int tiles, int first, int step, int spans, int pieces, Tile tile,
                                       Row row, uint32_t x_bytes, const uint8_t* xscale, int xrows,
-                                      f32x4 (&acc)[RT][kSets], int turn = 0) const {
+                                      f32x4 (&acc)[RT], int turn = 0) const {
     const int mine = first < spans ? (spans - first + step - 1) / step : 0;
     const int total = mine * tiles;
     if (total == 0) return;
@@ -264,7 +255,7 @@ struct RowStream {
     int u = 0, before = 0;                       // units requested before the span's activations
     for (int si = 0; si < mine; ++si) {
       const int span = span_at(si);
-      u32x4 x[kSets][kFrags];
+      u32x4 x[kFrags];
       uint32_t xs = 0;
       for_tiles<RT>(tiles, [&](auto at) __attribute__((always_inline)) {
         constexpr int t = decltype(at)::value;
@@ -287,7 +278,7 @@ struct RowStream {
           request_span(span_at(si + 1));
         }
         request();
-        multiply(unit, x, xs, acc[t]);
+        acc[t] = multiply(unit, x, xs, acc[t]);
         ++u;
       });
     }
