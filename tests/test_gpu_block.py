@@ -375,6 +375,55 @@ def test_nan_logits_select_distinct_experts_in_range(wq, tokens):
     assert got[0] == [0, 1, 2] and got[1] == [1, 2, 0]
 
 
+@pytest.mark.parametrize("weights", ["mxfp4", "int8"])
+@pytest.mark.parametrize("tokens,e,top", [(64, 64, 4), (37, 8, 2), (64, 2, 1), (23, 100, 3), (64, 16, 16), (6, 8, 1)])
+def test_all_tokens_at_the_same_experts(wq, tokens, e, top, weights):
+    """Routing as uneven as it gets, and every expert at once, where plans expect them alike."""
+    logits = np.tile(np.random.default_rng(e).normal(0, 1.5, (1, e)), (tokens, 1))
+    _moe(wq, np.random.default_rng(tokens + e), tokens, e, top, 64, 96, weights, "logits", "both", logits=logits)
+
+
+def test_layers_in_turn_captured_over_one_workspace(wq):
+    """Two layers of other sizes through one workspace, in a graph each, replayed in turn and after eager calls."""
+    import torch
+    rng = np.random.default_rng(21)
+    sizes = [(30, 8, 2, 96, 256), (2, 16, 4, 160, 64), (1, 4, 2, 64, 352)]
+    ws = torch.empty(max(wq.wq_moe_ffn_workspace_bytes(t, dim, f, e, top) for t, e, top, dim, f in sizes), dtype=torch.uint8,
+                     device="cuda")
+    plans, graphs, outs, wants = [], [], [], []
+    for t, e, top, dim, f in sizes:
+        w13, t13 = _experts(rng, e, 2 * f, dim, "mxfp4")
+        w2, t2 = _experts(rng, e, dim, f, "mxfp4")
+        x, xt = bf16(rng.normal(0, 1, (t, dim)))
+        r, rt = bf16(rng.normal(0, dim ** -0.5, (e, dim)))
+        y = empty(t, dim)
+        plans.append(wq.wq_moe_ffn_prepare(xt, *t13, *t2, y, router=rt, top=top, workspace=ws))
+        want, sel, gates = block.moe_ffn(x, x @ r.T, w13, w2, top)
+        outs.append(y)
+        wants.append((want, _moe_allowed(x, w13, w2, sel, gates, want, 3, "f32")))
+    for p in plans:
+        wq.wq_moe_ffn_run(p)
+    torch.cuda.synchronize()
+    for p in plans:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            wq.wq_moe_ffn_run(p)
+    for _ in range(3):
+        for y in outs:
+            y.fill_(7)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for y, (want, allowed) in zip(outs, wants):
+            within(f64(y), want, allowed, "replay")
+        for y, p in zip(outs, plans):
+            y.fill_(9)
+            wq.wq_moe_ffn_run(p)
+        torch.cuda.synchronize()
+        for y, (want, allowed) in zip(outs, wants):
+            within(f64(y), want, allowed, "call")
+
+
 def test_large_activations_between_the_products_keep_their_values(wq):
     """silu(h1) h3 next to the largest fp32, which no bf16 rounded to nearest reaches."""
     import torch
@@ -462,6 +511,26 @@ def test_block_norm_in_place_without_f_and_without_norm(wq, h):
     _block(wq, rng, 9, 264, h=h, f=None, out=False)
     _block(wq, rng, 9, 288, h=h, u="", norm=False)
     _block(wq, rng, 9, 288, h=h, u="mxfp4", out=False, norm=False, f=None)
+
+
+@pytest.mark.parametrize("q", [False, True])
+@pytest.mark.parametrize("h,out", [("f32", "bf16"), ("bf16", "f32")])
+def test_block_norm_of_one_type_into_the_other(wq, h, out, q):
+    import torch
+    rng = np.random.default_rng(17)
+    make = {"f32": f32, "bf16": bf16}
+    hv, ht = make[h](rng.normal(0, 3, (5, 288)))
+    fv, ft = make[out](rng.normal(0, 1, (5, 288)))
+    got = empty(5, 288, dtype={"f32": "float32", "bf16": "bfloat16"}[out])
+    codes, scale = (empty(5, 144, dtype="uint8"), empty(5, 9, dtype="uint8")) if q else (None, None)
+    wq.wq_block_norm_run(wq.wq_block_norm_prepare(ht, h_out=got, f=ft, scale=0.5, q=codes, q_scale=scale))
+    want, u = block.block_norm(hv, fv, scale=0.5, eps=float(np.float32(1e-6)))
+    # a product by a power of two and a sum, in fp32 or fp64, then the result's rounding
+    within(f64(got), want, 2.0 ** -23 * np.abs(want) + (BF16 if out == "bf16" else 0) * np.abs(want) * (1 + 2.0 ** -23), out)
+    if q:
+        want_q, want_s = block.mx_quantize(u)
+        assert np.array_equal(scale.cpu().numpy(), want_s) and np.array_equal(codes.cpu().numpy(), want_q)
+    assert torch.equal(ht.double().cpu(), torch.from_numpy(hv))
 
 
 @pytest.mark.parametrize("size", [1e-30, 1e30])

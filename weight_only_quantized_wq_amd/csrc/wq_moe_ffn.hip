@@ -1,5 +1,7 @@
 // A whole mixture-of-experts layer for a few tokens: router, selected experts (SwiGLU)
-// and their weighted sum.  Bound by the bytes of the experts in use, each read once.
+// and their weighted sum.  Bound by the bytes of the experts in use: W1 and W3 are read once
+// for up to 4, 8 or 16 tokens of an expert (by the number of tokens), W2 for up to 2, 3 or 5,
+// and again for as many more.
 //
 //   scores   x router^T in fp64, every expert's sum in the same order, so that equal
 //            router rows score the same; where the caller gives logits, none
@@ -14,10 +16,10 @@
 // The second product takes silu(h1) h3 in three bf16 parts (24 bits, an fp32 value's), as
 // further columns of the matrix instruction.
 //
-// Measured (dim 4096, f 14336): one token of two int8 experts (352 MB) 76 us, 4.6 TB/s
-// (up 46, moe_few_kernel 26); 6 tokens of 8 experts in MXFP4 (616 MB) 141 us (scores 5.4,
-// up 67 to 80, down 55, join 4.7).  61 tokens of 128 experts (dim 2048, f 768, 316 MB) 97
-// us (scores 5.7, selection 4.8, up 45, down 38, join 4.7): many starts of short streams.
+// Measured (dim 4096, f 14336): one token of two int8 experts (352 MB) 73 us, 4.8 TB/s;
+// 6 tokens of 8 experts in MXFP4 (616 MB) 134 us, 64 tokens (749 MB) 300.  61 tokens of 128
+// experts (dim 2048, f 768, 316 MB) 99 us, five dependent launches and many starts of short
+// streams.
 #include <stdint.h>
 
 #include <math.h>
@@ -465,7 +467,7 @@ __global__ __launch_bounds__(256) void moe_join_kernel(MoeArgs a) {
 // One token, or two: a workgroup takes 16 rows of W2 of every expert in use, so that the
 // sum over experts stays inside it and nothing is joined; its waves take (expert, span)
 // pairs in turn, each with the activations that meet it.  (One token of Mixtral's int8
-// layer: 25.4 us, where moe_down_kernel and the join take 26.9 and 4.7.)
+// layer: 25.4 us, where moe_down_kernel and the join took 26.9 and 4.7.)
 
 // The experts in use, in order.
 struct MoeDown {
@@ -745,8 +747,9 @@ static void experts_launch(MoeArgs a, hipStream_t s) {
   const int mean = (a.tokens * a.top + a.e - 1) / a.e;      // tokens of an expert
   // Many experts of a few tokens each: two workgroups of four waves on a CU, whose starts
   // (the search for an expert's tokens, the first loads) and ends lie beside the other's
-  // streams.  61 tokens of 128 experts: 104 us, with one of eight waves 119; but 16 tokens
-  // of Mixtral's eight 182 and 166, its int8 layer for one token 79 and 75.
+  // streams.  61 tokens of 128 experts: 104 us, with one workgroup 116; but 16 tokens of
+  // Mixtral's eight 182 and 166, its int8 layer for one token 79 and 75, and 10 to 32 tokens
+  // of 16 to 60 experts the same in the mean (16 of 16 150 and 139, 16 of 32 115 and 117).
   const bool many = a.tokens > 8 && a.e >= 64 && mean <= 4;
   if (a.tokens <= 4)
     up_launch<MX, 4, 8, 3>(a, s);

@@ -12,12 +12,14 @@
 // Scale rows are multiples of 8 bytes here (windows of 256 inputs); others are padded
 // beforehand (mx_pad_kernel).
 //
-// Tiles of 256 x 256: per CU and clock the direct loads give about 50 bytes, which is what
-// bounds smaller ones.  bf16, 2000 rows x 28672 x 4096: 393 us, 1.19 PFLOP/s (a library's
-// bf16 product of this shape, with W in bf16, 332); with zeros for data the same kernel
-// runs a third faster, so what is left is the chip's power, and conversions, which are 5 %.
-// Both in 4 bits, 4096 rows x 10240 x 8192: 217 us, 3.2 PFLOP/s; without the matrix
-// instructions it takes 165, so it is bound by the loads.
+// bf16, 2000 rows x 28672 x 4096: 393 us, 1.19 PFLOP/s (a library's bf16 product of this
+// shape, with W in bf16, 332); with zeros for data the same kernel runs a third faster, so
+// what is left is the chip's power, and conversions, which are 5 %.
+// Both in 4 bits, 4096 rows x 10240 x 8192: 217 us, 3.2 PFLOP/s, half of what the matrix
+// pipe gives.  Without the matrix instructions it takes 165, though its loads are 14 bytes
+// per CU and clock only: with two buffers one stage is under way while one is multiplied,
+// and its latency is what bounds it (matrix pipe busy 33 % of the time, LDS 16 %), besides
+// 2.5 rounds of 256 tiles.  Stages of 128 inputs in four buffers are not built.
 #pragma once
 
 #include <stdint.h>
